@@ -58,15 +58,32 @@ EXPORTS = ["e3_num_paths", "e3_path_info", "e3_supported", "e3_cg_block",
            "e3_radial_hidden_size", "e3_radial_hidden", "e3_conv_forward_radial_hidden",
            "e3_radial_mlp_hidden", "e3_conv_backward_radial_scratch_size",
            "e3_conv_backward_radial_hidden",
+           "e3_layer_norm", "e3_layer_norm_workspace_size", "e3_layer_norm_backward",
+           "e3_param_check", "e3_grad_norm_workspace_size", "e3_grad_norm", "e3_adamw",
+           "e3_adamw_moments",
            "e3_release_all",
            "e3_last_error"]
 E3_GEN_FORWARD, E3_GEN_DX, E3_GEN_DW, E3_GEN_DY, E3_GEN_GEMM = 0, 1, 2, 3, 4
 E3_GEN_GEMM_DX, E3_GEN_GEMM_DW, E3_GEN_GEMM_DY = 5, 6, 7
+E3_NORM_UNCENTERED = 1
+E3_ADAMW_SKIP_NONFINITE = 1
 
 
 class _CRadial(C.Structure):
     _fields_ = [("cutoff", C.c_float), ("n_basis", C.c_int32), ("hidden", C.c_int32),
                 ("W1", C.c_void_p), ("W2", C.c_void_p)]
+
+
+class _Param(C.Structure):
+    _fields_ = [("n", C.c_int64), ("p", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p),
+                ("v", C.c_void_p), ("m_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("p_bf16", C.c_void_p), ("weight_decay", C.c_float), ("grad_dtype", C.c_int)]
+
+
+class _AdamwArgs(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
+                ("eps", C.c_double), ("step", C.c_int64), ("step_dev", C.c_void_p),
+                ("lr_dev", C.c_void_p), ("grad_scale", C.c_void_p), ("flags", C.c_int32)]
 
 
 def lib():
@@ -140,6 +157,16 @@ def lib():
     L.e3_conv_backward_noalloc.argtypes = [dp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                            C.c_int, vp]
     L.e3_check_graph_host.argtypes = [i32, i32, vp, vp]
+    L.e3_layer_norm.argtypes = [ip, i64, vp, vp, vp, C.c_float, i32, vp, C.c_int, vp]
+    L.e3_layer_norm_workspace_size.argtypes = [ip, i64, C.POINTER(sz)]
+    L.e3_layer_norm_backward.argtypes = [ip, i64, vp, vp, vp, C.c_float, i32, vp, vp, vp, vp, sz,
+                                         C.c_int, vp]
+    pp = C.POINTER(_Param)
+    L.e3_param_check.argtypes = [i32, pp]
+    L.e3_grad_norm_workspace_size.argtypes = [i32, pp, C.POINTER(sz)]
+    L.e3_grad_norm.argtypes = [i32, pp, C.c_double, vp, vp, sz, vp]
+    L.e3_adamw.argtypes = [i32, pp, C.POINTER(_AdamwArgs), vp]
+    L.e3_adamw_moments.argtypes = [i32, pp, C.POINTER(vp), C.POINTER(vp), vp]
     L.e3_release_all.argtypes = []
     L.e3_last_error.restype = C.c_char_p
     for name in EXPORTS:
@@ -997,3 +1024,292 @@ def conv_double_backward_generic(desc: Desc, rowptr, sender, workspace, Y, x, w,
         _ptr(ddm), _ptr(scratch), scratch.numel() * scratch.element_size(), _dtype_code(x),
         _stream(stream)))
     return dx2, dY2, dw2, ddm
+
+
+# ------------------------------------------------------------ normalisation
+
+def _on(device, call, stream):
+    """call(stream) on `device`, whichever device is current: on the given
+    stream, or on the device's current one."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _norm_shapes(irreps, x, weight, bias=None):
+    """Checks the operands both directions share; (rows, C, number of blocks,
+    number of 0e blocks)."""
+    import torch
+    _need(x, "x")
+    if x.dim() != 3 or x.shape[1] != synth.dim(irreps):
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows][{synth.dim(irreps)}][C]")
+    rows, _, ch = x.shape
+    scalars = sum(1 for l, p in irreps if l == 0 and p == 1)
+    if weight is not None:
+        _need(weight, "weight", shape=(len(irreps), ch), dtype=torch.float32)
+    if bias is not None:
+        _need(bias, "bias", shape=(scalars, ch), dtype=torch.float32)
+    _same_device(x.device, weight=weight, bias=bias)
+    return rows, ch, len(irreps), scalars
+
+
+def layer_norm(irreps, x, weight=None, bias=None, eps=1e-5, flags=0, out=None, stream=None):
+    """Normalised features y [rows][dim][C] of x over `irreps` ([(l, parity)]),
+    block by block: 0e blocks centred over their channels (unless
+    E3_NORM_UNCENTERED), every block divided by its root mean square over
+    components and channels, times weight [blocks][C], plus bias [0e blocks][C]
+    for 0e blocks.  [(0, 1)] is the ordinary layer norm over C channels.  out
+    may be x."""
+    import torch
+    rows, ch, _, _ = _norm_shapes(irreps, x, weight, bias)
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out, "out", shape=tuple(x.shape), dtype=x.dtype)
+    _same_device(x.device, out=out)
+    a = _irreps_struct(irreps, ch)
+    _check(_on(x.device, lambda s: lib().e3_layer_norm(
+        C.byref(a), rows, _ptr(x), _ptr(weight), _ptr(bias), eps, flags, _ptr(out),
+        _dtype_code(x), s), stream))
+    return out
+
+
+def layer_norm_workspace_size(irreps, rows: int, channels: int) -> int:
+    a, nb = _irreps_struct(irreps, channels), C.c_size_t()
+    _check(lib().e3_layer_norm_workspace_size(C.byref(a), rows, C.byref(nb)))
+    return nb.value
+
+
+def layer_norm_backward(irreps, x, weight, dy, eps=1e-5, flags=0, dx=None, dweight=None,
+                        dbias=None, workspace=None, stream=None):
+    """(dx, dweight [blocks][C], dbias [0e blocks][C]) of layer_norm for the
+    cotangent dy; weight may be None (ones).  dx may be x or dy."""
+    import torch
+    rows, ch, n_blocks, scalars = _norm_shapes(irreps, x, weight)
+    dev, shape = x.device, tuple(x.shape)
+    _need(dy, "dy", shape=shape, dtype=x.dtype)
+    if dx is None:
+        dx = torch.empty_like(x)
+    if dweight is None:
+        dweight = torch.empty((n_blocks, ch), device=dev, dtype=torch.float32)
+    if dbias is None:
+        dbias = torch.empty((scalars, ch), device=dev, dtype=torch.float32)
+    if workspace is None:
+        workspace = torch.empty(layer_norm_workspace_size(irreps, rows, ch), device=dev,
+                                dtype=torch.uint8)
+    _need(dx, "dx", shape=shape, dtype=x.dtype)
+    _need(dweight, "dweight", shape=(n_blocks, ch), dtype=torch.float32)
+    _need(dbias, "dbias", shape=(scalars, ch), dtype=torch.float32)
+    _need(workspace, "workspace")
+    _same_device(dev, dy=dy, dx=dx, dweight=dweight, dbias=dbias, workspace=workspace)
+    a = _irreps_struct(irreps, ch)
+    _check(_on(dev, lambda s: lib().e3_layer_norm_backward(
+        C.byref(a), rows, _ptr(x), _ptr(weight), _ptr(dy), eps, flags, _ptr(dx), _ptr(dweight),
+        _ptr(dbias), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _dtype_code(x), s), stream))
+    return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------- optimizer
+
+class Params:
+    """The tensors of a network's weights with what their update reads and
+    writes (lists of equal length; every tensor contiguous, on one GPU):
+
+      params        float32, any shape; None for a list that only serves
+                    grad_norm
+      grads         float32 or bfloat16, the shape of the parameter
+      m, v          moments: float32 of as many elements, or 8-bit codes
+                    (int8 and uint8), for which m_scale and v_scale (float32
+                    [ceil(n/256)], None for the other tensors) are needed;
+                    adamw_state makes them
+      copies        bfloat16 copies of the parameters to be kept up to date,
+                    or None
+      weight_decay  one number, or one a tensor
+
+    Keeps references to the tensors and their addresses: a tensor whose
+    storage is replaced needs a new list (set_grads for new gradients)."""
+
+    def __init__(self, params=None, grads=None, m=None, v=None, m_scale=None, v_scale=None,
+                 copies=None, weight_decay=0.0):
+        import torch
+        if grads is None:
+            raise ValueError("grads is required")
+        n = len(grads)
+        self.updates = params is not None
+        cols = {"params": params, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale,
+                "copies": copies}
+        if not self.updates and any(c is not None for c in cols.values()):
+            raise ValueError("params is required with moments, scales or copies")
+        if self.updates and (m is None or v is None):
+            raise ValueError("m and v are required with params")
+        for name, c in cols.items():
+            if c is not None and len(c) != n:
+                raise ValueError(f"{name} has {len(c)} tensors, grads {n}")
+        decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(decay) != n:
+            raise ValueError(f"weight_decay has {len(decay)} values, expected {n}")
+        self._arr = (_Param * max(1, n))()
+        self._n = n
+        self.device = None
+        self._keep = {k: list(c) if c is not None else [None] * n for k, c in cols.items()}
+        self.set_grads(grads)
+        for i in range(n):
+            e, size = self._arr[i], grads[i].numel()
+            e.weight_decay = decay[i]
+            if not self.updates:
+                continue
+            p, mi, vi, ms, vs, cp = (self._keep[k][i] for k in
+                                     ("params", "m", "v", "m_scale", "v_scale", "copies"))
+            _need(p, f"params[{i}]", shape=tuple(grads[i].shape), dtype=torch.float32)
+            codes = ms is not None or vs is not None
+            _need(mi, f"m[{i}]", dtype=torch.int8 if codes else torch.float32)
+            _need(vi, f"v[{i}]", dtype=torch.uint8 if codes else torch.float32)
+            for t, name in ((mi, "m"), (vi, "v")):
+                if t.numel() != size:
+                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {size}")
+            if codes:
+                for t, name in ((ms, "m_scale"), (vs, "v_scale")):
+                    _need(t, f"{name}[{i}]", shape=((size + 255) // 256,), dtype=torch.float32)
+            if cp is not None:
+                _need(cp, f"copies[{i}]", shape=tuple(p.shape), dtype=torch.bfloat16)
+            for t, name in ((p, "params"), (mi, "m"), (vi, "v"), (ms, "m_scale"),
+                            (vs, "v_scale"), (cp, "copies")):
+                _same_device(self.device, **{f"{name}[{i}]": t})
+            e.p, e.m, e.v = p.data_ptr(), mi.data_ptr(), vi.data_ptr()
+            e.m_scale = ms.data_ptr() if codes else None
+            e.v_scale = vs.data_ptr() if codes else None
+            e.p_bf16 = cp.data_ptr() if cp is not None else None
+        if self.updates:
+            _check(lib().e3_param_check(n, self._arr))
+        nb = C.c_size_t()
+        _check(lib().e3_grad_norm_workspace_size(n, self._arr, C.byref(nb)))
+        self.workspace_bytes = nb.value  # of grad_norm
+
+    def set_grads(self, grads):
+        """Other gradient tensors for the same parameters."""
+        if len(grads) != self._n:
+            raise ValueError(f"grads has {len(grads)} tensors, expected {self._n}")
+        codes = []
+        for i, g in enumerate(grads):
+            old = self._keep["params"][i]
+            _need(g, f"grads[{i}]", shape=None if old is None else tuple(old.shape))
+            if self._arr[i].grad is not None and old is None and g.numel() != self._arr[i].n:
+                raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {self._arr[i].n}")
+            if self.device is None:
+                self.device = g.device
+            _same_device(self.device, **{f"grads[{i}]": g})
+            codes.append(_dtype_code(g))
+        for i, g in enumerate(grads):
+            e = self._arr[i]
+            e.n, e.grad, e.grad_dtype = g.numel(), g.data_ptr(), codes[i]
+        self._grads = list(grads)
+        if self.updates and self._arr[0].p:
+            _check(lib().e3_param_check(self._n, self._arr))
+
+    def __len__(self):
+        return self._n
+
+
+def adamw_state(params, bits=32):
+    """Zero moments for a list of parameters: (m, v, m_scale, v_scale), lists
+    as Params takes them; bits 32, or 8 (a list gives each tensor its own)."""
+    import torch
+    bits = [bits] * len(params) if isinstance(bits, int) else list(bits)
+    if len(bits) != len(params) or any(b not in (8, 32) for b in bits):
+        raise ValueError("bits is 8 or 32, or one of them for every parameter")
+    m, v, ms, vs = [], [], [], []
+    for p, b in zip(params, bits):
+        n, dev = p.numel(), p.device
+        z = lambda size, dt: torch.zeros(size, device=dev, dtype=dt)  # noqa: E731
+        m.append(z(n, torch.int8 if b == 8 else torch.float32))
+        v.append(z(n, torch.uint8 if b == 8 else torch.float32))
+        ms.append(z((n + 255) // 256, torch.float32) if b == 8 else None)
+        vs.append(z((n + 255) // 256, torch.float32) if b == 8 else None)
+    return m, v, ms, vs
+
+
+def grad_norm(params: Params, max_norm=float("inf"), out=None, workspace=None, stream=None):
+    """float32 [2] on the GPU: the 2-norm of all gradients together and the
+    factor min(1, max_norm / (norm + 1e-6)) that clips it (NaN for a norm that
+    is not finite); out[1:] is adamw's grad_scale."""
+    import torch
+    dev = params.device or torch.device("cuda", torch.cuda.current_device())
+    if out is None:
+        out = torch.empty(2, device=dev, dtype=torch.float32)
+    if workspace is None:
+        workspace = torch.empty(params.workspace_bytes, device=dev, dtype=torch.uint8)
+    _need(out, "out", shape=(2,), dtype=torch.float32)
+    _need(workspace, "workspace")
+    _same_device(dev, out=out, workspace=workspace)
+    _check(_on(dev, lambda s: lib().e3_grad_norm(
+        len(params), params._arr, max_norm, _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), s), stream))
+    return out
+
+
+def adamw(params: Params, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=None, flags=0,
+          stream=None):
+    """One AdamW step over every tensor of the list.  step (1 for the first
+    update) is an int, or an int64 GPU tensor of one element; lr a number, or
+    a float32 GPU tensor of one element (both are read when the step runs, so
+    a captured step can be replayed); grad_scale a float32 GPU tensor of one
+    element that multiplies the gradients."""
+    import torch
+    if not params.updates:
+        raise ValueError("the list holds gradients only")
+    a = _AdamwArgs(0.0, beta1, beta2, eps, 1, None, None, None, flags)
+    for t, name, dt in ((step, "step", torch.int64), (lr, "lr", torch.float32),
+                        (grad_scale, "grad_scale", torch.float32)):
+        if isinstance(t, torch.Tensor):
+            _need(t, name, dtype=dt)
+            if t.numel() != 1:
+                raise ValueError(f"{name} must hold one element")
+            _same_device(params.device or t.device, **{name: t})
+    if isinstance(step, torch.Tensor):
+        a.step_dev = step.data_ptr()
+    else:
+        a.step = step
+    if isinstance(lr, torch.Tensor):
+        a.lr_dev = lr.data_ptr()
+    else:
+        a.lr = lr
+    if grad_scale is not None:
+        a.grad_scale = grad_scale.data_ptr()
+    dev = params.device or torch.device("cuda", torch.cuda.current_device())
+    _check(_on(dev, lambda s: lib().e3_adamw(len(params), params._arr, C.byref(a), s), stream))
+
+
+def adamw_moments(params: Params, m_out=None, v_out=None, stream=None):
+    """(m, v): lists of the 8-bit moments of every tensor as float32 [n]."""
+    import torch
+    if not params.updates:
+        raise ValueError("the list holds gradients only")
+    n = len(params)
+    outs = []
+    for given, name in ((m_out, "m_out"), (v_out, "v_out")):
+        if given is None:
+            given = [torch.empty(params._arr[i].n, device=params.device, dtype=torch.float32)
+                     for i in range(n)]
+        if len(given) != n:
+            raise ValueError(f"{name} has {len(given)} tensors, expected {n}")
+        ptrs = (C.c_void_p * max(1, n))()
+        for i, t in enumerate(given):
+            _need(t, f"{name}[{i}]", dtype=torch.float32)
+            if t.numel() != params._arr[i].n:
+                raise ValueError(f"{name}[{i}] has {t.numel()} elements, "
+                                 f"expected {params._arr[i].n}")
+            _same_device(params.device, **{f"{name}[{i}]": t})
+            ptrs[i] = t.data_ptr()
+        outs.append((given, ptrs))
+    dev = params.device or torch.device("cuda", torch.cuda.current_device())
+    _check(_on(dev, lambda s: lib().e3_adamw_moments(n, params._arr, outs[0][1], outs[1][1], s),
+               stream))
+    return outs[0][0], outs[1][0]

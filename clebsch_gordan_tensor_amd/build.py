@@ -32,6 +32,8 @@ HIP_SOURCES = [
     "kernels/radial.hip",
     "kernels/generic.hip",
     "kernels/gemm.hip",
+    "kernels/norm.hip",
+    "kernels/optimizer.hip",
     "api.cpp",
     "host/cg_ladder.cpp",
 ]

@@ -2346,6 +2346,314 @@ e3_status e3_conv_double_backward_generic(
                                   scratch, dtype, hipStream_t(stream), fwd, bwd);
 }
 
+namespace {
+
+// A byte range [at, at + bytes) of device memory.
+struct Range {
+  uintptr_t at;
+  uint64_t bytes;
+};
+Range range(const void* p, uint64_t bytes) { return {reinterpret_cast<uintptr_t>(p), bytes}; }
+bool overlap(Range a, Range b) {
+  return a.bytes > 0 && b.bytes > 0 && a.at < b.at + b.bytes && b.at < a.at + a.bytes;
+}
+bool aligned_to(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+struct Norm {
+  std::vector<e3k::NormBlock> blocks;
+  int C = 0, dim = 0, scalars = 0;
+};
+
+e3_status parse_norm(const e3_irreps* irreps, int64_t n_rows, int32_t flags, Norm& n) {
+  if (!irreps) return fail(E3_ERR_INVALID_ARG, "irreps pointer is null");
+  std::vector<e3k::IrSpec> l;
+  std::vector<int> mul;
+  if (irreps->n > 1024)
+    return fail(E3_ERR_UNSUPPORTED, "the normalisation takes at most 1024 blocks");
+  e3_status s = parse_list(*irreps, "irreps", l, mul);
+  if (s != E3_OK) return s;
+  if (l.empty()) return fail(E3_ERR_IRREPS, "irreps need at least one block");
+  if (flags & ~int32_t(E3_NORM_UNCENTERED)) return fail(E3_ERR_INVALID_ARG, "unknown flags");
+  n.C = mul[0];
+  int top = 0;
+  for (size_t i = 0; i < l.size(); ++i) {
+    if (mul[i] != n.C) return fail(E3_ERR_IRREPS, "blocks need one multiplicity");
+    const bool scalar = l[i].l == 0 && l[i].p == 1;
+    e3k::NormBlock b{};
+    b.comp0 = n.dim;
+    b.nc = 2 * l[i].l + 1;
+    b.index = int(i);
+    b.bias = scalar ? n.scalars++ : -1;
+    b.centered = scalar && !(flags & E3_NORM_UNCENTERED);
+    n.blocks.push_back(b);
+    n.dim += b.nc;
+    top = std::max(top, l[i].l);
+  }
+  if (top > 8 ||
+      n.C > (top > 3 ? e3k::kNormMaxChannelsHigh : e3k::kNormMaxChannels))
+    return fail(E3_ERR_UNSUPPORTED, "the normalisation takes degrees up to 8 and 4096 channels (1024 "
+                                    "when a degree is above 3)");
+  if (n_rows < 0) return fail(E3_ERR_INVALID_ARG, "n_rows < 0");
+  if (n_rows > (int64_t(1) << 60) / (int64_t(n.dim) * n.C))
+    return fail(E3_ERR_UNSUPPORTED, "n_rows too large");
+  return E3_OK;
+}
+
+e3_status norm_args(float eps, e3_dtype dtype) {
+  if (dtype != E3_F32 && dtype != E3_BF16) return fail(E3_ERR_INVALID_ARG, "unknown dtype");
+  if (!(eps > 0.0f) || !std::isfinite(eps))
+    return fail(E3_ERR_INVALID_ARG, "eps must be positive and finite");
+  return E3_OK;
+}
+
+// y (or dx) may be `in` itself, element for element, but not overlap it otherwise.
+bool partly_overlaps(const void* out, const void* in, uint64_t bytes) {
+  return out != in && overlap(range(out, bytes), range(in, bytes));
+}
+
+}  // namespace
+
+e3_status e3_layer_norm(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                        const float* weight, const float* bias, float eps, int32_t flags, void* y,
+                        e3_dtype dtype, void* stream) {
+  Norm n;
+  e3_status s;
+  if ((s = parse_norm(irreps, n_rows, flags, n)) != E3_OK || (s = norm_args(eps, dtype)) != E3_OK)
+    return s;
+  if (n_rows == 0) return ok();
+  if (!x || !y) return fail(E3_ERR_INVALID_ARG, "null pointer");
+  const unsigned esize = dtype == E3_BF16 ? 2 : 4;
+  if (!aligned_to(x, esize) || !aligned_to(y, esize) || !aligned_to(weight, 4) ||
+      !aligned_to(bias, 4))
+    return fail(E3_ERR_ALIGNMENT, "x, y, weight and bias must be aligned to their elements");
+  if (partly_overlaps(y, x, uint64_t(n_rows) * n.dim * n.C * esize))
+    return fail(E3_ERR_INVALID_ARG, "y overlaps x without being x");
+  e3k::NormArgs a{};
+  a.n_rows = n_rows;
+  a.dim = n.dim;
+  a.C = n.C;
+  a.x = x;
+  a.y = y;
+  a.w = weight;
+  a.b = bias;
+  a.eps = eps;
+  return hip_status(e3k::launch_norm(false, a, n.blocks.data(), int(n.blocks.size()),
+                                     dtype == E3_BF16, hipStream_t(stream)),
+                    "layer_norm");
+}
+
+e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, size_t* bytes) {
+  Norm n;
+  const e3_status s = parse_norm(irreps, n_rows, 0, n);
+  if (s != E3_OK) return s;
+  if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
+  *bytes = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), int(n.blocks.size()));
+  return ok();
+}
+
+e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                                 const float* weight, const void* dy, float eps, int32_t flags,
+                                 void* dx, float* dweight, float* dbias, void* workspace,
+                                 size_t ws_bytes, e3_dtype dtype, void* stream) {
+  Norm n;
+  e3_status s;
+  if ((s = parse_norm(irreps, n_rows, flags, n)) != E3_OK || (s = norm_args(eps, dtype)) != E3_OK)
+    return s;
+  const int nb = int(n.blocks.size());
+  const size_t need = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), nb);
+  if (!workspace || ws_bytes < need)
+    return fail(E3_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  if (n_rows > 0 && (!x || !dy || !dx)) return fail(E3_ERR_INVALID_ARG, "null pointer");
+  const unsigned esize = dtype == E3_BF16 ? 2 : 4;
+  if (!aligned16(workspace)) return fail(E3_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if (!aligned_to(x, esize) || !aligned_to(dy, esize) || !aligned_to(dx, esize) ||
+      !aligned_to(weight, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
+    return fail(E3_ERR_ALIGNMENT, "x, dy, dx, weight, dweight and dbias must be aligned to their "
+                                  "elements");
+  const uint64_t bytes = uint64_t(n_rows) * n.dim * n.C * esize;
+  if (partly_overlaps(dx, x, bytes) || partly_overlaps(dx, dy, bytes))
+    return fail(E3_ERR_INVALID_ARG, "dx overlaps x or dy without being it");
+  e3k::NormArgs a{};
+  a.n_rows = n_rows;
+  a.dim = n.dim;
+  a.C = n.C;
+  a.x = x;
+  a.dy = dy;
+  a.y = dx;
+  a.w = weight;
+  a.dw = dweight;
+  a.db = dbias;
+  a.part = static_cast<float*>(workspace);
+  a.eps = eps;
+  return hip_status(e3k::launch_norm(true, a, n.blocks.data(), nb, dtype == E3_BF16,
+                                     hipStream_t(stream)),
+                    "layer_norm_backward");
+}
+
+namespace {
+
+std::string tensor_at(int32_t i) { return "tensor " + std::to_string(i) + ": "; }
+
+// The kernels' form of a list.  `grads` and `state`: what the call uses.
+e3_status parse_params(int32_t n, const e3_param* p, bool grads, bool state,
+                       std::vector<e3k::ParamTensor>& out) {
+  if (n < 0 || (n > 0 && !p)) return fail(E3_ERR_INVALID_ARG, "bad list of tensors");
+  if (n > 65536) return fail(E3_ERR_UNSUPPORTED, "a list holds at most 65536 tensors");
+  out.clear();
+  out.reserve(size_t(n));
+  for (int32_t i = 0; i < n; ++i) {
+    const e3_param& t = p[i];
+    if (t.n < 0 || t.n > e3k::kMaxParamElements)
+      return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "n must be in [0, 2^35]");
+    if (grads && t.grad_dtype != E3_F32 && t.grad_dtype != E3_BF16)
+      return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "unknown grad_dtype");
+    if (t.n > 0 && grads && !t.grad) return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "null pointer");
+    if (grads && !aligned_to(t.grad, t.grad_dtype == E3_BF16 ? 2 : 4))
+      return fail(E3_ERR_ALIGNMENT, tensor_at(i) + "grad must be aligned to its element");
+    if (state) {
+      if (t.n > 0 && (!t.p || !t.m || !t.v))
+        return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "null pointer");
+      if (!t.m_scale != !t.v_scale)
+        return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "m_scale and v_scale come together");
+      if (!std::isfinite(t.weight_decay))
+        return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "weight_decay must be finite");
+      if (!aligned_to(t.p, 4) || !aligned_to(t.p_bf16, 2) || !aligned_to(t.m_scale, 4) ||
+          !aligned_to(t.v_scale, 4) ||
+          (!t.m_scale && (!aligned_to(t.m, 4) || !aligned_to(t.v, 4))))
+        return fail(E3_ERR_ALIGNMENT,
+                    tensor_at(i) + "p, moments, scales and p_bf16 must be aligned to their elements");
+    }
+    out.push_back({t.n, t.p, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.p_bf16, t.weight_decay,
+                   t.grad_dtype == E3_BF16});
+  }
+  return E3_OK;
+}
+
+}  // namespace
+
+e3_status e3_param_check(int32_t n_params, const e3_param* params) {
+  std::vector<e3k::ParamTensor> t;
+  const e3_status s = parse_params(n_params, params, true, true, t);
+  if (s != E3_OK) return s;
+  struct Use {
+    Range r;
+    bool written;
+    int32_t tensor;
+  };
+  std::vector<Use> uses;
+  for (int32_t i = 0; i < n_params; ++i) {
+    const e3_param& q = params[i];
+    const uint64_t n = uint64_t(q.n), runs = 4 * ((n + 255) / 256);
+    const uint64_t moment = q.m_scale ? n : 4 * n;
+    const Use u[] = {{range(q.p, 4 * n), true, i},
+                     {range(q.grad, (q.grad_dtype == E3_BF16 ? 2 : 4) * n), false, i},
+                     {range(q.m, moment), true, i},
+                     {range(q.v, moment), true, i},
+                     {range(q.m_scale, q.m_scale ? runs : 0), true, i},
+                     {range(q.v_scale, q.v_scale ? runs : 0), true, i},
+                     {range(q.p_bf16, q.p_bf16 ? 2 * n : 0), true, i}};
+    for (const Use& x : u)
+      if (x.r.bytes > 0) uses.push_back(x);
+  }
+  std::sort(uses.begin(), uses.end(), [](const Use& a, const Use& b) { return a.r.at < b.r.at; });
+  // the furthest end so far of what is written, and of everything
+  const Use *written = nullptr, *any = nullptr;
+  const auto end = [](const Use* u) { return u->r.at + u->r.bytes; };
+  for (const Use& u : uses) {
+    const Use* hit = u.written ? any : written;
+    if (hit && u.r.at < end(hit))
+      return fail(E3_ERR_INVALID_ARG, tensor_at(u.tensor) + "memory overlaps what tensor " +
+                                          std::to_string(hit->tensor) + " uses");
+    if (u.written && (!written || end(&u) > end(written))) written = &u;
+    if (!any || end(&u) > end(any)) any = &u;
+  }
+  return ok();
+}
+
+e3_status e3_grad_norm_workspace_size(int32_t n_params, const e3_param* params, size_t* bytes) {
+  std::vector<e3k::ParamTensor> t;
+  const e3_status s = parse_params(n_params, params, true, false, t);
+  if (s != E3_OK) return s;
+  if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
+  *bytes = 8 * std::max<size_t>(1, e3k::grad_norm_partials(t.data(), int(t.size())));
+  return ok();
+}
+
+e3_status e3_grad_norm(int32_t n_params, const e3_param* params, double max_norm, float* out,
+                       void* workspace, size_t ws_bytes, void* stream) {
+  std::vector<e3k::ParamTensor> t;
+  const e3_status s = parse_params(n_params, params, true, false, t);
+  if (s != E3_OK) return s;
+  if (!(max_norm > 0.0)) return fail(E3_ERR_INVALID_ARG, "max_norm must be positive");
+  const size_t need = 8 * std::max<size_t>(1, e3k::grad_norm_partials(t.data(), int(t.size())));
+  if (!workspace || ws_bytes < need)
+    return fail(E3_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  if (!out) return fail(E3_ERR_INVALID_ARG, "null pointer");
+  if (!aligned_to(workspace, 8) || !aligned_to(out, 4))
+    return fail(E3_ERR_ALIGNMENT, "workspace must be 8-byte aligned, out 4-byte aligned");
+  return hip_status(e3k::launch_grad_norm(t.data(), int(t.size()), max_norm,
+                                          static_cast<double*>(workspace), out,
+                                          hipStream_t(stream)),
+                    "grad_norm");
+}
+
+e3_status e3_adamw(int32_t n_params, const e3_param* params, const e3_adamw_args* args,
+                   void* stream) {
+  std::vector<e3k::ParamTensor> t;
+  const e3_status s = parse_params(n_params, params, true, true, t);
+  if (s != E3_OK) return s;
+  if (!args) return fail(E3_ERR_INVALID_ARG, "args is null");
+  const e3_adamw_args& g = *args;
+  if (!(g.beta1 >= 0.0 && g.beta1 < 1.0 && g.beta2 >= 0.0 && g.beta2 < 1.0))
+    return fail(E3_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+  if (!(g.eps > 0.0) || !(float(g.eps) > 0.0f) || !std::isfinite(float(g.eps)))
+    return fail(E3_ERR_INVALID_ARG, "eps must be positive and finite in float32");
+  if (!g.lr_dev && !std::isfinite(g.lr)) return fail(E3_ERR_INVALID_ARG, "lr must be finite");
+  if (!g.step_dev && g.step < 1) return fail(E3_ERR_INVALID_ARG, "step counts from 1");
+  if (g.flags & ~int32_t(E3_ADAMW_SKIP_NONFINITE))
+    return fail(E3_ERR_INVALID_ARG, "unknown flags");
+  if ((g.flags & E3_ADAMW_SKIP_NONFINITE) && !g.grad_scale)
+    return fail(E3_ERR_INVALID_ARG, "E3_ADAMW_SKIP_NONFINITE needs grad_scale");
+  if (!aligned_to(g.step_dev, 8) || !aligned_to(g.lr_dev, 4) || !aligned_to(g.grad_scale, 4))
+    return fail(E3_ERR_ALIGNMENT, "step_dev, lr_dev and grad_scale must be aligned to their type");
+  e3k::AdamArgs a{};
+  a.lr = g.lr;
+  a.beta1 = g.beta1;
+  a.beta2 = g.beta2;
+  a.step = std::max<int64_t>(1, g.step);
+  a.lr_f = float(g.lr);
+  a.size = float(g.lr / (1.0 - std::pow(g.beta1, double(a.step))));
+  a.inv_c2 = float(1.0 / (1.0 - std::pow(g.beta2, double(a.step))));
+  a.eps = float(g.eps);
+  a.step_dev = g.step_dev;
+  a.lr_dev = g.lr_dev;
+  a.grad_scale = g.grad_scale;
+  a.skip_nonfinite = (g.flags & E3_ADAMW_SKIP_NONFINITE) != 0;
+  return hip_status(e3k::launch_adamw(t.data(), int(t.size()), a, hipStream_t(stream)), "adamw");
+}
+
+e3_status e3_adamw_moments(int32_t n_params, const e3_param* params, float* const* m_out,
+                           float* const* v_out, void* stream) {
+  std::vector<e3k::ParamTensor> t;
+  const e3_status s = parse_params(n_params, params, false, true, t);
+  if (s != E3_OK) return s;
+  if (n_params > 0 && (!m_out || !v_out)) return fail(E3_ERR_INVALID_ARG, "null pointer");
+  for (int32_t i = 0; i < n_params; ++i) {
+    if (!t[i].m_scale)
+      return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "its moments are not 8-bit codes");
+    if (t[i].n > 0 && (!m_out[i] || !v_out[i]))
+      return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "null pointer");
+    if (!aligned_to(m_out[i], 4) || !aligned_to(v_out[i], 4))
+      return fail(E3_ERR_ALIGNMENT, tensor_at(i) + "outputs must be 4-byte aligned");
+    t[i].p = m_out[i];
+    t[i].grad = v_out[i];
+  }
+  return hip_status(e3k::launch_moments8(t.data(), int(t.size()), hipStream_t(stream)),
+                    "adamw_moments");
+}
+
 const char* e3_last_error(void) { return g_last_error.c_str(); }
 
 e3_status e3_check_graph(int32_t n_nodes, int32_t n_edges, const int32_t* rowptr,

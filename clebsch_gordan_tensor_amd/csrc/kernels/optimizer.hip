@@ -1,0 +1,435 @@
+// The update of a network's weights: the 2-norm of all gradients with its
+// clip factor, and the AdamW step, each over a list of tensors whose pointers
+// travel in the kernel arguments (no table in device memory, nothing copied
+// to the device, so the calls can be captured into a graph).
+//
+//   g = s grad,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = p - lr wd p - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+//
+// Moments in 8 bits: every 256 consecutive elements of a tensor share a
+// float32 scale per moment,
+//   m = s c |c|,  c in [-127, 127],  s = max|m| / 127^2
+//   v = (s c^2)^2, c in [0, 255],    s = sqrt(max v) / 255^2
+// so the step between codes shrinks towards zero: relative steps of 2/c over
+// a range of 1.6e4 (m) and 6.5e4 (sqrt v).  A code is the number of borders
+// s (k + 1/2)^2, or (s (k + 1/2)^2)^2, below the value; a v that is not zero
+// takes at least code 1, so no element is divided by eps alone because its v
+// was rounded away.  Codes are those of the moments in 64 bits, where both
+// products above are exact or rounded once: they do not hang on how a 32-bit
+// evaluation would round.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "common.h"
+#include "registry.h"
+
+namespace e3k {
+namespace {
+
+typedef float of4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef __bf16 ob4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float tf4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32u __attribute__((aligned(1)));
+
+constexpr int kParamThreads = 256;
+constexpr int kQBlock = 256;  // elements per scale
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 32) / kParamThreads - 1;  // 2^32 threads a launch
+static_assert(sizeof(ParamList) + sizeof(AdamArgs) <= 4096, "kernel arguments");
+static_assert(kMaxParamElements / kAdamChunk < kMaxWorkgroups);
+
+// Four consecutive elements, those at n and beyond 0.
+__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float (&v)[4]) {
+  if (i + 4 <= n) {
+    const tf4 t = *reinterpret_cast<const of4*>(p + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? p[i + e] : 0.0f;
+  }
+}
+__device__ __forceinline__ void load4(const __bf16* p, int64_t i, int64_t n, float (&v)[4]) {
+  if (i + 4 <= n) {
+    const tf4 t = __builtin_convertvector(*reinterpret_cast<const ob4*>(p + i), tf4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < n ? float(p[i + e]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void load4_grad(const ParamTensor& t, int64_t i, float (&v)[4]) {
+  if (t.grad_bf16) load4(static_cast<const __bf16*>(t.grad), i, t.n, v);
+  else load4(static_cast<const float*>(t.grad), i, t.n, v);
+}
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float (&v)[4]) {
+  if (i + 4 <= n) {
+    const tf4 t = {v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<of4*>(p + i) = t;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < n) p[i + e] = v[e];
+  }
+}
+__device__ __forceinline__ void store4(__bf16* p, int64_t i, int64_t n, const float (&v)[4]) {
+  if (i + 4 <= n) {
+    const tf4 t = {v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<ob4*>(p + i) = __builtin_convertvector(t, ob4);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < n) p[i + e] = __bf16(v[e]);
+  }
+}
+// Four codes as the bytes of a word.
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
+  if (i + 4 <= n) return *reinterpret_cast<const u32u*>(p + i);
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) w |= uint32_t(p[i + e]) << (8 * e);
+  return w;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, uint32_t w) {
+  if (i + 4 <= n) {
+    *reinterpret_cast<u32u*>(p + i) = w;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) p[i + e] = uint8_t(w >> (8 * e));
+}
+
+__device__ __forceinline__ int tensor_of(const ParamList& l) {
+  int i = 0;
+  while (i + 1 < l.n && int(blockIdx.x) >= l.wg0[i + 1]) ++i;
+  return i;
+}
+
+// ------------------------------------------------------- the gradients' norm
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// One partial per workgroup; squares and sums in 64 bits, so no gradient of
+// float32's range overflows and the order of summation does not show.
+__global__ void __launch_bounds__(kParamThreads) k_grad_norm(const ParamList l, double* part) {
+  __shared__ double s_sum[kParamThreads / 64];
+  const int ti = tensor_of(l);
+  const ParamTensor t = l.t[ti];
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kNormChunk;
+  double s = 0.0;
+#pragma unroll
+  for (int it = 0; it < kNormChunk / (4 * kParamThreads); ++it) {
+    const int64_t i = base + (it * kParamThreads + int(threadIdx.x)) * 4;
+    if (i >= t.n) break;
+    float g[4];
+    load4_grad(t, i, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = fma(double(g[e]), double(g[e]), s);
+  }
+  s = wave_sum64(s);
+  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int j = 1; j < kParamThreads / 64; ++j) s += s_sum[j];
+    part[blockIdx.x] = s;
+  }
+}
+
+// out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)), NaN where the
+// norm (as float32) is not finite.
+__global__ void __launch_bounds__(1024)
+    k_grad_norm_total(int64_t n, const double* part, double max_norm, float* out) {
+  __shared__ double s_sum[16];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+  s = wave_sum64(s);
+  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int j = 1; j < 16; ++j) s += s_sum[j];
+  const double norm = sqrt(s), f = max_norm / (norm + 1e-6);
+  out[0] = float(norm);
+  out[1] = isfinite(float(norm)) ? float(f < 1.0 ? f : 1.0) : __builtin_nanf("");
+}
+
+// ------------------------------------------------------------------ the step
+
+struct Step {
+  float lr, size, inv_c2, eps;  // size = lr / (1 - b1^t), inv_c2 = 1 / (1 - b2^t)
+  float scale;                  // of the gradients
+  bool skip;
+};
+
+__device__ __forceinline__ double pow_int(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1, b *= b)
+    if (t & 1) r *= b;
+  return r;
+}
+
+__device__ __forceinline__ Step step_of(const AdamArgs& a) {
+  Step s{a.lr_f, a.size, a.inv_c2, a.eps, 1.0f, false};
+  if (a.step_dev || a.lr_dev) {
+    const double lr = a.lr_dev ? double(*a.lr_dev) : a.lr;
+    const int64_t t = a.step_dev ? max(int64_t(1), *a.step_dev) : a.step;
+    s.lr = float(lr);
+    s.size = float(lr / (1.0 - pow_int(a.beta1, t)));
+    s.inv_c2 = float(1.0 / (1.0 - pow_int(a.beta2, t)));
+  }
+  if (a.grad_scale) {
+    s.scale = *a.grad_scale;
+    s.skip = a.skip_nonfinite && !isfinite(s.scale);
+  }
+  return s;
+}
+
+// p after the step.  Decay and update are added first and taken off together:
+// one rounding of p, and lr wd is not lost in 1 - lr wd.
+__device__ __forceinline__ float stepped(float p, float m, float v, float lr_wd, const Step& s) {
+  const float d = __builtin_amdgcn_sqrtf(v * s.inv_c2) + s.eps;
+  return p - fmaf(s.size * m, __builtin_amdgcn_rcpf(d), lr_wd * p);
+}
+
+__global__ void __launch_bounds__(kParamThreads) k_adamw(const ParamList l, const AdamArgs a) {
+  const Step st = step_of(a);
+  if (st.skip) return;
+  const int ti = tensor_of(l);
+  const ParamTensor t = l.t[ti];
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kAdamChunk;
+  const float lr_wd = st.lr * t.weight_decay;
+  const float b1 = float(a.beta1), c1 = float(1.0 - a.beta1);
+  const float b2 = float(a.beta2), c2 = float(1.0 - a.beta2);
+  float* m = static_cast<float*>(t.m);
+  float* v = static_cast<float*>(t.v);
+#pragma unroll
+  for (int it = 0; it < kAdamChunk / (4 * kParamThreads); ++it) {
+    const int64_t i = base + (it * kParamThreads + int(threadIdx.x)) * 4;
+    if (i >= t.n) break;
+    float p4[4], g4[4], m4[4], v4[4];
+    load4(t.p, i, t.n, p4);
+    load4_grad(t, i, g4);
+    load4(m, i, t.n, m4);
+    load4(v, i, t.n, v4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float g = g4[e] * st.scale;
+      m4[e] = fmaf(b1, m4[e], c1 * g);
+      v4[e] = fmaf(b2, v4[e], c2 * g * g);
+      p4[e] = stepped(p4[e], m4[e], v4[e], lr_wd, st);
+    }
+    store4(t.p, i, t.n, p4);
+    store4(m, i, t.n, m4);
+    store4(v, i, t.n, v4);
+    if (t.copy) store4(static_cast<__bf16*>(t.copy), i, t.n, p4);
+  }
+}
+
+// ------------------------------------------------------------ 8-bit moments
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t u) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) u = max(u, uint32_t(__shfl_xor(int(u), o)));
+  return u;
+}
+
+__device__ __forceinline__ double value_m(int c, double s) { return s * double(c * abs(c)); }
+__device__ __forceinline__ double value_v(int c, double s) {
+  const double r = s * double(c * c);
+  return r * r;
+}
+
+// The code of a = |m|: t = sqrt(a / s) in 32 bits is off by 3e-5 at most
+// (sqrt, conversion and 1/s, of values up to 127), so only within 1e-4 of a
+// border the 64-bit border itself decides.
+__device__ __forceinline__ int code_m(double a, double s, double inv) {
+  const float t = __builtin_amdgcn_sqrtf(float(a * inv));
+  const float f = floorf(t), r = t - f - 0.5f;
+  int c = int(f) + (r > 0.0f);
+  if (fabsf(r) < 1e-4f) {
+    const double b = double(f) + 0.5;
+    c = int(f) + (s * (b * b) < a);
+  }
+  return min(c, 127);
+}
+
+// As code_m; t = (v / s^2)^(1/4) is off by 7e-5 at most (values up to 255).
+__device__ __forceinline__ int code_v(double v, double s, double inv2) {
+  const float t = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(float(v * inv2)));
+  const float f = floorf(t), r = t - f - 0.5f;
+  int c = int(f) + (r > 0.0f);
+  if (fabsf(r) < 2e-4f) {
+    const double b = double(f) + 0.5, q = s * (b * b);
+    c = int(f) + (q * q < v);
+  }
+  return max(min(c, 255), int(v > 0.0));
+}
+
+// A wavefront per block of 256 elements, four consecutive ones a lane.  The
+// maxima are taken over the bit patterns of |m| and v (so a NaN wins): a
+// block that holds one reads back as NaN instead of losing it.
+__global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, const AdamArgs a) {
+  const Step st = step_of(a);
+  if (st.skip) return;
+  const int ti = tensor_of(l);
+  const ParamTensor t = l.t[ti];
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kAdamChunk;
+  const float lr_wd = st.lr * t.weight_decay;
+  const double scale = double(st.scale);
+  const double b1 = a.beta1, c1 = 1.0 - a.beta1, b2 = a.beta2, c2 = 1.0 - a.beta2;
+  uint8_t* mc = static_cast<uint8_t*>(t.m);
+  uint8_t* vc = static_cast<uint8_t*>(t.v);
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  for (int q = wv; q < kAdamChunk / kQBlock; q += kParamThreads / 64) {
+    const int64_t b0 = base + q * kQBlock;
+    if (b0 >= t.n) break;  // the whole wavefront
+    const int64_t i = b0 + lane * 4, blk = b0 / kQBlock;
+    float p4[4], g4[4];
+    load4(t.p, i, t.n, p4);
+    load4_grad(t, i, g4);
+    const uint32_t mw = load_codes(mc, i, t.n), vw = load_codes(vc, i, t.n);
+    const double sm = double(t.m_scale[blk]), sv = double(t.v_scale[blk]);
+    double m4[4], v4[4];
+    uint32_t am = 0, av = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double g = double(g4[e]) * scale;
+      m4[e] = fma(b1, value_m(int(int8_t(mw >> (8 * e))), sm), c1 * g);
+      v4[e] = fma(b2, value_v(int((vw >> (8 * e)) & 255u), sv), c2 * g * g);
+      const float mf = float(m4[e]), vf = float(v4[e]);
+      am = max(am, __float_as_uint(fabsf(mf)));
+      av = max(av, __float_as_uint(vf) & 0x7FFFFFFFu);
+      p4[e] = stepped(p4[e], mf, vf, lr_wd, st);
+    }
+    const float nm = float(double(__uint_as_float(wave_max(am))) * (1.0 / 16129.0));
+    const float nv = float(sqrt(double(__uint_as_float(wave_max(av)))) * (1.0 / 65025.0));
+    const double dm = double(nm), dv = double(nv);
+    const double im = dm > 0.0 ? 1.0 / dm : 0.0, iv = dv > 0.0 ? 1.0 / (dv * dv) : 0.0;
+    uint32_t mo = 0, vo = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = code_m(fabs(m4[e]), dm, im);
+      mo |= (uint32_t(m4[e] < 0.0 ? -c : c) & 255u) << (8 * e);
+      vo |= uint32_t(code_v(v4[e], dv, iv)) << (8 * e);
+    }
+    store4(t.p, i, t.n, p4);
+    store_codes(mc, i, t.n, mo);
+    store_codes(vc, i, t.n, vo);
+    if (t.copy) store4(static_cast<__bf16*>(t.copy), i, t.n, p4);
+    if (lane == 0) {
+      t.m_scale[blk] = nm;
+      t.v_scale[blk] = nv;
+    }
+  }
+}
+
+// The moments as float32: p and grad hold the destinations of m and v.
+__global__ void __launch_bounds__(kParamThreads) k_moments8(const ParamList l) {
+  const int ti = tensor_of(l);
+  const ParamTensor t = l.t[ti];
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kAdamChunk;
+  float* mo = t.p;
+  float* vo = static_cast<float*>(const_cast<void*>(t.grad));
+#pragma unroll
+  for (int it = 0; it < kAdamChunk / (4 * kParamThreads); ++it) {
+    const int64_t i = base + (it * kParamThreads + int(threadIdx.x)) * 4;
+    if (i >= t.n) break;
+    const uint32_t mw = load_codes(static_cast<const uint8_t*>(t.m), i, t.n);
+    const uint32_t vw = load_codes(static_cast<const uint8_t*>(t.v), i, t.n);
+    const double sm = double(t.m_scale[i / kQBlock]), sv = double(t.v_scale[i / kQBlock]);
+    float m4[4], v4[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m4[e] = float(value_m(int(int8_t(mw >> (8 * e))), sm));
+      v4[e] = float(value_v(int((vw >> (8 * e)) & 255u), sv));
+    }
+    store4(mo, i, t.n, m4);
+    store4(vo, i, t.n, v4);
+  }
+}
+
+// Calls f(list, workgroups) for runs of at most kParamsPerLaunch of the
+// tensors that `take` picks, empty ones left out.
+template <class P, class F>
+hipError_t for_lists(const ParamTensor* t, int n, int64_t chunk, P&& take, F&& f) {
+  ParamList l;
+  l.n = 0;
+  int64_t wgs = 0;
+  const auto flush = [&]() -> hipError_t {
+    if (l.n == 0) return hipSuccess;
+    const hipError_t e = f(static_cast<const ParamList&>(l), unsigned(wgs));
+    l.n = 0;
+    wgs = 0;
+    return e;
+  };
+  for (int i = 0; i < n; ++i) {
+    if (t[i].n == 0 || !take(t[i])) continue;
+    const int64_t w = (t[i].n + chunk - 1) / chunk;
+    if (l.n == kParamsPerLaunch || wgs + w > kMaxWorkgroups) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    l.t[l.n] = t[i];
+    l.wg0[l.n++] = int(wgs);
+    wgs += w;
+  }
+  return flush();
+}
+
+}  // namespace
+
+size_t grad_norm_partials(const ParamTensor* t, int n) {
+  size_t w = 0;
+  for (int i = 0; i < n; ++i) w += size_t((t[i].n + kNormChunk - 1) / kNormChunk);
+  return w;
+}
+
+hipError_t launch_grad_norm(const ParamTensor* t, int n, double max_norm, double* part, float* out,
+                            hipStream_t s) {
+  int64_t done = 0;
+  const hipError_t e = for_lists(
+      t, n, kNormChunk, [](const ParamTensor&) { return true; },
+      [&](const ParamList& l, unsigned wgs) {
+        hipLaunchKernelGGL(k_grad_norm, dim3(wgs), dim3(kParamThreads), 0, s, l, part + done);
+        done += wgs;
+        return hipGetLastError();
+      });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_grad_norm_total, dim3(1), dim3(1024), 0, s, done, part, max_norm, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw(const ParamTensor* t, int n, const AdamArgs& a, hipStream_t s) {
+  const hipError_t e = for_lists(
+      t, n, kAdamChunk, [](const ParamTensor& p) { return p.m_scale == nullptr; },
+      [&](const ParamList& l, unsigned wgs) {
+        hipLaunchKernelGGL(k_adamw, dim3(wgs), dim3(kParamThreads), 0, s, l, a);
+        return hipGetLastError();
+      });
+  if (e != hipSuccess) return e;
+  return for_lists(
+      t, n, kAdamChunk, [](const ParamTensor& p) { return p.m_scale != nullptr; },
+      [&](const ParamList& l, unsigned wgs) {
+        hipLaunchKernelGGL(k_adamw8, dim3(wgs), dim3(kParamThreads), 0, s, l, a);
+        return hipGetLastError();
+      });
+}
+
+hipError_t launch_moments8(const ParamTensor* t, int n, hipStream_t s) {
+  return for_lists(
+      t, n, kAdamChunk, [](const ParamTensor&) { return true; },
+      [&](const ParamList& l, unsigned wgs) {
+        hipLaunchKernelGGL(k_moments8, dim3(wgs), dim3(kParamThreads), 0, s, l);
+        return hipGetLastError();
+      });
+}
+
+}  // namespace e3k

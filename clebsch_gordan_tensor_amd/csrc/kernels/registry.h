@@ -361,6 +361,77 @@ struct LinearDwArgs {
 };
 hipError_t launch_linear_dw(const LinearDwArgs& a, int bf16, hipStream_t s);
 
+// Normalisation of irreps features (norm.hip).  blk: the irrep blocks of one
+// launch, each with its own workgroups [wg0, wg0 + n_wg).
+constexpr int kNormMaxBlocks = 64;
+constexpr int kNormMaxChannels = 4096;      // degrees up to 3
+constexpr int kNormMaxChannelsHigh = 1024;  // degrees 4 to 8
+struct NormBlock {
+  int comp0, nc;  // first component of the row, components (2l + 1)
+  int index;      // weight row
+  int bias;       // bias row, or -1
+  int centered;
+  int wg0, n_wg;
+};
+struct NormArgs {
+  int64_t n_rows;
+  int dim, C;    // components of a row, channels
+  int group;     // lanes of a team within a wavefront
+  int n_blocks;
+  const void* x;
+  const void* dy;
+  void* y;       // forward: y; backward: dx
+  const float* w;
+  const float* b;
+  float* dw;
+  float* db;
+  float* part;   // backward: [workgroup][dw, db][C]
+  float eps;
+  NormBlock blk[kNormMaxBlocks];
+};
+// floats of `part` that launch_norm's backward needs
+size_t norm_part_floats(int64_t n_rows, int C, const NormBlock* blocks, int n_blocks);
+hipError_t launch_norm(bool bwd, const NormArgs& a, const NormBlock* blocks, int n_blocks,
+                       int bf16, hipStream_t s);
+
+// Lists of parameter tensors (optimizer.hip), passed in the kernel arguments
+// (4 KB at most).
+struct ParamTensor {
+  int64_t n;
+  float* p;
+  const void* grad;
+  void* m;        // float32, or int8 codes where m_scale is given
+  void* v;        // float32, or uint8 codes
+  float* m_scale;
+  float* v_scale;
+  void* copy;     // bf16 copy of p, or null
+  float weight_decay;
+  int grad_bf16;
+};
+constexpr int kParamsPerLaunch = 48;
+constexpr int kNormChunk = 16384;  // elements of a workgroup of the gradients' norm
+constexpr int kAdamChunk = 4096;   // of the step
+constexpr int64_t kMaxParamElements = int64_t(1) << 35;
+struct ParamList {
+  int n;
+  int wg0[kParamsPerLaunch];  // first workgroup of each tensor
+  ParamTensor t[kParamsPerLaunch];
+};
+struct AdamArgs {
+  double lr, beta1, beta2;
+  int64_t step;
+  float lr_f, size, inv_c2, eps;  // lr, lr / (1 - beta1^step), 1 / (1 - beta2^step)
+  const int64_t* step_dev;        // device values in place of step and lr, or null
+  const float* lr_dev;
+  const float* grad_scale;        // device factor of the gradients, or null
+  int skip_nonfinite;
+};
+size_t grad_norm_partials(const ParamTensor* t, int n);
+hipError_t launch_grad_norm(const ParamTensor* t, int n, double max_norm, double* part, float* out,
+                            hipStream_t s);
+hipError_t launch_adamw(const ParamTensor* t, int n, const AdamArgs& a, hipStream_t s);
+hipError_t launch_moments8(const ParamTensor* t, int n, hipStream_t s);
+
 // Workspace layout of the transposed edge index (int32 words).
 struct TransposeLayout {
   int64_t npad, colptr, cursor, tmp_e, tmp_b, perm, recv, padlist, order, flag, pos, key, order2,

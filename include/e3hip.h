@@ -588,6 +588,123 @@ e3_status e3_linear_backward(const e3_irreps* in, const e3_irreps* out, int64_t 
                              const void* x, const float* W, const void* dy, void* dx, float* dW,
                              void* workspace, size_t ws_bytes, e3_dtype dtype, void* stream);
 
+/* Normalisation of irreps features (a layer norm that commutes with rotations
+ * and inversion, next to e3_linear), and its gradients.  For every row r and
+ * block i of `irreps` (degree l, K = (2l+1) C values x[r][i, m][k]):
+ *   xc   = x - (mean over the channels)  for 0e blocks, x for the others (no
+ *          other block has a mean that a rotation or the inversion leaves)
+ *   rstd = 1 / sqrt(sum_{m,k} xc^2 / K + eps)
+ *   y    = xc rstd weight[i][k] (+ bias[j][k] for the j-th 0e block)
+ * A list of one 0e block is the ordinary layer norm over C channels; with
+ * E3_NORM_UNCENTERED 0e blocks keep their mean (root-mean-square norm).
+ * x, y [n_rows][dim][C] in the storage type, every block of multiplicity C;
+ * weight [n_blocks][C] and bias [number of 0e blocks][C] float32, either may
+ * be NULL (1 and 0).  Statistics and products in float32, one rounding to
+ * the storage type.  C up to 4096 (1024 when a degree is above 3), degrees up
+ * to 8, at most 1024 blocks; eps > 0; pointers aligned to their element.
+ * y may be x, but must not overlap it otherwise.  A row that holds an
+ * infinity or NaN gives NaN in that block and leaves the others alone. */
+enum { E3_NORM_UNCENTERED = 1 };
+e3_status e3_layer_norm(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                        const float* weight, const float* bias, float eps, int32_t flags, void* y,
+                        e3_dtype dtype, void* stream);
+
+/* Bytes of the workspace of e3_layer_norm_backward (partial sums of the
+ * weight's and bias's gradients; at most 8 KB per channel; host only). */
+e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, size_t* bytes);
+
+/* Backward of e3_layer_norm for the cotangent dy [n_rows][dim][C]; the
+ * statistics are formed again from x (nothing is kept from the forward).
+ * With xh = xc rstd and g = dy weight[i][k]:
+ *   dx = rstd (g - [mean_k g, centred 0e blocks] - xh mean_{m,k}(g xh))
+ *   dweight[i][k] = sum_{r,m} dy xh      dbias[j][k] = sum_r dy   (float32)
+ * dweight and dbias (either may be NULL: not wanted) are summed through fixed
+ * partials in the caller's workspace (e3_layer_norm_workspace_size bytes,
+ * 16-byte aligned): reproducible.  weight NULL: 1.  dx may be x or dy, but
+ * must not overlap them otherwise.  n_rows = 0 gives zero dweight and dbias.
+ * Limits and alignment as the forward. */
+e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                                 const float* weight, const void* dy, float eps, int32_t flags,
+                                 void* dx, float* dweight, float* dbias, void* workspace,
+                                 size_t ws_bytes, e3_dtype dtype, void* stream);
+
+/* One tensor of a network's weights with what its update reads and writes:
+ * the optimizer calls take a HOST array of at most 65536 of these (device
+ * pointers inside; read during the call only).  Every pointer needs its element's alignment.
+ * Moments are float32, or, where m_scale and v_scale are given, 8-bit codes:
+ * every 256 consecutive elements (the last run may be shorter) share a scale,
+ *   m[i] = m_scale[i/256] c |c|,  c int8 in [-127, 127],
+ *   v[i] = (v_scale[i/256] c^2)^2, c uint8 in [0, 255].
+ * All-zero codes and scales are zero moments. */
+typedef struct {
+  int64_t n;          /* elements, 0 <= n <= 2^35; an empty tensor is left out */
+  float* p;           /* [n] the weights */
+  const void* grad;   /* [n] their gradient, of type grad_dtype */
+  void* m;            /* [n] first moment: float32, or int8 codes */
+  void* v;            /* [n] second moment: float32, or uint8 codes */
+  float* m_scale;     /* [ceil(n/256)], both or neither */
+  float* v_scale;
+  void* p_bf16;       /* [n] bf16 copy of the updated weights, or NULL */
+  float weight_decay;
+  e3_dtype grad_dtype;
+} e3_param;
+
+/* Host-only check of a list, once where a program makes it: sizes, pointers
+ * and alignment of every tensor (as e3_adamw checks them) and that nothing
+ * written (p, m, v, scales, bf16 copies) overlaps anything else of the list.
+ * E3_OK, E3_ERR_INVALID_ARG or E3_ERR_ALIGNMENT (e3_last_error names the
+ * tensor). */
+e3_status e3_param_check(int32_t n_params, const e3_param* params);
+
+/* The 2-norm of all gradients of a list taken together and the factor that
+ * clips it: out[0] = norm, out[1] = min(1, max_norm / (norm + 1e-6)), float32
+ * on the device (for e3_adamw's grad_scale: no synchronisation).  Squares and
+ * sums in 64 bits, through fixed partials in the caller's workspace
+ * (e3_grad_norm_workspace_size bytes, 8-byte aligned): reproducible.
+ * max_norm > 0 (INFINITY: never clips).  A norm that is not finite gives the
+ * factor NaN.  Only n, grad and grad_dtype of the tensors are used. */
+e3_status e3_grad_norm_workspace_size(int32_t n_params, const e3_param* params, size_t* bytes);
+e3_status e3_grad_norm(int32_t n_params, const e3_param* params, double max_norm, float* out,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/* One AdamW step over a list of tensors (a launch for every 48 of them and
+ * form of the moments), for the gradients of e3_linear_backward,
+ * e3_radial_mlp_backward, e3_layer_norm_backward:
+ *   g = s grad                                (s = *grad_scale, or 1)
+ *   m = beta1 m + (1 - beta1) g               v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr weight_decay p
+ *         - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * p is updated from the moments before these are rounded to 8 bits.  Float32
+ * moments: float32 arithmetic.  8-bit moments: moments and codes in 64 bits;
+ * new scales m_scale = max|m| / 127^2 and v_scale = sqrt(max v) / 255^2 per
+ * run; a code is the number of borders m_scale (k+1/2)^2, or
+ * (v_scale (k+1/2)^2)^2, k = 0, 1, ..., below the value (at most 127, 255),
+ * at least 1 for v > 0.  A run that meets a moment that is not finite in
+ * float32 reads back as NaN.
+ * args: step t >= 1 and lr from the host, or from the device (step_dev, an
+ * int64 taken as 1 where it is less; lr_dev, a float), so that a captured
+ * step can be replayed.  E3_ADAMW_SKIP_NONFINITE (needs grad_scale): nothing
+ * is changed when *grad_scale is not finite, as e3_grad_norm's factor is for
+ * a norm that is not.
+ * The tensors must pass e3_param_check; overlap is not checked again. */
+enum { E3_ADAMW_SKIP_NONFINITE = 1 };
+typedef struct {
+  double lr, beta1, beta2, eps; /* lr finite; 0 <= beta < 1; eps > 0 */
+  int64_t step;                 /* t, 1 for the first update */
+  const int64_t* step_dev;      /* device, or NULL */
+  const float* lr_dev;          /* device, or NULL */
+  const float* grad_scale;      /* device, or NULL */
+  int32_t flags;
+} e3_adamw_args;
+e3_status e3_adamw(int32_t n_params, const e3_param* params, const e3_adamw_args* args,
+                   void* stream);
+
+/* 8-bit moments as float32 (for inspection, checkpoints, another optimizer):
+ * m_out[i] and v_out[i] (HOST arrays of device pointers, float32 [n]) of
+ * tensor i, whose moments must be codes. */
+e3_status e3_adamw_moments(int32_t n_params, const e3_param* params, float* const* m_out,
+                           float* const* v_out, void* stream);
+
 /* Text of the last error on this thread ("" if none). */
 const char* e3_last_error(void);
 
