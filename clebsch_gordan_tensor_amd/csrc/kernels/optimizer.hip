@@ -36,6 +36,7 @@ typedef uint32_t u32u __attribute__((aligned(1)));
 
 constexpr int kParamThreads = 256;
 constexpr int kQBlock = 256;  // elements per scale
+constexpr int kPass = 4 * kParamThreads;  // elements a workgroup takes at once
 constexpr int64_t kMaxWorkgroups = (int64_t(1) << 32) / kParamThreads - 1;  // 2^32 threads a launch
 static_assert(sizeof(ParamList) + sizeof(AdamArgs) <= 4096, "kernel arguments");
 static_assert(kMaxParamElements / kAdamChunk < kMaxWorkgroups);
@@ -104,10 +105,13 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, ui
     if (i + e < n) p[i + e] = uint8_t(w >> (8 * e));
 }
 
+// The tensor this workgroup belongs to: a lane per tensor compares, one load
+// deep (walking the list took 0.1 us a tensor).
 __device__ __forceinline__ int tensor_of(const ParamList& l) {
-  int i = 0;
-  while (i + 1 < l.n && int(blockIdx.x) >= l.wg0[i + 1]) ++i;
-  return i;
+  static_assert(kParamsPerLaunch <= 64);
+  const int lane = threadIdx.x & 63;
+  const bool below = lane < l.n && l.wg0[min(lane, kParamsPerLaunch - 1)] <= int(blockIdx.x);
+  return __popcll(__ballot(below)) - 1;
 }
 
 // ------------------------------------------------------- the gradients' norm
@@ -118,23 +122,43 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return v;
 }
 
+// A thread's part of the squares of elements [base, end): four vectors of 16
+// bytes at a time, all asked for before the first is added.
+template <class T>
+__device__ __forceinline__ double sum_squares(const T* p, int64_t base, int64_t end) {
+  constexpr int V = 16 / sizeof(T);
+  double s[2] = {0.0, 0.0};
+  for (int64_t i0 = base + int(threadIdx.x) * V; i0 < end; i0 += 4 * V * kParamThreads) {
+    float g[4][V];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t i = i0 + j * V * kParamThreads;
+#pragma unroll
+      for (int h = 0; h < V; h += 4) {
+        float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (i + h < end) load4(p, i + h, end, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[j][h + e] = q[e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e & 1] = fma(double(g[j][e]), double(g[j][e]), s[e & 1]);
+  }
+  return s[0] + s[1];
+}
+
 // One partial per workgroup; squares and sums in 64 bits, so no gradient of
 // float32's range overflows and the order of summation does not show.
 __global__ void __launch_bounds__(kParamThreads) k_grad_norm(const ParamList l, double* part) {
   __shared__ double s_sum[kParamThreads / 64];
   const int ti = tensor_of(l);
   const ParamTensor t = l.t[ti];
-  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kNormChunk;
-  double s = 0.0;
-#pragma unroll
-  for (int it = 0; it < kNormChunk / (4 * kParamThreads); ++it) {
-    const int64_t i = base + (it * kParamThreads + int(threadIdx.x)) * 4;
-    if (i >= t.n) break;
-    float g[4];
-    load4_grad(t, i, g);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s = fma(double(g[e]), double(g[e]), s);
-  }
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * l.chunk;
+  const int64_t end = min(t.n, base + l.chunk);
+  double s = t.grad_bf16 ? sum_squares(static_cast<const __bf16*>(t.grad), base, end)
+                         : sum_squares(static_cast<const float*>(t.grad), base, end);
   s = wave_sum64(s);
   if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -204,16 +228,14 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw(const ParamList l, cons
   if (st.skip) return;
   const int ti = tensor_of(l);
   const ParamTensor t = l.t[ti];
-  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kAdamChunk;
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * l.chunk;
+  const int64_t end = min(t.n, base + l.chunk);
   const float lr_wd = st.lr * t.weight_decay;
   const float b1 = float(a.beta1), c1 = float(1.0 - a.beta1);
   const float b2 = float(a.beta2), c2 = float(1.0 - a.beta2);
   float* m = static_cast<float*>(t.m);
   float* v = static_cast<float*>(t.v);
-#pragma unroll
-  for (int it = 0; it < kAdamChunk / (4 * kParamThreads); ++it) {
-    const int64_t i = base + (it * kParamThreads + int(threadIdx.x)) * 4;
-    if (i >= t.n) break;
+  for (int64_t i = base + int(threadIdx.x) * 4; i < end; i += 4 * kParamThreads) {
     float p4[4], g4[4], m4[4], v4[4];
     load4(t.p, i, t.n, p4);
     load4_grad(t, i, g4);
@@ -281,16 +303,15 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, con
   if (st.skip) return;
   const int ti = tensor_of(l);
   const ParamTensor t = l.t[ti];
-  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kAdamChunk;
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * l.chunk;
+  const int64_t end = min(t.n, base + l.chunk);
   const float lr_wd = st.lr * t.weight_decay;
   const double scale = double(st.scale);
   const double b1 = a.beta1, c1 = 1.0 - a.beta1, b2 = a.beta2, c2 = 1.0 - a.beta2;
   uint8_t* mc = static_cast<uint8_t*>(t.m);
   uint8_t* vc = static_cast<uint8_t*>(t.v);
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int q = wv; q < kAdamChunk / kQBlock; q += kParamThreads / 64) {
-    const int64_t b0 = base + q * kQBlock;
-    if (b0 >= t.n) break;  // the whole wavefront
+  for (int64_t b0 = base + wv * kQBlock; b0 < end; b0 += kParamThreads / 64 * kQBlock) {
     const int64_t i = b0 + lane * 4, blk = b0 / kQBlock;
     float p4[4], g4[4];
     load4(t.p, i, t.n, p4);
@@ -335,13 +356,11 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, con
 __global__ void __launch_bounds__(kParamThreads) k_moments8(const ParamList l) {
   const int ti = tensor_of(l);
   const ParamTensor t = l.t[ti];
-  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * kAdamChunk;
+  const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * l.chunk;
+  const int64_t end = min(t.n, base + l.chunk);
   float* mo = t.p;
   float* vo = static_cast<float*>(const_cast<void*>(t.grad));
-#pragma unroll
-  for (int it = 0; it < kAdamChunk / (4 * kParamThreads); ++it) {
-    const int64_t i = base + (it * kParamThreads + int(threadIdx.x)) * 4;
-    if (i >= t.n) break;
+  for (int64_t i = base + int(threadIdx.x) * 4; i < end; i += 4 * kParamThreads) {
     const uint32_t mw = load_codes(static_cast<const uint8_t*>(t.m), i, t.n);
     const uint32_t vw = load_codes(static_cast<const uint8_t*>(t.v), i, t.n);
     const double sm = double(t.m_scale[i / kQBlock]), sv = double(t.v_scale[i / kQBlock]);
@@ -356,12 +375,22 @@ __global__ void __launch_bounds__(kParamThreads) k_moments8(const ParamList l) {
   }
 }
 
+// Elements of a workgroup: one pass of its threads while that does not fill the
+// card (2048 workgroups), up to `most` for long lists.
+int64_t chunk_of(const ParamTensor* t, int n, int64_t pass, int64_t most) {
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) total += t[i].n;
+  const int64_t even = (total + 2048 * pass - 1) / (2048 * pass) * pass;
+  return std::clamp(even, pass, most);
+}
+
 // Calls f(list, workgroups) for runs of at most kParamsPerLaunch of the
 // tensors that `take` picks, empty ones left out.
 template <class P, class F>
 hipError_t for_lists(const ParamTensor* t, int n, int64_t chunk, P&& take, F&& f) {
   ParamList l;
   l.n = 0;
+  l.chunk = int(chunk);
   int64_t wgs = 0;
   const auto flush = [&]() -> hipError_t {
     if (l.n == 0) return hipSuccess;
@@ -387,8 +416,9 @@ hipError_t for_lists(const ParamTensor* t, int n, int64_t chunk, P&& take, F&& f
 }  // namespace
 
 size_t grad_norm_partials(const ParamTensor* t, int n) {
+  const int64_t chunk = chunk_of(t, n, kPass, kNormChunk);
   size_t w = 0;
-  for (int i = 0; i < n; ++i) w += size_t((t[i].n + kNormChunk - 1) / kNormChunk);
+  for (int i = 0; i < n; ++i) w += size_t((t[i].n + chunk - 1) / chunk);
   return w;
 }
 
@@ -396,7 +426,7 @@ hipError_t launch_grad_norm(const ParamTensor* t, int n, double max_norm, double
                             hipStream_t s) {
   int64_t done = 0;
   const hipError_t e = for_lists(
-      t, n, kNormChunk, [](const ParamTensor&) { return true; },
+      t, n, chunk_of(t, n, kPass, kNormChunk), [](const ParamTensor&) { return true; },
       [&](const ParamList& l, unsigned wgs) {
         hipLaunchKernelGGL(k_grad_norm, dim3(wgs), dim3(kParamThreads), 0, s, l, part + done);
         done += wgs;
@@ -408,15 +438,16 @@ hipError_t launch_grad_norm(const ParamTensor* t, int n, double max_norm, double
 }
 
 hipError_t launch_adamw(const ParamTensor* t, int n, const AdamArgs& a, hipStream_t s) {
+  const int64_t chunk = chunk_of(t, n, kPass, kAdamChunk);
   const hipError_t e = for_lists(
-      t, n, kAdamChunk, [](const ParamTensor& p) { return p.m_scale == nullptr; },
+      t, n, chunk, [](const ParamTensor& p) { return p.m_scale == nullptr; },
       [&](const ParamList& l, unsigned wgs) {
         hipLaunchKernelGGL(k_adamw, dim3(wgs), dim3(kParamThreads), 0, s, l, a);
         return hipGetLastError();
       });
   if (e != hipSuccess) return e;
   return for_lists(
-      t, n, kAdamChunk, [](const ParamTensor& p) { return p.m_scale != nullptr; },
+      t, n, chunk, [](const ParamTensor& p) { return p.m_scale != nullptr; },
       [&](const ParamList& l, unsigned wgs) {
         hipLaunchKernelGGL(k_adamw8, dim3(wgs), dim3(kParamThreads), 0, s, l, a);
         return hipGetLastError();
@@ -425,7 +456,7 @@ hipError_t launch_adamw(const ParamTensor* t, int n, const AdamArgs& a, hipStrea
 
 hipError_t launch_moments8(const ParamTensor* t, int n, hipStream_t s) {
   return for_lists(
-      t, n, kAdamChunk, [](const ParamTensor&) { return true; },
+      t, n, chunk_of(t, n, kPass, kAdamChunk), [](const ParamTensor&) { return true; },
       [&](const ParamList& l, unsigned wgs) {
         hipLaunchKernelGGL(k_moments8, dim3(wgs), dim3(kParamThreads), 0, s, l);
         return hipGetLastError();

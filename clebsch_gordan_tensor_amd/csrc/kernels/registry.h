@@ -409,11 +409,11 @@ struct ParamTensor {
   int grad_bf16;
 };
 constexpr int kParamsPerLaunch = 48;
-constexpr int kNormChunk = 16384;  // elements of a workgroup of the gradients' norm
-constexpr int kAdamChunk = 4096;   // of the step
+constexpr int kNormChunk = 16384;  // most elements of a workgroup of the gradients' norm
+constexpr int kAdamChunk = 4096;   // and of the step
 constexpr int64_t kMaxParamElements = int64_t(1) << 35;
 struct ParamList {
-  int n;
+  int n, chunk;  // tensors, elements of a workgroup
   int wg0[kParamsPerLaunch];  // first workgroup of each tensor
   ParamTensor t[kParamsPerLaunch];
 };
