@@ -2449,7 +2449,7 @@ e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, 
   const e3_status s = parse_norm(irreps, n_rows, 0, n);
   if (s != E3_OK) return s;
   if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
-  *bytes = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), int(n.blocks.size()));
+  *bytes = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), int(n.blocks.size()), 4);
   return ok();
 }
 
@@ -2462,7 +2462,7 @@ e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const 
   if ((s = parse_norm(irreps, n_rows, flags, n)) != E3_OK || (s = norm_args(eps, dtype)) != E3_OK)
     return s;
   const int nb = int(n.blocks.size());
-  const size_t need = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), nb);
+  const size_t need = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), nb, 4);
   if (!workspace || ws_bytes < need)
     return fail(E3_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   if (n_rows > 0 && (!x || !dy || !dx)) return fail(E3_ERR_INVALID_ARG, "null pointer");

@@ -38,8 +38,8 @@ __device__ __forceinline__ void load_vec(const T* p, float (&v)[V]) {
   } else {
     static_assert(V == 4);
     rf4 t;
-    if constexpr (std::is_same_v<T, float>) t = *reinterpret_cast<const nf4*>(p);
-    else t = __builtin_convertvector(*reinterpret_cast<const nb4*>(p), rf4);
+    if constexpr (std::is_same_v<T, float>) t = __builtin_nontemporal_load(reinterpret_cast<const nf4*>(p));
+    else t = __builtin_convertvector(__builtin_nontemporal_load(reinterpret_cast<const nb4*>(p)), rf4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = t[i];
   }
@@ -52,10 +52,14 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V]) {
     else *reinterpret_cast<__bf16*>(p) = __bf16(v[0]);
   } else {
     const rf4 t = {v[0], v[1], v[2], v[3]};
-    if constexpr (std::is_same_v<T, float>) *reinterpret_cast<nf4*>(p) = t;
-    else *reinterpret_cast<nb4*>(p) = __builtin_convertvector(t, nb4);
+    if constexpr (std::is_same_v<T, float>)
+      __builtin_nontemporal_store(nf4(t), reinterpret_cast<nf4*>(p));
+    else
+      __builtin_nontemporal_store(__builtin_convertvector(t, nb4), reinterpret_cast<nb4*>(p));
   }
 }
+
+constexpr int kNormThreads = 256;
 
 // Sums of N values over a team; every lane of the team gets them.  Teams of
 // at most 64 lanes (TEAM == 64: g of them, a power of two) lie in one
@@ -82,6 +86,7 @@ __device__ __forceinline__ void wave_team_sum(float (&v)[N], int g) {
   }
 }
 
+constexpr int kTeamSums = 6;  // sums at once, at most
 template <int TEAM, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], int g, float* lds, int& phase) {
   if constexpr (TEAM == 64) {
@@ -89,179 +94,262 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int g, float* lds, int& 
   } else {
     constexpr int W = TEAM / 64;
     wave_team_sum(v, 64);
-    float* buf = lds + phase * (W * 4);
+    static_assert(N <= kTeamSums);
+    float* buf = lds + phase * (W * kTeamSums);
     phase ^= 1;
     const int w = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) buf[w * 4 + i] = v[i];
+      for (int i = 0; i < N; ++i) buf[w * kTeamSums + i] = v[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float s = 0.0f;
-      for (int j = 0; j < W; ++j) s += buf[j * 4 + i];
+      for (int j = 0; j < W; ++j) s += buf[j * kTeamSums + i];
       v[i] = s;
     }
   }
 }
 
-// What a lane owns: V channels from k0, of which the first `skip` belong to
-// its neighbour (the last vector is moved back inside the row when C is no
-// multiple of V) and count as zero.
+// What a lane owns of a component row: K vectors of V channels, vector i from
+// channel k0[i]; the first skip[i] of them belong to a neighbour (the row's
+// last vector is moved back inside the row when C is no multiple of V, and
+// vectors past it altogether) and count as zero.
+template <int V, int K>
 struct Lane {
-  int k0, skip;
-};
-template <int V>
-__device__ __forceinline__ Lane lane_of(int q, int C) {
-  const int k = q * V;
-  const int skip = max(0, k - (C - V));
-  return {k - skip, skip};
-}
-
-template <class T, int V, int NC>
-__device__ __forceinline__ void load_segment(const T* p, int C, int skip, bool valid,
-                                             float (&x)[NC][V]) {
+  int k0[K], skip[K];
+  __device__ __forceinline__ Lane(int q, int g, int C) {
 #pragma unroll
-  for (int c = 0; c < NC; ++c) load_vec<T, V>(p + c * C, x[c]);
+    for (int i = 0; i < K; ++i) {
+      const int k = (q + i * g) * V;
+      skip[i] = max(0, k - (C - V));
+      k0[i] = k - skip[i];
+    }
+  }
+};
+
+template <class T, int V, int K, int NC>
+__device__ __forceinline__ void load_segment(const T* p, int C, const Lane<V, K>& ln,
+                                             float (&x)[NC][K][V]) {
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[c][v] = valid && v >= skip ? x[c][v] : 0.0f;
+    for (int i = 0; i < K; ++i) load_vec<T, V>(p + c * C + ln.k0[i], x[c][i]);
 }
-
-// x becomes xc; the sum over the segment's centred values' squares comes from
-// the caller's second reduction.
-template <int TEAM, int V>
-__device__ __forceinline__ void center(float (&x)[1][V], int C, int skip, int g, float* lds,
-                                       int& phase) {
-  float s[1] = {0.0f};
+template <int V, int K, int NC>
+__device__ __forceinline__ void clear_others(float (&x)[NC][K][V], const Lane<V, K>& ln,
+                                             bool valid) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) s[0] += x[0][v];
-  team_sum<TEAM>(s, g, lds, phase);
-  const float mu = s[0] / float(C);
+  for (int c = 0; c < NC; ++c)
 #pragma unroll
-  for (int v = 0; v < V; ++v) x[0][v] = v >= skip ? x[0][v] - mu : 0.0f;
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[c][i][v] = valid && v >= ln.skip[i] ? x[c][i][v] : 0.0f;
 }
-
-template <int TEAM>
-struct Team {
-  static constexpr int kThreads = TEAM == 64 ? 256 : TEAM;
-};
-
-template <class T, int V, int TEAM, int NC>
-__device__ __forceinline__ void fwd_rows(const NormArgs& a, const NormBlock& b, int wg, float* lds) {
-  const int g = TEAM == 64 ? a.group : TEAM;
-  const int teams = Team<TEAM>::kThreads / g;
-  const int team = int(threadIdx.x) / g;
-  const Lane ln = lane_of<V>(int(threadIdx.x) % g, a.C);
-  float w[V], bias[V];
+template <class T, int V, int K, int NC>
+__device__ __forceinline__ void store_segment(T* p, int C, const Lane<V, K>& ln,
+                                              const float (&o)[NC][K][V]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) w[v] = 1.0f, bias[v] = 0.0f;
-  if (a.w) load_vec<float, V>(a.w + int64_t(b.index) * a.C + ln.k0, w);
-  if (a.b && b.bias >= 0) load_vec<float, V>(a.b + int64_t(b.bias) * a.C + ln.k0, bias);
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.y);
-  int phase = 0;
-  for (int64_t r0 = int64_t(wg) * teams; r0 < a.n_rows; r0 += int64_t(b.n_wg) * teams) {
-    const bool valid = r0 + team < a.n_rows;
-    const int64_t row = valid ? r0 + team : r0;
-    const int64_t at = (row * a.dim + b.comp0) * a.C + ln.k0;
-    float xs[NC][V];
-    load_segment<T, V, NC>(x + at, a.C, ln.skip, valid, xs);
-    if constexpr (NC == 1)
-      if (b.centered) center<TEAM, V>(xs, a.C, ln.skip, g, lds, phase);
-    float s[1] = {0.0f};
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int v = 0; v < V; ++v) s[0] += xs[c][v] * xs[c][v];
-    team_sum<TEAM>(s, g, lds, phase);
-    const float rstd = 1.0f / sqrtf(s[0] / float(NC * a.C) + a.eps);
-    if (valid && ln.skip < V) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(xs[c][v] * rstd, w[v], bias[v]);
-        if (ln.skip == 0) {
-          store_vec<T, V>(y + at + c * a.C, o);
-        } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (v >= ln.skip) {
-              const float one[1] = {o[v]};
-              store_vec<T, 1>(y + at + c * a.C + v, one);
-            }
-        }
-      }
-    }
-  }
-}
-
-template <class T, int V, int TEAM, int NC>
-__device__ __forceinline__ void bwd_rows(const NormArgs& a, const NormBlock& b, int wg, float* lds,
-                                         float (&aw)[V], float (&ab)[V]) {
-  const int g = TEAM == 64 ? a.group : TEAM;
-  const int teams = Team<TEAM>::kThreads / g;
-  const int team = int(threadIdx.x) / g;
-  const Lane ln = lane_of<V>(int(threadIdx.x) % g, a.C);
-  float w[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) w[v] = 1.0f;
-  if (a.w) load_vec<float, V>(a.w + int64_t(b.index) * a.C + ln.k0, w);
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  T* dx = static_cast<T*>(a.y);
-  const float inv = 1.0f / float(NC * a.C);
-  int phase = 0;
-  for (int64_t r0 = int64_t(wg) * teams; r0 < a.n_rows; r0 += int64_t(b.n_wg) * teams) {
-    const bool valid = r0 + team < a.n_rows;
-    const int64_t row = valid ? r0 + team : r0;
-    const int64_t at = (row * a.dim + b.comp0) * a.C + ln.k0;
-    float xs[NC][V], d[NC][V];
-    load_segment<T, V, NC>(x + at, a.C, ln.skip, valid, xs);
-    load_segment<T, V, NC>(dy + at, a.C, ln.skip, valid, d);
-    if constexpr (NC == 1)
-      if (b.centered) center<TEAM, V>(xs, a.C, ln.skip, g, lds, phase);
-    float s[3] = {0.0f, 0.0f, 0.0f};  // of xc^2, g xc, g
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float gv = d[c][v] * w[v];
-        s[0] += xs[c][v] * xs[c][v];
-        s[1] += gv * xs[c][v];
-        if (NC == 1) s[2] += gv;
-      }
-    team_sum<TEAM>(s, g, lds, phase);
-    const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
-    const float along = s[1] * inv * rstd;
-    const float mg = NC == 1 && b.centered ? s[2] * inv : 0.0f;
+  for (int i = 0; i < K; ++i) {
+    if (ln.skip[i] >= V) continue;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      float o[V];
+      T* at = p + c * C + ln.k0[i];
+      if (ln.skip[i] == 0) {
+        store_vec<T, V>(at, o[c][i]);
+      } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float xh = xs[c][v] * rstd;
-        aw[v] = fmaf(d[c][v], xh, aw[v]);
-        if (NC == 1) ab[v] += d[c][v];
-        o[v] = rstd * (d[c][v] * w[v] - mg - xh * along);
-      }
-      if (valid && ln.skip < V) {
-        if (ln.skip == 0) {
-          store_vec<T, V>(dx + at + c * a.C, o);
-        } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (v >= ln.skip) {
-              const float one[1] = {o[v]};
-              store_vec<T, 1>(dx + at + c * a.C + v, one);
-            }
-        }
+        for (int v = 0; v < V; ++v)
+          if (v >= ln.skip[i]) {
+            const float one[1] = {o[c][i][v]};
+            store_vec<T, 1>(at + v, one);
+          }
       }
     }
   }
+}
+// A row of per-channel float32 weights; `other` where there are none.
+template <int V, int K>
+__device__ __forceinline__ void load_weights(const float* p, const Lane<V, K>& ln, float other,
+                                             float (&w)[K][V]) {
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[i][v] = p ? p[ln.k0[i] + v] : other;
+}
+
+// Rows a team takes at once: of scalars two, so that their loads are under way
+// together and their sums share the joining steps.
+constexpr int rows_at_once(int nc, int k) { return nc == 1 && k == 1 ? 2 : 1; }
+
+// x becomes xc (one component row a segment).
+template <int TEAM, int V, int K, int U>
+__device__ __forceinline__ void center(float (&x)[U][1][K][V], float inv, const Lane<V, K>& ln,
+                                       int g, float* lds, int& phase) {
+  float s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    s[u] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[u] += x[u][0][i][v];
+  }
+  team_sum<TEAM>(s, g, lds, phase);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float mu = s[u] * inv;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[u][0][i][v] = v >= ln.skip[i] ? x[u][0][i][v] - mu : 0.0f;
+  }
+}
+
+// The rows a team takes at once; those past the end repeat the last one, not
+// valid.  (Asking for the next rows before these are reduced changed nothing
+// beyond 3% either way, forward or backward.)
+template <int U>
+struct Rows {
+  int64_t at[U];
+  bool valid[U];
+  __device__ __forceinline__ Rows(int64_t r0, int teams, int team, int64_t n) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at[u] = r0 + u * teams + team;
+      valid[u] = at[u] < n;
+      at[u] = valid[u] ? at[u] : n - 1;
+    }
+  }
+};
+// Calls f(rows) over the rows of this workgroup.
+template <int U, class F>
+__device__ __forceinline__ void for_rows(const NormArgs& a, const NormBlock& b, int wg, int teams,
+                                         int team, F&& f) {
+  const int64_t step = int64_t(teams) * U;
+  for (int64_t r0 = wg * step; r0 < a.n_rows; r0 += b.n_wg * step)
+    f(Rows<U>(r0, teams, team, a.n_rows));
+}
+
+template <class T, int V, int K, int TEAM, int NC>
+__device__ __forceinline__ void fwd_rows(const NormArgs& a, const NormBlock& b, int wg, float* lds) {
+  constexpr int U = rows_at_once(NC, K);
+  const int g = TEAM == 64 ? a.group : TEAM;
+  const int teams = kNormThreads / g;
+  const Lane<V, K> ln(int(threadIdx.x) % g, g, a.C);
+  float w[K][V], bias[K][V];
+  load_weights(a.w ? a.w + int64_t(b.index) * a.C : nullptr, ln, 1.0f, w);
+  load_weights(a.b && b.bias >= 0 ? a.b + int64_t(b.bias) * a.C : nullptr, ln, 0.0f, bias);
+  const T* x = static_cast<const T*>(a.x) + int64_t(b.comp0) * a.C;
+  T* y = static_cast<T*>(a.y) + int64_t(b.comp0) * a.C;
+  const int64_t ld = int64_t(a.dim) * a.C;
+  const float inv = 1.0f / float(NC * a.C);
+  int phase = 0;
+  for_rows<U>(a, b, wg, teams, int(threadIdx.x) / g, [&](const Rows<U>& r) {
+    float xs[U][NC][K][V], s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_segment<T>(x + r.at[u] * ld, a.C, ln, xs[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) clear_others(xs[u], ln, true);
+    if constexpr (NC == 1)
+      if (b.centered) center<TEAM>(xs, inv, ln, g, lds, phase);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s[u] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) s[u] += xs[u][c][i][v] * xs[u][c][i][v];
+    }
+    team_sum<TEAM>(s, g, lds, phase);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float rstd = 1.0f / sqrtf(s[u] * inv + a.eps);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            xs[u][c][i][v] = fmaf(xs[u][c][i][v] * rstd, w[i][v], bias[i][v]);
+      if (r.valid[u]) store_segment<T>(y + r.at[u] * ld, a.C, ln, xs[u]);
+    }
+  });
+}
+
+template <class T, int V, int K, int TEAM, int NC>
+__device__ __forceinline__ void bwd_rows(const NormArgs& a, const NormBlock& b, int wg, float* lds,
+                                         float (&aw)[K][V], float (&ab)[K][V]) {
+  constexpr int U = rows_at_once(NC, K);
+  const int g = TEAM == 64 ? a.group : TEAM;
+  const int teams = kNormThreads / g;
+  const Lane<V, K> ln(int(threadIdx.x) % g, g, a.C);
+  float w[K][V];
+  load_weights(a.w ? a.w + int64_t(b.index) * a.C : nullptr, ln, 1.0f, w);
+  const T* x = static_cast<const T*>(a.x) + int64_t(b.comp0) * a.C;
+  const T* dy = static_cast<const T*>(a.dy) + int64_t(b.comp0) * a.C;
+  T* dx = static_cast<T*>(a.y) + int64_t(b.comp0) * a.C;
+  const int64_t ld = int64_t(a.dim) * a.C;
+  const float inv = 1.0f / float(NC * a.C);
+  int phase = 0;
+  for_rows<U>(a, b, wg, teams, int(threadIdx.x) / g, [&](const Rows<U>& r) {
+    float xs[U][NC][K][V], d[U][NC][K][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      load_segment<T>(x + r.at[u] * ld, a.C, ln, xs[u]);
+      load_segment<T>(dy + r.at[u] * ld, a.C, ln, d[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      clear_others(xs[u], ln, r.valid[u]);
+      clear_others(d[u], ln, r.valid[u]);
+    }
+    if constexpr (NC == 1)
+      if (b.centered) center<TEAM>(xs, inv, ln, g, lds, phase);
+    constexpr int S = NC == 1 ? 3 : 2;  // sums of xc^2, g xc and, for scalars, g
+    float s[U * S];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float* q = s + u * S;
+#pragma unroll
+      for (int i = 0; i < S; ++i) q[i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float gv = d[u][c][i][v] * w[i][v];
+            q[0] += xs[u][c][i][v] * xs[u][c][i][v];
+            q[1] += gv * xs[u][c][i][v];
+            if constexpr (NC == 1) q[2] += gv;
+          }
+    }
+    team_sum<TEAM>(s, g, lds, phase);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float* q = s + u * S;
+      const float rstd = 1.0f / sqrtf(q[0] * inv + a.eps);
+      const float along = q[1] * inv * rstd;
+      float mg = 0.0f;
+      if constexpr (NC == 1) mg = b.centered ? q[2] * inv : 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float xh = xs[u][c][i][v] * rstd, dv = d[u][c][i][v];
+            aw[i][v] = fmaf(dv, xh, aw[i][v]);
+            if constexpr (NC == 1) ab[i][v] += dv;
+            xs[u][c][i][v] = rstd * (dv * w[i][v] - mg - xh * along);
+          }
+      if (r.valid[u]) store_segment<T>(dx + r.at[u] * ld, a.C, ln, xs[u]);
+    }
+  });
 }
 
 // The block this workgroup belongs to: a lane per block compares, one load deep.
@@ -275,7 +363,9 @@ __device__ __forceinline__ int block_of(const NormArgs& a) {
 // Calls f(integral_constant<NC>) for the block's component count.
 template <int NCMAX, class F>
 __device__ __forceinline__ void with_components(int nc, F&& f) {
-  if constexpr (NCMAX == 7) {
+  if constexpr (NCMAX == 1) {
+    f(std::integral_constant<int, 1>{});
+  } else if constexpr (NCMAX == 7) {
     switch (nc) {
       case 1: f(std::integral_constant<int, 1>{}); break;
       case 3: f(std::integral_constant<int, 3>{}); break;
@@ -293,30 +383,33 @@ __device__ __forceinline__ void with_components(int nc, F&& f) {
   }
 }
 
-template <class T, int V, int TEAM, int NCMAX>
-__global__ void __launch_bounds__(Team<TEAM>::kThreads) k_norm_fwd(const NormArgs a) {
-  __shared__ float lds[TEAM == 64 ? 1 : 2 * (TEAM / 64) * 4];
+template <class T, int V, int K, int TEAM, int NCMAX>
+__global__ void __launch_bounds__(kNormThreads) k_norm_fwd(const NormArgs a) {
+  __shared__ float lds[TEAM == 64 ? 1 : 2 * (TEAM / 64) * kTeamSums];
   const int i = block_of(a);
   const NormBlock b = a.blk[i];
   const int wg = int(blockIdx.x) - b.wg0;
   with_components<NCMAX>(b.nc, [&](auto nc) {
-    fwd_rows<T, V, TEAM, decltype(nc)::value>(a, b, wg, lds);
+    fwd_rows<T, V, K, TEAM, decltype(nc)::value>(a, b, wg, lds);
   });
 }
 
 // dw and db of this workgroup's rows to its partials (or, where it is the
 // block's only one, to the results).
-template <class T, int V, int TEAM, int NCMAX>
-__global__ void __launch_bounds__(Team<TEAM>::kThreads) k_norm_bwd(const NormArgs a) {
-  __shared__ float lds[TEAM == 64 ? 4 * 64 * V * 2 : 2 * (TEAM / 64) * 4];
-  const int i = block_of(a);
-  const NormBlock b = a.blk[i];
+template <class T, int V, int K, int TEAM, int NCMAX>
+__global__ void __launch_bounds__(kNormThreads) k_norm_bwd(const NormArgs a) {
+  constexpr int kRow = 64 * V * K;  // most channels of a team within a wavefront
+  __shared__ float lds[TEAM == 64 ? 2 * 4 * kRow : 2 * (TEAM / 64) * kTeamSums];
+  const int bi = block_of(a);
+  const NormBlock b = a.blk[bi];
   const int wg = int(blockIdx.x) - b.wg0;
-  float aw[V], ab[V];
+  float aw[K][V], ab[K][V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) aw[v] = ab[v] = 0.0f;
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) aw[i][v] = ab[i][v] = 0.0f;
   with_components<NCMAX>(b.nc, [&](auto nc) {
-    bwd_rows<T, V, TEAM, decltype(nc)::value>(a, b, wg, lds, aw, ab);
+    bwd_rows<T, V, K, TEAM, decltype(nc)::value>(a, b, wg, lds, aw, ab);
   });
   const bool only = b.n_wg == 1;
   float* ow = only ? (a.dw ? a.dw + int64_t(b.index) * a.C : nullptr)
@@ -329,38 +422,44 @@ __global__ void __launch_bounds__(Team<TEAM>::kThreads) k_norm_bwd(const NormArg
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     for (int o = a.group; o < 64; o <<= 1)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        aw[v] += __shfl_xor(aw[v], o);
-        ab[v] += __shfl_xor(ab[v], o);
-      }
-    const Lane ln = lane_of<V>(lane, a.C);
-    if (lane < a.group) {
+      for (int i = 0; i < K; ++i)
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v >= ln.skip) {
-          lds[wv * 64 * V + ln.k0 + v] = aw[v];
-          lds[(4 + wv) * 64 * V + ln.k0 + v] = ab[v];
+        for (int v = 0; v < V; ++v) {
+          aw[i][v] += __shfl_xor(aw[i][v], o);
+          ab[i][v] += __shfl_xor(ab[i][v], o);
         }
+    if (lane < a.group) {
+      const Lane<V, K> ln(lane, a.group, a.C);
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v >= ln.skip[i]) {
+            lds[wv * kRow + ln.k0[i] + v] = aw[i][v];
+            lds[(4 + wv) * kRow + ln.k0[i] + v] = ab[i][v];
+          }
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < a.C; k += 256) {
+    for (int k = threadIdx.x; k < a.C; k += kNormThreads) {
       float sw = 0.0f, sb = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sw += lds[j * 64 * V + k];
-        sb += lds[(4 + j) * 64 * V + k];
+        sw += lds[j * kRow + k];
+        sb += lds[(4 + j) * kRow + k];
       }
       if (ow) ow[k] = sw;
       if (ob) ob[k] = sb;
     }
   } else {
-    const Lane ln = lane_of<V>(threadIdx.x, a.C);
+    const Lane<V, K> ln(threadIdx.x, TEAM, a.C);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v >= ln.skip) {
-        if (ow) ow[ln.k0 + v] = aw[v];
-        if (ob) ob[ln.k0 + v] = ab[v];
-      }
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v >= ln.skip[i]) {
+          if (ow) ow[ln.k0[i] + v] = aw[i][v];
+          if (ob) ob[ln.k0[i] + v] = ab[i][v];
+        }
   }
 }
 
@@ -398,24 +497,36 @@ __global__ void __launch_bounds__(1024) k_norm_sum(const NormArgs a) {
   if (which == 1 && a.db && b.bias >= 0) a.db[int64_t(b.bias) * a.C + k] = s;
 }
 
-// Lanes of a team and channels per lane.  A lane owns 4 channels, or 1 when
-// the row has fewer than 4; teams of up to 64 lanes share a wavefront.
+// Team and lanes for C channels.  A lane owns vectors of 4 channels, or single
+// channels when the row has fewer than 4; teams of up to 64 lanes share a
+// wavefront.  Longer rows of scalars stay in one wavefront to 1024 channels (2
+// or 4 vectors a lane: no barrier, the loads of a row under way together);
+// those of other degrees, and all beyond 1024, take the workgroup.
 struct Shape {
-  int v, team, group;
+  int v, k, team, group;
 };
-Shape shape_of(int C) {
-  if (C < 4) return {1, 64, C <= 1 ? 1 : C <= 2 ? 2 : 4};
+Shape shape_of(int C, int top) {
+  if (C < 4) return {1, 1, 64, C <= 1 ? 1 : C <= 2 ? 2 : 4};
   int g = 1;
   while (g * 4 < C && g < 64) g *= 2;
-  if (C <= 256) return {4, 64, g};
-  if (C <= 1024) return {4, 256, 256};
-  return {4, 1024, 1024};
+  if (C <= 256) return {4, 1, 64, g};
+  if (top == 1 && C <= 1024) return {4, C <= 512 ? 2 : 4, 64, 64};
+  return {4, C <= 1024 ? 1 : 4, 256, 256};
 }
 
-// Workgroups of every block of [first, last), in proportion to its components.
-int plan(NormArgs& a, const NormBlock* blocks, int n_blocks, int budget) {
-  const Shape sh = shape_of(a.C);
-  const int teams = (sh.team == 64 ? 256 : sh.team) / sh.group;
+// Workgroups of every block, in proportion to its components: 6 on a compute
+// unit, what the forward's registers let be resident (64,000 rows of
+// 128x(0e+1o+2e+3o), us: forward 1536 workgroups 197, 2048 209, 4096 203;
+// backward 1024 301, 1536 296, 2048 314).  The backward's
+// each leave 8 C bytes of partials to write and read again: past 256 of them a
+// workgroup has at least 128 bytes of every channel to read, and a single
+// block's are as many on each of the 256 compute units (1001 scalar channels,
+// 20,011 rows: 512 workgroups 52 us, 556 62, 768 56, 1024 59).
+constexpr int kBudget = 1536;
+
+int plan(NormArgs& a, const NormBlock* blocks, int n_blocks, int top, bool bwd, int esize) {
+  const Shape sh = shape_of(a.C, top);
+  const int teams = kNormThreads / sh.group;
   a.group = sh.group;
   a.n_blocks = n_blocks;
   int dim = 0, wg = 0;
@@ -423,43 +534,68 @@ int plan(NormArgs& a, const NormBlock* blocks, int n_blocks, int budget) {
   const int64_t steps = (a.n_rows + teams - 1) / teams;
   for (int i = 0; i < n_blocks; ++i) {
     a.blk[i] = blocks[i];
-    const int64_t share = std::max<int64_t>(1, int64_t(budget) * blocks[i].nc / dim);
+    const int64_t nc = blocks[i].nc;
+    int64_t n = std::min<int64_t>(int64_t(kBudget) * nc / dim, steps);
+    if (bwd) n = std::min(n, std::max<int64_t>(256, a.n_rows * nc * esize / 128));
+    if (bwd && n_blocks == 1 && n > 256) n -= n % 256;
     a.blk[i].wg0 = wg;
-    a.blk[i].n_wg = int(std::max<int64_t>(1, std::min(share, (steps + 3) / 4)));
+    n = std::max<int64_t>(1, n);
+    const int64_t turns = std::max<int64_t>(1, (steps + n - 1) / n);
+    a.blk[i].n_wg = int(std::max<int64_t>(1, (steps + turns - 1) / turns));  // alike in length
     wg += a.blk[i].n_wg;
   }
   return wg;
 }
 
-constexpr int kFwdBudget = 4096, kBwdBudget = 1024;
-
 template <class T, int NCMAX>
-hipError_t launch(bool bwd, const NormArgs& a, int wgs, hipStream_t s) {
-  const Shape sh = shape_of(a.C);
-  const dim3 grid{unsigned(wgs)}, wg{unsigned(sh.team == 64 ? 256 : sh.team)};
-#define E3_NORM_LAUNCH(V, TEAM)                                                             \
-  if (bwd) hipLaunchKernelGGL((k_norm_bwd<T, V, TEAM, NCMAX>), grid, wg, 0, s, a);          \
-  else hipLaunchKernelGGL((k_norm_fwd<T, V, TEAM, NCMAX>), grid, wg, 0, s, a)
-  if (sh.v == 1) { E3_NORM_LAUNCH(1, 64); }
-  else if (sh.team == 64) { E3_NORM_LAUNCH(4, 64); }
-  else if (sh.team == 256) { E3_NORM_LAUNCH(4, 256); }
-  else if constexpr (NCMAX == 7) { E3_NORM_LAUNCH(4, 1024); }
-  else return hipErrorInvalidValue;
-#undef E3_NORM_LAUNCH
-  return hipGetLastError();
+hipError_t launch_top(bool bwd, const NormArgs& a, int wgs, hipStream_t s) {
+  const Shape sh = shape_of(a.C, NCMAX);
+  const dim3 grid{unsigned(wgs)}, wg{unsigned(kNormThreads)};
+  const auto go = [&](auto v, auto k, auto team) {
+    constexpr int V = decltype(v)::value, K = decltype(k)::value, TEAM = decltype(team)::value;
+    if (bwd) hipLaunchKernelGGL((k_norm_bwd<T, V, K, TEAM, NCMAX>), grid, wg, 0, s, a);
+    else hipLaunchKernelGGL((k_norm_fwd<T, V, K, TEAM, NCMAX>), grid, wg, 0, s, a);
+    return hipGetLastError();
+  };
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 4> four{};
+  constexpr std::integral_constant<int, 64> wave{};
+  constexpr std::integral_constant<int, 256> group{};
+  if (sh.v == 1) return go(one, one, wave);
+  if (sh.team == 64) {
+    if (sh.k == 1) return go(four, one, wave);
+    if constexpr (NCMAX == 1)
+      return sh.k == 2 ? go(four, std::integral_constant<int, 2>{}, wave) : go(four, four, wave);
+  } else {
+    if constexpr (NCMAX > 1)
+      if (sh.k == 1) return go(four, one, group);
+    if constexpr (NCMAX <= 7)
+      if (sh.k == 4) return go(four, four, group);
+  }
+  return hipErrorInvalidValue;
 }
 
-// Calls f(blocks, count) for runs of at most kNormMaxBlocks blocks, the
-// degrees up to 3 and those above apart (their kernels differ in registers).
+template <class T>
+hipError_t launch(int top, bool bwd, const NormArgs& a, int wgs, hipStream_t s) {
+  return top == 1   ? launch_top<T, 1>(bwd, a, wgs, s)
+         : top == 7 ? launch_top<T, 7>(bwd, a, wgs, s)
+                    : launch_top<T, 17>(bwd, a, wgs, s);
+}
+
+// Calls f(blocks, count, most components) for runs of at most kNormMaxBlocks
+// blocks, the degrees up to 3 and those above apart, and lists of scalars by
+// themselves: their kernels differ in registers.
 template <class F>
 hipError_t for_runs(const NormBlock* blocks, int n, F&& f) {
+  int top = 1;
+  for (int i = 0; i < n; ++i) top = std::max(top, blocks[i].nc);
   for (int high = 0; high < 2; ++high) {
     NormBlock run[kNormMaxBlocks];
     int m = 0;
     for (int i = 0; i <= n; ++i) {
       if (i < n && (blocks[i].nc > 7) == bool(high)) run[m++] = blocks[i];
       if (m > 0 && (i == n || m == kNormMaxBlocks)) {
-        const hipError_t e = f(run, m, bool(high));
+        const hipError_t e = f(run, m, high ? 17 : top == 1 ? 1 : 7);
         if (e != hipSuccess) return e;
         m = 0;
       }
@@ -470,13 +606,13 @@ hipError_t for_runs(const NormBlock* blocks, int n, F&& f) {
 
 }  // namespace
 
-size_t norm_part_floats(int64_t n_rows, int C, const NormBlock* blocks, int n_blocks) {
+size_t norm_part_floats(int64_t n_rows, int C, const NormBlock* blocks, int n_blocks, int esize) {
   size_t most = 0;
-  (void)for_runs(blocks, n_blocks, [&](const NormBlock* run, int m, bool) {
+  (void)for_runs(blocks, n_blocks, [&](const NormBlock* run, int m, int top) {
     NormArgs a{};
     a.n_rows = n_rows;
     a.C = C;
-    most = std::max(most, size_t(plan(a, run, m, kBwdBudget)) * 2 * C);
+    most = std::max(most, size_t(plan(a, run, m, top, true, esize)) * 2 * C);
     return hipSuccess;
   });
   return most;
@@ -484,11 +620,10 @@ size_t norm_part_floats(int64_t n_rows, int C, const NormBlock* blocks, int n_bl
 
 hipError_t launch_norm(bool bwd, const NormArgs& args, const NormBlock* blocks, int n_blocks,
                        int bf16, hipStream_t s) {
-  return for_runs(blocks, n_blocks, [&](const NormBlock* run, int m, bool high) {
+  return for_runs(blocks, n_blocks, [&](const NormBlock* run, int m, int top) {
     NormArgs a = args;
-    const int wgs = plan(a, run, m, bwd ? kBwdBudget : kFwdBudget);
-    hipError_t e = high ? (bf16 ? launch<bf16_t, 17>(bwd, a, wgs, s) : launch<float, 17>(bwd, a, wgs, s))
-                        : (bf16 ? launch<bf16_t, 7>(bwd, a, wgs, s) : launch<float, 7>(bwd, a, wgs, s));
+    const int wgs = plan(a, run, m, top, bwd, bf16 ? 2 : 4);
+    const hipError_t e = bf16 ? launch<bf16_t>(top, bwd, a, wgs, s) : launch<float>(top, bwd, a, wgs, s);
     bool sum = false;
     for (int i = 0; i < m; ++i) sum |= a.blk[i].n_wg > 1;
     if (e != hipSuccess || !bwd || !sum) return e;

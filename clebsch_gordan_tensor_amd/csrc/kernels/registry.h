@@ -390,7 +390,7 @@ struct NormArgs {
   NormBlock blk[kNormMaxBlocks];
 };
 // floats of `part` that launch_norm's backward needs
-size_t norm_part_floats(int64_t n_rows, int C, const NormBlock* blocks, int n_blocks);
+size_t norm_part_floats(int64_t n_rows, int C, const NormBlock* blocks, int n_blocks, int esize);
 hipError_t launch_norm(bool bwd, const NormArgs& a, const NormBlock* blocks, int n_blocks,
                        int bf16, hipStream_t s);
 

@@ -610,7 +610,7 @@ e3_status e3_layer_norm(const e3_irreps* irreps, int64_t n_rows, const void* x,
                         e3_dtype dtype, void* stream);
 
 /* Bytes of the workspace of e3_layer_norm_backward (partial sums of the
- * weight's and bias's gradients; at most 8 KB per channel; host only). */
+ * weight's and bias's gradients; about 12 KB per channel at most; host only). */
 e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, size_t* bytes);
 
 /* Backward of e3_layer_norm for the cotangent dy [n_rows][dim][C]; the
