@@ -9,6 +9,7 @@ or ``python -m clebsch_gordan_tensor_amd.build``); a missing library raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass
 
@@ -1028,37 +1029,64 @@ def conv_double_backward_generic(desc: Desc, rowptr, sender, workspace, Y, x, w,
 
 # ------------------------------------------------------------ normalisation
 
-def _on(device, call, stream):
-    """call(stream) on `device`, whichever device is current: on the given
-    stream, or on the device's current one."""
+def _raw_stream(device, stream):
+    """The given stream's handle, or that of the device's current stream."""
     import torch
+    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+            else stream.cuda_stream)
+
+
+def _on(device, fn, *args, stream=None):
+    """Calls fn(*args, stream) with `device` current, whichever device is now."""
+    import torch
+    s = _raw_stream(device, stream)
     if torch.cuda.current_device() == device.index:
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s)
+    if status != 0:
+        _check(status)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need_on(device, t, name, shape, dtype):
+    """_need, on `device`; None passes."""
+    if t is not None:
+        _need(t, name, shape, dtype)
+        if t.device != device:
             raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
 
 
-def _norm_shapes(irreps, x, weight, bias=None):
-    """Checks the operands both directions share; (rows, C, number of blocks,
-    number of 0e blocks)."""
-    import torch
+@functools.lru_cache(maxsize=256)
+def _norm_spec(irreps, channels):
+    """(struct, components, blocks, 0e blocks) of an irreps tuple."""
+    return (_irreps_struct(irreps, channels), synth.dim(irreps), len(irreps),
+            sum(1 for l, p in irreps if l == 0 and p == 1))
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace_size(irreps, rows, channels):
+    nb = C.c_size_t()
+    _check(lib().e3_layer_norm_workspace_size(C.byref(_norm_spec(irreps, channels)[0]), rows,
+                                              C.byref(nb)))
+    return nb.value
+
+
+def _norm_x(irreps, x):
+    """(irreps tuple, its spec) after the checks of x."""
     _need(x, "x")
-    if x.dim() != 3 or x.shape[1] != synth.dim(irreps):
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows][{synth.dim(irreps)}][C]")
-    rows, _, ch = x.shape
-    scalars = sum(1 for l, p in irreps if l == 0 and p == 1)
-    if weight is not None:
-        _need(weight, "weight", shape=(len(irreps), ch), dtype=torch.float32)
-    if bias is not None:
-        _need(bias, "bias", shape=(scalars, ch), dtype=torch.float32)
-    _same_device(x.device, weight=weight, bias=bias)
-    return rows, ch, len(irreps), scalars
+    irreps = tuple(map(tuple, irreps))
+    if x.dim() != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows][components][channels]")
+    spec = _norm_spec(irreps, x.shape[2])
+    if x.shape[1] != spec[1]:
+        raise ValueError(f"x has {x.shape[1]} components, the irreps {spec[1]}")
+    return irreps, spec
 
 
 def layer_norm(irreps, x, weight=None, bias=None, eps=1e-5, flags=0, out=None, stream=None):
@@ -1069,22 +1097,22 @@ def layer_norm(irreps, x, weight=None, bias=None, eps=1e-5, flags=0, out=None, s
     for 0e blocks.  [(0, 1)] is the ordinary layer norm over C channels.  out
     may be x."""
     import torch
-    rows, ch, _, _ = _norm_shapes(irreps, x, weight, bias)
+    irreps, (st, _, n_blocks, scalars) = _norm_x(irreps, x)
+    dev, shape = x.device, x.shape
+    _need_on(dev, weight, "weight", (n_blocks, shape[2]), torch.float32)
+    _need_on(dev, bias, "bias", (scalars, shape[2]), torch.float32)
     if out is None:
         out = torch.empty_like(x)
-    _need(out, "out", shape=tuple(x.shape), dtype=x.dtype)
-    _same_device(x.device, out=out)
-    a = _irreps_struct(irreps, ch)
-    _check(_on(x.device, lambda s: lib().e3_layer_norm(
-        C.byref(a), rows, _ptr(x), _ptr(weight), _ptr(bias), eps, flags, _ptr(out),
-        _dtype_code(x), s), stream))
+    else:
+        _need_on(dev, out, "out", shape, x.dtype)
+    _on(dev, lib().e3_layer_norm, C.byref(st), shape[0], x.data_ptr(), _addr(weight), _addr(bias),
+        eps, flags, out.data_ptr(), _dtype_code(x), stream=stream)
     return out
 
 
 def layer_norm_workspace_size(irreps, rows: int, channels: int) -> int:
-    a, nb = _irreps_struct(irreps, channels), C.c_size_t()
-    _check(lib().e3_layer_norm_workspace_size(C.byref(a), rows, C.byref(nb)))
-    return nb.value
+    """Bytes of layer_norm_backward's workspace."""
+    return _norm_workspace_size(tuple(map(tuple, irreps)), rows, channels)
 
 
 def layer_norm_backward(irreps, x, weight, dy, eps=1e-5, flags=0, dx=None, dweight=None,
@@ -1092,28 +1120,29 @@ def layer_norm_backward(irreps, x, weight, dy, eps=1e-5, flags=0, dx=None, dweig
     """(dx, dweight [blocks][C], dbias [0e blocks][C]) of layer_norm for the
     cotangent dy; weight may be None (ones).  dx may be x or dy."""
     import torch
-    rows, ch, n_blocks, scalars = _norm_shapes(irreps, x, weight)
-    dev, shape = x.device, tuple(x.shape)
-    _need(dy, "dy", shape=shape, dtype=x.dtype)
+    irreps, (st, _, n_blocks, scalars) = _norm_x(irreps, x)
+    dev, shape, f32 = x.device, x.shape, torch.float32
+    ch = shape[2]
+    _need_on(dev, weight, "weight", (n_blocks, ch), f32)
+    _need(dy, "dy")
+    _need_on(dev, dy, "dy", shape, x.dtype)
+    _need_on(dev, dx, "dx", shape, x.dtype)
+    _need_on(dev, dweight, "dweight", (n_blocks, ch), f32)
+    _need_on(dev, dbias, "dbias", (scalars, ch), f32)
+    _need_on(dev, workspace, "workspace", None, None)
     if dx is None:
         dx = torch.empty_like(x)
     if dweight is None:
-        dweight = torch.empty((n_blocks, ch), device=dev, dtype=torch.float32)
+        dweight = torch.empty((n_blocks, ch), device=dev, dtype=f32)
     if dbias is None:
-        dbias = torch.empty((scalars, ch), device=dev, dtype=torch.float32)
+        dbias = torch.empty((scalars, ch), device=dev, dtype=f32)
     if workspace is None:
-        workspace = torch.empty(layer_norm_workspace_size(irreps, rows, ch), device=dev,
+        workspace = torch.empty(_norm_workspace_size(irreps, shape[0], ch), device=dev,
                                 dtype=torch.uint8)
-    _need(dx, "dx", shape=shape, dtype=x.dtype)
-    _need(dweight, "dweight", shape=(n_blocks, ch), dtype=torch.float32)
-    _need(dbias, "dbias", shape=(scalars, ch), dtype=torch.float32)
-    _need(workspace, "workspace")
-    _same_device(dev, dy=dy, dx=dx, dweight=dweight, dbias=dbias, workspace=workspace)
-    a = _irreps_struct(irreps, ch)
-    _check(_on(dev, lambda s: lib().e3_layer_norm_backward(
-        C.byref(a), rows, _ptr(x), _ptr(weight), _ptr(dy), eps, flags, _ptr(dx), _ptr(dweight),
-        _ptr(dbias), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _dtype_code(x), s), stream))
+    _on(dev, lib().e3_layer_norm_backward, C.byref(st), shape[0], x.data_ptr(), _addr(weight),
+        dy.data_ptr(), eps, flags, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _dtype_code(x),
+        stream=stream)
     return dx, dweight, dbias
 
 
@@ -1158,60 +1187,55 @@ class Params:
             raise ValueError(f"weight_decay has {len(decay)} values, expected {n}")
         self._arr = (_Param * max(1, n))()
         self._n = n
-        self.device = None
         self._keep = {k: list(c) if c is not None else [None] * n for k, c in cols.items()}
-        self.set_grads(grads)
-        for i in range(n):
-            e, size = self._arr[i], grads[i].numel()
-            e.weight_decay = decay[i]
-            if not self.updates:
-                continue
-            p, mi, vi, ms, vs, cp = (self._keep[k][i] for k in
-                                     ("params", "m", "v", "m_scale", "v_scale", "copies"))
-            _need(p, f"params[{i}]", shape=tuple(grads[i].shape), dtype=torch.float32)
-            codes = ms is not None or vs is not None
-            _need(mi, f"m[{i}]", dtype=torch.int8 if codes else torch.float32)
-            _need(vi, f"v[{i}]", dtype=torch.uint8 if codes else torch.float32)
-            for t, name in ((mi, "m"), (vi, "v")):
-                if t.numel() != size:
-                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {size}")
-            if codes:
-                for t, name in ((ms, "m_scale"), (vs, "v_scale")):
-                    _need(t, f"{name}[{i}]", shape=((size + 255) // 256,), dtype=torch.float32)
-            if cp is not None:
-                _need(cp, f"copies[{i}]", shape=tuple(p.shape), dtype=torch.bfloat16)
-            for t, name in ((p, "params"), (mi, "m"), (vi, "v"), (ms, "m_scale"),
-                            (vs, "v_scale"), (cp, "copies")):
-                _same_device(self.device, **{f"{name}[{i}]": t})
-            e.p, e.m, e.v = p.data_ptr(), mi.data_ptr(), vi.data_ptr()
-            e.m_scale = ms.data_ptr() if codes else None
-            e.v_scale = vs.data_ptr() if codes else None
-            e.p_bf16 = cp.data_ptr() if cp is not None else None
+        self.device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        self.sizes = [g.numel() for g in grads]
         if self.updates:
-            _check(lib().e3_param_check(n, self._arr))
+            codes = [a is not None or b is not None
+                     for a, b in zip(self._keep["m_scale"], self._keep["v_scale"])]
+            runs = [((k + 255) // 256,) if c else None for k, c in zip(self.sizes, codes)]
+            self._fill("p", "params", torch.float32, [g.shape for g in grads])
+            self._fill("m", "m", [torch.int8 if c else torch.float32 for c in codes])
+            self._fill("v", "v", [torch.uint8 if c else torch.float32 for c in codes])
+            self._fill("m_scale", "m_scale", torch.float32, runs, codes)
+            self._fill("v_scale", "v_scale", torch.float32, runs, codes)
+            self._fill("p_bf16", "copies", torch.bfloat16, [g.shape for g in grads],
+                       [c is not None for c in self._keep["copies"]])
+        for e, k, d in zip(self._arr, self.sizes, decay):
+            e.n, e.weight_decay = k, d
+        self.set_grads(grads)
         nb = C.c_size_t()
         _check(lib().e3_grad_norm_workspace_size(n, self._arr, C.byref(nb)))
         self.workspace_bytes = nb.value  # of grad_norm
+
+    def _fill(self, field, name, dtypes, shapes=None, given=None):
+        """One pointer of every tensor, after its checks."""
+        for i, t in enumerate(self._keep[name]):
+            if given is not None and not given[i]:
+                continue
+            at = f"{name}[{i}]"
+            _need(t, at)
+            _need_on(self.device, t, at, shapes[i] if shapes else None,
+                     dtypes[i] if isinstance(dtypes, list) else dtypes)
+            if shapes is None and t.numel() != self.sizes[i]:
+                raise ValueError(f"{at} has {t.numel()} elements, expected {self.sizes[i]}")
+            setattr(self._arr[i], field, t.data_ptr())
 
     def set_grads(self, grads):
         """Other gradient tensors for the same parameters."""
         if len(grads) != self._n:
             raise ValueError(f"grads has {len(grads)} tensors, expected {self._n}")
         codes = []
-        for i, g in enumerate(grads):
-            old = self._keep["params"][i]
-            _need(g, f"grads[{i}]", shape=None if old is None else tuple(old.shape))
-            if self._arr[i].grad is not None and old is None and g.numel() != self._arr[i].n:
-                raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {self._arr[i].n}")
-            if self.device is None:
-                self.device = g.device
-            _same_device(self.device, **{f"grads[{i}]": g})
+        for i, (g, p) in enumerate(zip(grads, self._keep["params"])):
+            _need(g, f"grads[{i}]")
+            _need_on(self.device, g, f"grads[{i}]", None if p is None else p.shape, None)
+            if g.numel() != self.sizes[i]:
+                raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {self.sizes[i]}")
             codes.append(_dtype_code(g))
-        for i, g in enumerate(grads):
-            e = self._arr[i]
-            e.n, e.grad, e.grad_dtype = g.numel(), g.data_ptr(), codes[i]
+        for e, g, code in zip(self._arr, grads, codes):
+            e.grad, e.grad_dtype = g.data_ptr(), code
         self._grads = list(grads)
-        if self.updates and self._arr[0].p:
+        if self.updates:
             _check(lib().e3_param_check(self._n, self._arr))
 
     def __len__(self):
@@ -1241,17 +1265,15 @@ def grad_norm(params: Params, max_norm=float("inf"), out=None, workspace=None, s
     factor min(1, max_norm / (norm + 1e-6)) that clips it (NaN for a norm that
     is not finite); out[1:] is adamw's grad_scale."""
     import torch
-    dev = params.device or torch.device("cuda", torch.cuda.current_device())
+    dev = params.device
+    _need_on(dev, out, "out", (2,), torch.float32)
+    _need_on(dev, workspace, "workspace", None, None)
     if out is None:
         out = torch.empty(2, device=dev, dtype=torch.float32)
     if workspace is None:
         workspace = torch.empty(params.workspace_bytes, device=dev, dtype=torch.uint8)
-    _need(out, "out", shape=(2,), dtype=torch.float32)
-    _need(workspace, "workspace")
-    _same_device(dev, out=out, workspace=workspace)
-    _check(_on(dev, lambda s: lib().e3_grad_norm(
-        len(params), params._arr, max_norm, _ptr(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), s), stream))
+    _on(dev, lib().e3_grad_norm, len(params), params._arr, max_norm, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
     return out
 
 
@@ -1265,26 +1287,26 @@ def adamw(params: Params, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale
     import torch
     if not params.updates:
         raise ValueError("the list holds gradients only")
+    dev = params.device
     a = _AdamwArgs(0.0, beta1, beta2, eps, 1, None, None, None, flags)
-    for t, name, dt in ((step, "step", torch.int64), (lr, "lr", torch.float32),
-                        (grad_scale, "grad_scale", torch.float32)):
-        if isinstance(t, torch.Tensor):
-            _need(t, name, dtype=dt)
-            if t.numel() != 1:
-                raise ValueError(f"{name} must hold one element")
-            _same_device(params.device or t.device, **{name: t})
     if isinstance(step, torch.Tensor):
-        a.step_dev = step.data_ptr()
+        a.step_dev = _one_value(dev, step, "step", torch.int64)
     else:
         a.step = step
     if isinstance(lr, torch.Tensor):
-        a.lr_dev = lr.data_ptr()
+        a.lr_dev = _one_value(dev, lr, "lr", torch.float32)
     else:
         a.lr = lr
     if grad_scale is not None:
-        a.grad_scale = grad_scale.data_ptr()
-    dev = params.device or torch.device("cuda", torch.cuda.current_device())
-    _check(_on(dev, lambda s: lib().e3_adamw(len(params), params._arr, C.byref(a), s), stream))
+        a.grad_scale = _one_value(dev, grad_scale, "grad_scale", torch.float32)
+    _on(dev, lib().e3_adamw, len(params), params._arr, C.byref(a), stream=stream)
+
+
+def _one_value(device, t, name, dtype):
+    _need_on(device, t, name, None, dtype)
+    if t.numel() != 1:
+        raise ValueError(f"{name} must hold one element")
+    return t.data_ptr()
 
 
 def adamw_moments(params: Params, m_out=None, v_out=None, stream=None):
@@ -1292,24 +1314,21 @@ def adamw_moments(params: Params, m_out=None, v_out=None, stream=None):
     import torch
     if not params.updates:
         raise ValueError("the list holds gradients only")
-    n = len(params)
+    n, dev = len(params), params.device
     outs = []
     for given, name in ((m_out, "m_out"), (v_out, "v_out")):
         if given is None:
-            given = [torch.empty(params._arr[i].n, device=params.device, dtype=torch.float32)
-                     for i in range(n)]
+            given = [torch.empty(k, device=dev, dtype=torch.float32) for k in params.sizes]
         if len(given) != n:
             raise ValueError(f"{name} has {len(given)} tensors, expected {n}")
-        ptrs = (C.c_void_p * max(1, n))()
-        for i, t in enumerate(given):
-            _need(t, f"{name}[{i}]", dtype=torch.float32)
-            if t.numel() != params._arr[i].n:
-                raise ValueError(f"{name}[{i}] has {t.numel()} elements, "
-                                 f"expected {params._arr[i].n}")
-            _same_device(params.device, **{f"{name}[{i}]": t})
-            ptrs[i] = t.data_ptr()
-        outs.append((given, ptrs))
-    dev = params.device or torch.device("cuda", torch.cuda.current_device())
-    _check(_on(dev, lambda s: lib().e3_adamw_moments(n, params._arr, outs[0][1], outs[1][1], s),
-               stream))
+        T = torch.Tensor  # column by column: a list may hold hundreds
+        if not (list(map(T.numel, given)) == params.sizes and all(map(T.is_contiguous, given))
+                and set(map(T.get_device, given)) <= {dev.index}
+                and {t.dtype for t in given} <= {torch.float32}):
+            for i, (t, k) in enumerate(zip(given, params.sizes)):
+                _need_on(dev, _need(t, f"{name}[{i}]"), f"{name}[{i}]", None, torch.float32)
+                if t.numel() != k:
+                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {k}")
+        outs.append((given, (C.c_void_p * max(1, n))(*map(T.data_ptr, given))))
+    _on(dev, lib().e3_adamw_moments, n, params._arr, outs[0][1], outs[1][1], stream=stream)
     return outs[0][0], outs[1][0]
