@@ -2625,7 +2625,7 @@ e3_status e3_adamw(int32_t n_params, const e3_param* params, const e3_adamw_args
   a.step = std::max<int64_t>(1, g.step);
   a.lr_f = float(g.lr);
   a.size = float(g.lr / (1.0 - std::pow(g.beta1, double(a.step))));
-  a.inv_c2 = float(1.0 / (1.0 - std::pow(g.beta2, double(a.step))));
+  a.root = float(1.0 / std::sqrt(1.0 - std::pow(g.beta2, double(a.step))));
   a.eps = float(g.eps);
   a.step_dev = g.step_dev;
   a.lr_dev = g.lr_dev;

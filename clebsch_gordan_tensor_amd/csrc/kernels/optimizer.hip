@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(1024)
 // ------------------------------------------------------------------ the step
 
 struct Step {
-  float lr, size, inv_c2, eps;  // size = lr / (1 - b1^t), inv_c2 = 1 / (1 - b2^t)
+  float lr, size, root, eps;  // size = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t)
   float scale;                  // of the gradients
   bool skip;
 };
@@ -201,13 +201,13 @@ __device__ __forceinline__ double pow_int(double b, int64_t t) {
 }
 
 __device__ __forceinline__ Step step_of(const AdamArgs& a) {
-  Step s{a.lr_f, a.size, a.inv_c2, a.eps, 1.0f, false};
+  Step s{a.lr_f, a.size, a.root, a.eps, 1.0f, false};
   if (a.step_dev || a.lr_dev) {
     const double lr = a.lr_dev ? double(*a.lr_dev) : a.lr;
     const int64_t t = a.step_dev ? max(int64_t(1), *a.step_dev) : a.step;
     s.lr = float(lr);
     s.size = float(lr / (1.0 - pow_int(a.beta1, t)));
-    s.inv_c2 = float(1.0 / (1.0 - pow_int(a.beta2, t)));
+    s.root = float(1.0 / sqrt(1.0 - pow_int(a.beta2, t)));
   }
   if (a.grad_scale) {
     s.scale = *a.grad_scale;
@@ -216,10 +216,12 @@ __device__ __forceinline__ Step step_of(const AdamArgs& a) {
   return s;
 }
 
-// p after the step.  Decay and update are added first and taken off together:
-// one rounding of p, and lr wd is not lost in 1 - lr wd.
-__device__ __forceinline__ float stepped(float p, float m, float v, float lr_wd, const Step& s) {
-  const float d = __builtin_amdgcn_sqrtf(v * s.inv_c2) + s.eps;
+// p after the step, from sqrt(v).  Decay and update are added first and taken
+// off together: one rounding of p, and lr wd is not lost in 1 - lr wd.  Root
+// and reciprocal are the hardware's, off by a step at most.
+__device__ __forceinline__ float stepped(float p, float m, float root_v, float lr_wd,
+                                         const Step& s) {
+  const float d = fmaf(root_v, s.root, s.eps);
   return p - fmaf(s.size * m, __builtin_amdgcn_rcpf(d), lr_wd * p);
 }
 
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw(const ParamList l, cons
       const float g = g4[e] * st.scale;
       m4[e] = fmaf(b1, m4[e], c1 * g);
       v4[e] = fmaf(b2, v4[e], c2 * g * g);
-      p4[e] = stepped(p4[e], m4[e], v4[e], lr_wd, st);
+      p4[e] = stepped(p4[e], m4[e], __builtin_amdgcn_sqrtf(v4[e]), lr_wd, st);
     }
     store4(t.p, i, t.n, p4);
     store4(m, i, t.n, m4);
@@ -257,47 +259,72 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw(const ParamList l, cons
 
 // ------------------------------------------------------------ 8-bit moments
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t u) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) u = max(u, uint32_t(__shfl_xor(int(u), o)));
-  return u;
+// Largest of two bit patterns over the wavefront, in every lane.
+__device__ __forceinline__ void wave_max2(uint32_t& a, uint32_t& b) {
+  const auto step = [&](auto ctrl) {
+    constexpr int C = decltype(ctrl)::value;
+    a = max(a, uint32_t(__builtin_amdgcn_mov_dpp(int(a), C, 0xF, 0xF, false)));
+    b = max(b, uint32_t(__builtin_amdgcn_mov_dpp(int(b), C, 0xF, 0xF, false)));
+  };
+  step(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  step(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  step(std::integral_constant<int, 0x141>{});  // half-row mirror
+  step(std::integral_constant<int, 0x140>{});  // row mirror
+  auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  a = max(uint32_t(r[0]), uint32_t(r[1]));
+  r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  b = max(uint32_t(r[0]), uint32_t(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+  a = max(uint32_t(r[0]), uint32_t(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  b = max(uint32_t(r[0]), uint32_t(r[1]));
 }
 
-__device__ __forceinline__ double value_m(int c, double s) { return s * double(c * abs(c)); }
-__device__ __forceinline__ double value_v(int c, double s) {
-  const double r = s * double(c * c);
-  return r * r;
+constexpr uint32_t kFlip = 0x80808080u;  // int8 codes as bytes c + 128
+
+// Byte e of a word as a float.
+template <int E>
+__device__ __forceinline__ float byte_of(uint32_t w) {
+  return float((w >> (8 * E)) & 255u);
 }
 
-// The code of a = |m|: t = sqrt(a / s) in 32 bits is off by 3e-5 at most
-// (sqrt, conversion and 1/s, of values up to 127), so only within 1e-4 of a
-// border the 64-bit border itself decides.
-__device__ __forceinline__ int code_m(double a, double s, double inv) {
-  const float t = __builtin_amdgcn_sqrtf(float(a * inv));
-  const float f = floorf(t), r = t - f - 0.5f;
-  int c = int(f) + (r > 0.0f);
-  if (fabsf(r) < 1e-4f) {
-    const double b = double(f) + 0.5;
-    c = int(f) + (s * (b * b) < a);
+// c |c| and c^2 of the codes: at most 16 bits, exact.
+template <int E>
+__device__ __forceinline__ float square_m(uint32_t flipped) {
+  const float c = byte_of<E>(flipped) - 128.0f;
+  return c * fabsf(c);
+}
+template <int E>
+__device__ __forceinline__ float square_v(uint32_t w) {
+  const float c = byte_of<E>(w);
+  return c * c;
+}
+
+// A code from its 32-bit root t, off by 3e-5 (m: values to 127) or 7e-5 (v: to
+// 255) at most: nearer to a border than `kNear` 64 bits decide, as they do all
+// over when the scale is so small that 32-bit roots lose the value (`tiny`).
+constexpr float kNear = 1e-4f;
+constexpr float kTinyM = 1e-36f, kTinyV = 1e-18f;
+
+__device__ __forceinline__ bool near_border(float t, float c) {
+  return fabsf(t - c) > 0.5f - kNear;
+}
+// P = 1: borders s (k + 1/2)^2; P = 2: their squares.
+template <int P>
+__device__ float code_exact(float t, double value, double s, bool tiny) {
+  if (tiny) {
+    const double q = P == 1 ? value / s : sqrt(value) / s;
+    t = float(sqrt(q));
   }
-  return min(c, 127);
-}
-
-// As code_m; t = (v / s^2)^(1/4) is off by 7e-5 at most (values up to 255).
-__device__ __forceinline__ int code_v(double v, double s, double inv2) {
-  const float t = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(float(v * inv2)));
   const float f = floorf(t), r = t - f - 0.5f;
-  int c = int(f) + (r > 0.0f);
-  if (fabsf(r) < 2e-4f) {
-    const double b = double(f) + 0.5, q = s * (b * b);
-    c = int(f) + (q * q < v);
-  }
-  return max(min(c, 255), int(v > 0.0));
+  if (fabsf(r) > 2.0f * kNear) return f + (r > 0.0f ? 1.0f : 0.0f);
+  const double h = double(f) + 0.5, b = s * (h * h);
+  return f + ((P == 1 ? b : b * b) < value ? 1.0f : 0.0f);
 }
 
 // A wavefront per block of 256 elements, four consecutive ones a lane.  The
 // maxima are taken over the bit patterns of |m| and v (so a NaN wins): a
-// block that holds one reads back as NaN instead of losing it.
+// block that holds a value that is not finite reads back as NaN.
 __global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, const AdamArgs a) {
   const Step st = step_of(a);
   if (st.skip) return;
@@ -307,7 +334,7 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, con
   const int64_t end = min(t.n, base + l.chunk);
   const float lr_wd = st.lr * t.weight_decay;
   const double scale = double(st.scale);
-  const double b1 = a.beta1, c1 = 1.0 - a.beta1, b2 = a.beta2, c2 = 1.0 - a.beta2;
+  const double c1 = (1.0 - a.beta1) * scale, c2 = (1.0 - a.beta2) * scale * scale;
   uint8_t* mc = static_cast<uint8_t*>(t.m);
   uint8_t* vc = static_cast<uint8_t*>(t.v);
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -316,35 +343,63 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, con
     float p4[4], g4[4];
     load4(t.p, i, t.n, p4);
     load4_grad(t, i, g4);
-    const uint32_t mw = load_codes(mc, i, t.n), vw = load_codes(vc, i, t.n);
-    const double sm = double(t.m_scale[blk]), sv = double(t.v_scale[blk]);
+    const uint32_t mw = load_codes(mc, i, t.n) ^ kFlip;
+    const uint32_t vw = load_codes(vc, i, t.n);
+    const double sm = a.beta1 * double(t.m_scale[blk]), sv = double(t.v_scale[blk]);
+    const double sv2 = a.beta2 * (sv * sv);
+    const float qm[4] = {square_m<0>(mw), square_m<1>(mw), square_m<2>(mw), square_m<3>(mw)};
+    const float qv[4] = {square_v<0>(vw), square_v<1>(vw), square_v<2>(vw), square_v<3>(vw)};
     double m4[4], v4[4];
+    float mf[4], root[4];
     uint32_t am = 0, av = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const double g = double(g4[e]) * scale;
-      m4[e] = fma(b1, value_m(int(int8_t(mw >> (8 * e))), sm), c1 * g);
-      v4[e] = fma(b2, value_v(int((vw >> (8 * e)) & 255u), sv), c2 * g * g);
-      const float mf = float(m4[e]), vf = float(v4[e]);
-      am = max(am, __float_as_uint(fabsf(mf)));
+      const double g = double(g4[e]), q = double(qv[e]);
+      m4[e] = fma(sm, double(qm[e]), c1 * g);
+      v4[e] = fma(sv2, q * q, c2 * (g * g));
+      mf[e] = float(m4[e]);
+      const float vf = float(v4[e]);
+      am = max(am, __float_as_uint(fabsf(mf[e])));
       av = max(av, __float_as_uint(vf) & 0x7FFFFFFFu);
-      p4[e] = stepped(p4[e], mf, vf, lr_wd, st);
+      root[e] = __builtin_amdgcn_sqrtf(vf);
+      p4[e] = stepped(p4[e], mf[e], root[e], lr_wd, st);
     }
-    const float nm = float(double(__uint_as_float(wave_max(am))) * (1.0 / 16129.0));
-    const float nv = float(sqrt(double(__uint_as_float(wave_max(av)))) * (1.0 / 65025.0));
-    const double dm = double(nm), dv = double(nv);
-    const double im = dm > 0.0 ? 1.0 / dm : 0.0, iv = dv > 0.0 ? 1.0 / (dv * dv) : 0.0;
+    store4(t.p, i, t.n, p4);
+    if (t.copy) store4(static_cast<__bf16*>(t.copy), i, t.n, p4);
+    wave_max2(am, av);
+    float nm = float(double(__uint_as_float(am)) * (1.0 / 16129.0));
+    float nv = float(sqrt(double(__uint_as_float(av))) * (1.0 / 65025.0));
+    nm = isfinite(nm) ? nm : __builtin_nanf("");
+    nv = isfinite(nv) ? nv : __builtin_nanf("");
+    const bool tiny_m = nm < kTinyM && nm > 0.0f, tiny_v = nv < kTinyV && nv > 0.0f;
+    const float im = nm > 0.0f ? __builtin_amdgcn_rcpf(nm) : 0.0f;
+    const float iv = nv > 0.0f ? __builtin_amdgcn_rcpf(nv) : 0.0f;
+    float tm[4], tv[4], cm[4], cv[4];
+    bool near = tiny_m || tiny_v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      tm[e] = __builtin_amdgcn_sqrtf(fabsf(mf[e]) * im);
+      tv[e] = __builtin_amdgcn_sqrtf(root[e] * iv);
+      cm[e] = rintf(tm[e]);
+      cv[e] = rintf(tv[e]);
+      near = near || near_border(tm[e], cm[e]) || near_border(tv[e], cv[e]);
+    }
+    if (near) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        cm[e] = nm > 0.0f ? code_exact<1>(tm[e], fabs(m4[e]), double(nm), tiny_m) : 0.0f;
+        cv[e] = nv > 0.0f ? code_exact<2>(tv[e], v4[e], double(nv), tiny_v) : 0.0f;
+      }
+    }
     uint32_t mo = 0, vo = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int c = code_m(fabs(m4[e]), dm, im);
-      mo |= (uint32_t(m4[e] < 0.0 ? -c : c) & 255u) << (8 * e);
-      vo |= uint32_t(code_v(v4[e], dv, iv)) << (8 * e);
+      const float c = copysignf(fminf(cm[e], 127.0f), mf[e]) + 128.0f;
+      mo = __builtin_amdgcn_cvt_pk_u8_f32(c, e, mo);
+      vo = __builtin_amdgcn_cvt_pk_u8_f32(v4[e] > 0.0 ? fmaxf(cv[e], 1.0f) : 0.0f, e, vo);
     }
-    store4(t.p, i, t.n, p4);
-    store_codes(mc, i, t.n, mo);
+    store_codes(mc, i, t.n, mo ^ kFlip);
     store_codes(vc, i, t.n, vo);
-    if (t.copy) store4(static_cast<__bf16*>(t.copy), i, t.n, p4);
     if (lane == 0) {
       t.m_scale[blk] = nm;
       t.v_scale[blk] = nv;
@@ -361,14 +416,17 @@ __global__ void __launch_bounds__(kParamThreads) k_moments8(const ParamList l) {
   float* mo = t.p;
   float* vo = static_cast<float*>(const_cast<void*>(t.grad));
   for (int64_t i = base + int(threadIdx.x) * 4; i < end; i += 4 * kParamThreads) {
-    const uint32_t mw = load_codes(static_cast<const uint8_t*>(t.m), i, t.n);
+    const uint32_t mw = load_codes(static_cast<const uint8_t*>(t.m), i, t.n) ^ kFlip;
     const uint32_t vw = load_codes(static_cast<const uint8_t*>(t.v), i, t.n);
     const double sm = double(t.m_scale[i / kQBlock]), sv = double(t.v_scale[i / kQBlock]);
+    const float qm[4] = {square_m<0>(mw), square_m<1>(mw), square_m<2>(mw), square_m<3>(mw)};
+    const float qv[4] = {square_v<0>(vw), square_v<1>(vw), square_v<2>(vw), square_v<3>(vw)};
     float m4[4], v4[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      m4[e] = float(value_m(int(int8_t(mw >> (8 * e))), sm));
-      v4[e] = float(value_v(int((vw >> (8 * e)) & 255u), sv));
+      const double r = sv * double(qv[e]);
+      m4[e] = float(sm * double(qm[e]));
+      v4[e] = float(r * r);
     }
     store4(mo, i, t.n, m4);
     store4(vo, i, t.n, v4);

@@ -420,7 +420,7 @@ struct ParamList {
 struct AdamArgs {
   double lr, beta1, beta2;
   int64_t step;
-  float lr_f, size, inv_c2, eps;  // lr, lr / (1 - beta1^step), 1 / (1 - beta2^step)
+  float lr_f, size, root, eps;  // lr, lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
   const int64_t* step_dev;        // device values in place of step and lr, or null
   const float* lr_dev;
   const float* grad_scale;        // device factor of the gradients, or null

@@ -79,7 +79,7 @@ class Net:
                 continue
             ms, vs = host(self.MS[i]), host(self.VS[i])
             for a, r in zip((ms, vs), R.scales(m, v)):
-                assert np.all(np.abs(a - r) <= 2.0 ** -23 * r), what
+                assert np.all(np.abs(a - r) <= np.maximum(2.0 ** -23 * r, 2.0 ** -149)), what
             for a, r, s, top, power in ((host(self.M[i]), np.abs(m), ms, 127, 1),
                                         (host(self.V[i]), v, vs, 255, 2)):
                 c, near = R.codes(r, s, top, power)
@@ -108,6 +108,15 @@ def test_first_steps_from_zero(gpu, bits):
     assert ms == vs == [None, None] if bits == 32 else torch.all(ms[0] == 0)
     gpu.adamw(net.list, 1, LR)
     net.check(gpu, 1)
+
+
+@pytest.mark.parametrize("scale", [1e-12, 1e-14, 1e-16, 1e-18, 1e-20, 1e8, 1e17])
+def test_gradients_of_any_size(gpu, scale):
+    # moments down to float32's smallest values and up to its largest; the scales' own float32
+    # rounding (absolute where they are subnormal) is taken from the GPU's
+    net = Net(gpu, [5000], 8, 4, scale=scale)
+    gpu.adamw(net.list, 3, LR)
+    net.check(gpu, 3)
 
 
 def test_mixed_list(gpu):
