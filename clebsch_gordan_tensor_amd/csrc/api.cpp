@@ -2506,7 +2506,7 @@ e3_status parse_params(int32_t n, const e3_param* p, bool grads, bool state,
   for (int32_t i = 0; i < n; ++i) {
     const e3_param& t = p[i];
     if (t.n < 0 || t.n > e3k::kMaxParamElements)
-      return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "n must be in [0, 2^35]");
+      return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "n must be in [0, 2^33]");
     if (grads && t.grad_dtype != E3_F32 && t.grad_dtype != E3_BF16)
       return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "unknown grad_dtype");
     if (t.n > 0 && grads && !t.grad) return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "null pointer");

@@ -409,9 +409,10 @@ struct ParamTensor {
   int grad_bf16;
 };
 constexpr int kParamsPerLaunch = 48;
-constexpr int kNormChunk = 16384;  // most elements of a workgroup of the gradients' norm
-constexpr int kAdamChunk = 4096;   // and of the step
-constexpr int64_t kMaxParamElements = int64_t(1) << 35;
+// most elements of a workgroup: of the gradients' norm, of the step with 8-bit
+// moments, of reading these back
+constexpr int kNormChunk = 65536, kAdamChunk = 4096, kReadChunk = 2048;
+constexpr int64_t kMaxParamElements = int64_t(1) << 33;
 struct ParamList {
   int n, chunk;  // tensors, elements of a workgroup
   int wg0[kParamsPerLaunch];  // first workgroup of each tensor

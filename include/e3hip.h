@@ -637,7 +637,7 @@ e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const 
  *   v[i] = (v_scale[i/256] c^2)^2, c uint8 in [0, 255].
  * All-zero codes and scales are zero moments. */
 typedef struct {
-  int64_t n;          /* elements, 0 <= n <= 2^35; an empty tensor is left out */
+  int64_t n;          /* elements, 0 <= n <= 2^33; an empty tensor is left out */
   float* p;           /* [n] the weights */
   const void* grad;   /* [n] their gradient, of type grad_dtype */
   void* m;            /* [n] first moment: float32, or int8 codes */
