@@ -1148,6 +1148,16 @@ def layer_norm_backward(irreps, x, weight, dy, eps=1e-5, flags=0, dx=None, dweig
 
 # ---------------------------------------------------------------- optimizer
 
+def _column(device, tensors, dtypes):
+    """Whether every one is a contiguous tensor of its dtype on `device` (a
+    list may hold hundreds: the whole column is looked at once)."""
+    import torch
+    T = torch.Tensor
+    return (all(isinstance(t, T) for t in tensors) and all(map(T.is_contiguous, tensors))
+            and set(map(T.get_device, tensors)) <= {device.index}
+            and [t.dtype for t in tensors] == dtypes)
+
+
 class Params:
     """The tensors of a network's weights with what their update reads and
     writes (lists of equal length; every tensor contiguous, on one GPU):
@@ -1210,33 +1220,50 @@ class Params:
 
     def _fill(self, field, name, dtypes, shapes=None, given=None):
         """One pointer of every tensor, after its checks."""
-        for i, t in enumerate(self._keep[name]):
-            if given is not None and not given[i]:
-                continue
-            at = f"{name}[{i}]"
-            _need(t, at)
-            _need_on(self.device, t, at, shapes[i] if shapes else None,
-                     dtypes[i] if isinstance(dtypes, list) else dtypes)
-            if shapes is None and t.numel() != self.sizes[i]:
-                raise ValueError(f"{at} has {t.numel()} elements, expected {self.sizes[i]}")
+        at = range(self._n) if given is None else [i for i in range(self._n) if given[i]]
+        ts = [self._keep[name][i] for i in at]
+        want = [dtypes[i] for i in at] if isinstance(dtypes, list) else [dtypes] * len(ts)
+        if not (_column(self.device, ts, want) and
+                ([t.shape for t in ts] == [shapes[i] for i in at] if shapes else
+                 [t.numel() for t in ts] == [self.sizes[i] for i in at])):
+            for i, t, dt in zip(at, ts, want):  # which one it is
+                _need(t, f"{name}[{i}]")
+                _need_on(self.device, t, f"{name}[{i}]", shapes[i] if shapes else None, dt)
+                if t.numel() != (self.sizes[i] if shapes is None else t.numel()):
+                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, "
+                                     f"expected {self.sizes[i]}")
+        for i, t in zip(at, ts):
             setattr(self._arr[i], field, t.data_ptr())
 
     def set_grads(self, grads):
         """Other gradient tensors for the same parameters."""
+        import torch
         if len(grads) != self._n:
             raise ValueError(f"grads has {len(grads)} tensors, expected {self._n}")
-        codes = []
-        for i, (g, p) in enumerate(zip(grads, self._keep["params"])):
-            _need(g, f"grads[{i}]")
-            _need_on(self.device, g, f"grads[{i}]", None if p is None else p.shape, None)
-            if g.numel() != self.sizes[i]:
-                raise ValueError(f"grads[{i}] has {g.numel()} elements, expected {self.sizes[i]}")
-            codes.append(_dtype_code(g))
-        for e, g, code in zip(self._arr, grads, codes):
-            e.grad, e.grad_dtype = g.data_ptr(), code
+        types = {torch.float32: E3_F32, torch.bfloat16: E3_BF16}
+        shapes = [g.shape if p is None else p.shape for g, p in zip(grads, self._keep["params"])]
+        if not (_column(self.device, grads, [g.dtype for g in grads])
+                and all(g.dtype in types for g in grads)
+                and [g.shape for g in grads] == shapes
+                and [g.numel() for g in grads] == self.sizes):
+            for i, g in enumerate(grads):  # which one it is
+                _need(g, f"grads[{i}]")
+                _need_on(self.device, g, f"grads[{i}]", shapes[i], None)
+                _dtype_code(g)
+                if g.numel() != self.sizes[i]:
+                    raise ValueError(f"grads[{i}] has {g.numel()} elements, "
+                                     f"expected {self.sizes[i]}")
+        before = [(e.grad, e.grad_dtype) for e in self._arr]
+        for e, g in zip(self._arr, grads):
+            e.grad, e.grad_dtype = g.data_ptr(), types[g.dtype]
+        try:
+            if self.updates:
+                _check(lib().e3_param_check(self._n, self._arr))
+        except E3Error:  # the list stays as it was
+            for e, (at, code) in zip(self._arr, before):
+                e.grad, e.grad_dtype = at, code
+            raise
         self._grads = list(grads)
-        if self.updates:
-            _check(lib().e3_param_check(self._n, self._arr))
 
     def __len__(self):
         return self._n
@@ -1321,14 +1348,12 @@ def adamw_moments(params: Params, m_out=None, v_out=None, stream=None):
             given = [torch.empty(k, device=dev, dtype=torch.float32) for k in params.sizes]
         if len(given) != n:
             raise ValueError(f"{name} has {len(given)} tensors, expected {n}")
-        T = torch.Tensor  # column by column: a list may hold hundreds
-        if not (list(map(T.numel, given)) == params.sizes and all(map(T.is_contiguous, given))
-                and set(map(T.get_device, given)) <= {dev.index}
-                and {t.dtype for t in given} <= {torch.float32}):
+        if not (_column(dev, given, [torch.float32] * n)
+                and list(map(torch.Tensor.numel, given)) == params.sizes):
             for i, (t, k) in enumerate(zip(given, params.sizes)):
                 _need_on(dev, _need(t, f"{name}[{i}]"), f"{name}[{i}]", None, torch.float32)
                 if t.numel() != k:
                     raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {k}")
-        outs.append((given, (C.c_void_p * max(1, n))(*map(T.data_ptr, given))))
+        outs.append((given, (C.c_void_p * max(1, n))(*map(torch.Tensor.data_ptr, given))))
     _on(dev, lib().e3_adamw_moments, n, params._arr, outs[0][1], outs[1][1], stream=stream)
     return outs[0][0], outs[1][0]

@@ -205,6 +205,37 @@ def test_rows_apart(gpu):
     assert not np.isfinite(got[5, 0, 3])
 
 
+def test_refused(gpu):
+    irreps = _ir("0e+1o")
+    x, dy, w, b = (dev(a) for a in _case(irreps, 6, 16, 14))
+    for call in (lambda: gpu.layer_norm(_ir("0e+2e"), x), lambda: gpu.layer_norm(irreps, x[0]),
+                 lambda: gpu.layer_norm(irreps, x.transpose(0, 2)),
+                 lambda: gpu.layer_norm(irreps, x, w[:1]), lambda: gpu.layer_norm(irreps, x, w, w),
+                 lambda: gpu.layer_norm(irreps, x, out=x[:5]),
+                 lambda: gpu.layer_norm(irreps, x, w.cpu()),
+                 lambda: gpu.layer_norm_backward(irreps, x, w, dy[:5]),
+                 lambda: gpu.layer_norm_backward(irreps, x, w, None),
+                 lambda: gpu.layer_norm_backward(irreps, x, w, dy, dbias=w)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: gpu.layer_norm(irreps, x.double()), lambda: gpu.layer_norm(irreps, x.half()),
+                 lambda: gpu.layer_norm(irreps, x, w.bfloat16()),
+                 lambda: gpu.layer_norm_backward(irreps, x, w, dy.bfloat16())):
+        with pytest.raises(TypeError):
+            call()
+    room = torch.zeros(x.numel() + 64, device="cuda")
+    room[:x.numel()] = x.view(-1)
+    inside, shifted = room[:x.numel()].view(x.shape), room[64:].view(x.shape)
+    with pytest.raises(gpu.E3Error, match="overlaps"):
+        gpu.layer_norm(irreps, inside, out=shifted)
+    with pytest.raises(gpu.E3Error, match="overlaps"):
+        gpu.layer_norm_backward(irreps, x, None, inside, dx=shifted)
+    with pytest.raises(gpu.E3Error, match="workspace"):
+        gpu.layer_norm_backward(irreps, x, w, dy, workspace=torch.empty(16, device="cuda"))
+    with pytest.raises(gpu.E3Error, match="eps"):
+        gpu.layer_norm(irreps, x, eps=0.0)
+
+
 def test_empty(gpu):
     irreps = _ir("0e+1o")
     e = torch.empty((0, 4, 16), device="cuda")

@@ -253,6 +253,64 @@ def test_step_and_lr_on_the_device(gpu, bits):
             assert torch.allclose(x.float(), y.float(), rtol=1e-6, atol=1e-9)
 
 
+def test_lists_refused(gpu):
+    net = Net(gpu, [300, 20], 8, 13)
+    good = dict(params=net.P, grads=net.G, m=net.M, v=net.V, m_scale=net.MS, v_scale=net.VS)
+    half = lambda ts: [t.to(torch.float16) for t in ts]  # noqa: E731
+    wide = torch.zeros((300, 2), device="cuda")[:, 0]
+    for over, error, text in (
+            (dict(grads=net.G[:1]), ValueError, "params has 2"),
+            (dict(grads=half(net.G)), TypeError, "dtype"),
+            (dict(params=half(net.P)), TypeError, r"params\[0\]"),
+            (dict(params=[net.P[0][:299], net.P[1]]), ValueError, r"params\[0\]"),
+            (dict(grads=[wide, net.G[1]]), ValueError, "contiguous"),
+            (dict(m=[net.M[0], net.M[1].float()]), TypeError, r"m\[1\]"),
+            (dict(v=[net.V[0][:299], net.V[1]]), ValueError, r"v\[0\]"),
+            (dict(m_scale=[net.MS[0], None]), ValueError, r"m_scale\[1\]"),
+            (dict(v_scale=[net.VS[0][:1], net.VS[1]]), ValueError, r"v_scale\[0\]"),
+            (dict(copies=[net.P[0], None]), TypeError, r"copies\[0\]"),
+            (dict(weight_decay=[0.1]), ValueError, "weight_decay"),
+            (dict(v=[net.M[0].view(torch.uint8), net.V[1]]), gpu.E3Error, "overlaps"),
+            (dict(params=[net.P[0], net.P[0][:20]]), gpu.E3Error, "overlaps")):
+        with pytest.raises(error, match=text):
+            gpu.Params(**{**good, **over})
+    # new gradients that overlap a parameter are refused, and the list works on with the old ones
+    with pytest.raises(gpu.E3Error, match="overlaps"):
+        net.list.set_grads([net.P[0], net.G[1]])
+    with pytest.raises(ValueError):
+        net.list.set_grads(net.G[:1])
+    gpu.adamw(net.list, 1, LR)
+    net.check(gpu, 1)
+    only = gpu.Params(grads=net.G)
+    for call in (lambda: gpu.adamw(only, 1, LR), lambda: gpu.adamw_moments(only),
+                 lambda: gpu.adamw_moments(net.list, [net.P[0]], [net.P[1]]),
+                 lambda: gpu.adamw_moments(net.list, net.P, [net.P[0], net.P[0]]),
+                 lambda: gpu.adamw(net.list, 1, LR, grad_scale=torch.ones(2, device="cuda")),
+                 lambda: gpu.adamw(net.list, 1, torch.ones(1)),
+                 lambda: gpu.grad_norm(only, out=torch.zeros(3, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: gpu.adamw(net.list, torch.ones(1, device="cuda"), LR),
+                 lambda: gpu.grad_norm(only, out=torch.zeros(2, device="cuda", dtype=torch.float64))):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(gpu.E3Error, match="codes"):
+        gpu.adamw_moments(Net(gpu, [5], 32, 1).list)
+
+
+def test_new_gradients_each_step(gpu):
+    # gradients that autograd allocates anew, a bf16 one among float32 ones
+    net = Net(gpu, [300, 20], [8, 32], 14)
+    for t in (1, 2):
+        net.G = [torch.randn(300, device="cuda"), torch.randn(20, device="cuda").bfloat16()]
+        net.g = [host(g) for g in net.G]
+        net.p, net.m, net.v = ([host(x) for x in c] for c in (net.P, net.M, net.V))
+        net.ms, net.vs = ([None if x is None else host(x) for x in c] for c in (net.MS, net.VS))
+        net.list.set_grads(net.G)
+        gpu.adamw(net.list, t, LR)
+        net.check(gpu, t)
+
+
 def test_long_tensor(gpu):
     # past 2^31 elements: the ends against the same values in a short list
     n, k = 2 ** 31 + 515, 1027
