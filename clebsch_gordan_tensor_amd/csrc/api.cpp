@@ -2403,9 +2403,17 @@ e3_status parse_norm(const e3_irreps* irreps, int64_t n_rows, int32_t flags, Nor
 
 e3_status norm_args(float eps, e3_dtype dtype) {
   if (dtype != E3_F32 && dtype != E3_BF16) return fail(E3_ERR_INVALID_ARG, "unknown dtype");
-  if (!(eps > 0.0f) || !std::isfinite(eps))
-    return fail(E3_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (!(eps > 0.0f) || !std::isnormal(eps))
+    return fail(E3_ERR_INVALID_ARG, "eps must be positive and normal");
   return E3_OK;
+}
+
+// For either storage type.
+size_t norm_workspace(const Norm& n, int64_t n_rows) {
+  const auto floats = [&](int esize) {
+    return e3k::norm_part_floats(n_rows, n.dim, n.C, n.blocks.data(), int(n.blocks.size()), esize);
+  };
+  return 4 * std::max(floats(2), floats(4));
 }
 
 // y (or dx) may be `in` itself, element for element, but not overlap it otherwise.
@@ -2449,7 +2457,7 @@ e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, 
   const e3_status s = parse_norm(irreps, n_rows, 0, n);
   if (s != E3_OK) return s;
   if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
-  *bytes = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), int(n.blocks.size()), 4);
+  *bytes = norm_workspace(n, n_rows);
   return ok();
 }
 
@@ -2462,7 +2470,7 @@ e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const 
   if ((s = parse_norm(irreps, n_rows, flags, n)) != E3_OK || (s = norm_args(eps, dtype)) != E3_OK)
     return s;
   const int nb = int(n.blocks.size());
-  const size_t need = 4 * e3k::norm_part_floats(n_rows, n.C, n.blocks.data(), nb, 4);
+  const size_t need = norm_workspace(n, n_rows);
   if (!workspace || ws_bytes < need)
     return fail(E3_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   if (n_rows > 0 && (!x || !dy || !dx)) return fail(E3_ERR_INVALID_ARG, "null pointer");

@@ -372,12 +372,14 @@ struct NormBlock {
   int bias;       // bias row, or -1
   int centered;
   int wg0, n_wg;
+  int slot;       // of this launch's scalars, or -1
 };
 struct NormArgs {
   int64_t n_rows;
   int dim, C;    // components of a row, channels
-  int group;     // lanes of a team within a wavefront
-  int n_blocks;
+  int group;     // lanes of a team
+  int whole;     // the team's vectors are exactly the row's channels
+  int n_blocks, n_scalars;
   const void* x;
   const void* dy;
   void* y;       // forward: y; backward: dx
@@ -385,12 +387,14 @@ struct NormArgs {
   const float* b;
   float* dw;
   float* db;
-  float* part;   // backward: [workgroup][dw, db][C]
+  float* part;   // backward: partials [slot][dw, db][C]
+  int part_step; // a block's partials lie in slots wg0, wg0 + part_step, ...
   float eps;
   NormBlock blk[kNormMaxBlocks];
 };
 // floats of `part` that launch_norm's backward needs
-size_t norm_part_floats(int64_t n_rows, int C, const NormBlock* blocks, int n_blocks, int esize);
+size_t norm_part_floats(int64_t n_rows, int dim, int C, const NormBlock* blocks, int n_blocks,
+                        int esize);
 hipError_t launch_norm(bool bwd, const NormArgs& a, const NormBlock* blocks, int n_blocks,
                        int bf16, hipStream_t s);
 

@@ -600,8 +600,9 @@ e3_status e3_linear_backward(const e3_irreps* in, const e3_irreps* out, int64_t 
  * x, y [n_rows][dim][C] in the storage type, every block of multiplicity C;
  * weight [n_blocks][C] and bias [number of 0e blocks][C] float32, either may
  * be NULL (1 and 0).  Statistics and products in float32, one rounding to
- * the storage type.  C up to 4096 (1024 when a degree is above 3), degrees up
- * to 8, at most 1024 blocks; eps > 0; pointers aligned to their element.
+ * the storage type; a row's result does not depend on the other rows.  C up to 4096 (1024 when a degree is above 3), degrees up
+ * to 8, at most 1024 blocks; eps a positive normal float; pointers aligned to
+ * their element.
  * y may be x, but must not overlap it otherwise.  A row that holds an
  * infinity or NaN gives NaN in that block and leaves the others alone. */
 enum { E3_NORM_UNCENTERED = 1 };
@@ -610,7 +611,7 @@ e3_status e3_layer_norm(const e3_irreps* irreps, int64_t n_rows, const void* x,
                         e3_dtype dtype, void* stream);
 
 /* Bytes of the workspace of e3_layer_norm_backward (partial sums of the
- * weight's and bias's gradients; about 12 KB per channel at most; host only). */
+ * weight's and bias's gradients; host only). */
 e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, size_t* bytes);
 
 /* Backward of e3_layer_norm for the cotangent dy [n_rows][dim][C]; the

@@ -79,6 +79,8 @@ def test_layer_norm_of_scalars(gpu, C, rows):
 @pytest.mark.parametrize("irreps,C", [
     ("0e+1o+2e+3o", 128), ("0e+1o", 8), ("0e+1o+1e+2e+2o+3o+3e", 64), ("0o+0e+0e+1o", 37),
     ("3o+0e", 3), ("2e", 1), ("0e+1o+2e+3o", 300), ("1o+0e", 2050),
+    ("0e+1o+2e+3o", 24), ("0e+1o", 50), ("1o+2e", 100), ("0e+4e+1o", 20), ("0e+1o+2e+3o", 1500),
+    ("0e+1o+2e+3o", 2), ("0e", 1100), ("0e", 2500), ("0e", 6), ("1o", 600),
     ("0e+1o+2e+3o+4e+5o+6e+7o+8e", 16), ("8e+0e", 5), ("7o+4e+1o", 512), ("5o+6e", 1024),
 ])
 @pytest.mark.parametrize("rows", [1, 53])
@@ -103,6 +105,34 @@ def test_many_blocks(gpu):
     # more blocks than one launch takes, low and high degrees mixed
     irreps = _ir("0e+1o+4e") * 45
     _check(gpu, irreps, *_case(irreps, 9, 4, 4))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("irreps,C", [("0e", 128), ("0e", 13), ("0e", 700), ("0e+1o+2e+3o", 128),
+                                      ("0e+1o", 9), ("0e+1o", 3), ("0e+1o", 300), ("4e+0e", 64)])
+def test_a_row_by_itself(gpu, irreps, C, dtype):
+    # a row's result is the same wherever it stands, alone or among others, bit for bit
+    irreps = _ir(irreps)
+    x, dy, w, b = _case(irreps, 1030, C, C, dtype)
+    X, D, W, B = dev(x, dtype), dev(dy, dtype), dev(w), dev(b)
+    y, dx = gpu.layer_norm(irreps, X, W, B), gpu.layer_norm_backward(irreps, X, W, D)[0]
+    for rows in ([0], [1029], [3, 700, 1028]):
+        at = torch.tensor(rows, device="cuda")
+        part, dpart = X[at].contiguous(), D[at].contiguous()
+        assert torch.equal(gpu.layer_norm(irreps, part, W, B), y[at])
+        assert torch.equal(gpu.layer_norm_backward(irreps, part, W, dpart)[0], dx[at])
+
+
+@pytest.mark.parametrize("irreps", ["0e", "0e+1o", "0e+0e"])
+def test_a_single_channel(gpu, irreps):
+    # a centred scalar of one channel is its own mean: y is the bias and dx zero, exactly
+    irreps = _ir(irreps)
+    x, dy, w, b = _case(irreps, 70, 1, 15)
+    y = host(gpu.layer_norm(irreps, dev(x), dev(w), dev(b)))
+    dx, dw, _ = (host(t) for t in gpu.layer_norm_backward(irreps, dev(x), dev(w), dev(dy)))
+    for i, (at, _, bias) in enumerate(R.blocks_of(irreps)):
+        if bias >= 0:
+            assert np.all(y[:, at] == b[bias]) and np.all(dx[:, at] == 0) and np.all(dw[i] == 0)
 
 
 def test_mean_far_from_zero(gpu):

@@ -41,7 +41,7 @@ def test_layer_norm_refusals(lib):
     mixed = api._Irreps(2, (api._Irrep * 2)(api._Irrep(4, 0, 1), api._Irrep(8, 1, -1)))
     for call, status in ((dict(ir=None), INVALID), (dict(rows=-1), INVALID), (dict(x=None), INVALID),
                          (dict(y=None), INVALID), (dict(eps=0.0), INVALID),
-                         (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
+                         (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(eps=1e-40), INVALID),
                          (dict(flags=2), INVALID), (dict(dtype=7), INVALID), (dict(ir=mixed), IRREPS),
                          (dict(ir=api._Irreps(0, None)), IRREPS), (dict(ir="9e"), UNSUPPORTED),
                          (dict(mul=4097), UNSUPPORTED), (dict(ir="4e", mul=1025), UNSUPPORTED),
@@ -73,7 +73,7 @@ def test_layer_norm_workspace(lib):
     last = 0
     for rows in (0, 1, 100, 10 ** 4, 10 ** 6, 10 ** 9):
         size = api.layer_norm_workspace_size([(0, 1), (1, -1)], rows, 128)
-        assert last <= size <= 13 * 1024 * 128
+        assert last <= size <= 32 * 1024 * 128
         last = size
 
 
