@@ -684,24 +684,26 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rows(const NormArgs a, in
   }
   if constexpr (BWD) {
     __syncthreads();  // there may have been no piece
-    for (int i = 0; i < nb; ++i) {
-      const NormBlock b = a.blk[i];
+    // a wavefront for each (block, channel) in turn
+    const int lane = tid & 63;
+    for (int p = tid >> 6; p < nb * a.C; p += kNormThreads / 64) {
+      const NormBlock b = a.blk[p / a.C];
+      const int k = p % a.C;
+      float s[2] = {0.0f, 0.0f};
+      for (int e = lane; e < groups * b.nc; e += 64) {
+        const int at = e / b.nc * row + (b.comp0 + e % b.nc) * a.C + k;
+        s[0] += sum_w[at];
+        s[1] += sum_b[at];
+      }
+      wave_team_sum(s, 64);
       const bool only = b.n_wg == 1;
-      float* ow = only ? (a.dw ? a.dw + int64_t(b.index) * a.C : nullptr)
-                       : a.part + (int64_t(blockIdx.x) * a.part_step + b.wg0) * 2 * a.C;
+      float* at = a.part + (int64_t(blockIdx.x) * a.part_step + b.wg0) * 2 * a.C;
+      float* ow = only ? (a.dw ? a.dw + int64_t(b.index) * a.C : nullptr) : at;
       float* ob = b.bias < 0 ? nullptr
                   : only     ? (a.db ? a.db + int64_t(b.bias) * a.C : nullptr)
-                             : ow + a.C;
-      for (int k = tid; k < a.C; k += kNormThreads) {
-        float sw = 0.0f, sb = 0.0f;
-        for (int q = 0; q < groups; ++q)
-          for (int c = 0; c < b.nc; ++c) {
-            sw += sum_w[q * row + (b.comp0 + c) * a.C + k];
-            sb += sum_b[q * row + (b.comp0 + c) * a.C + k];
-          }
-        if (ow) ow[k] = sw;
-        if (ob) ob[k] = sb;
-      }
+                             : at + a.C;
+      if (lane == 0 && ow) ow[k] = s[0];
+      if (lane == 0 && ob) ob[k] = s[1];
     }
   }
 }
@@ -782,23 +784,36 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_whole(const NormArgs a) {
     }
   }
   if constexpr (BWD) {
+    // the lanes that hold an element: 4 teams' in every thread, the threads of
+    // a wavefront by permutes, the rest (4 at most) in order
+    const int e = tid % per, stride = kNormThreads / per, wave = tid >> 6;
+    const int part = per < 64 ? wave : tid / per, parts = per < 64 ? kNormThreads / 64 : stride;
+    const int all = nb + a.n_scalars;
     __syncthreads();
-    for (int i = 0; i < nb + a.n_scalars; ++i) {
+    for (int i = 0; i < all; ++i) {
+      float* of = sums + i * lane_row(V);
+      float s = 0.0f;
+      for (int j = tid / per; j < teams; j += stride) s += of[j * per + e];
+      for (int o = per; o < 64; o <<= 1) s += __shfl_xor(s, o);
+      __syncthreads();
+      of[part * per + e] = s;
+    }
+    __syncthreads();
+    for (int idx = tid; idx < all * per; idx += kNormThreads) {
+      const int i = idx / per, el = idx - i * per;
       // block i's dw, or the db of the scalar in slot i - nb
       int of = i;
       if (i >= nb)
         for (of = 0; a.blk[of].slot != i - nb;) ++of;
       const NormBlock b = a.blk[of];
       const bool only = b.n_wg == 1;
-      float* part = a.part + (int64_t(blockIdx.x) * a.part_step + b.wg0) * 2 * a.C;
-      float* out = i < nb ? (only ? a.dw ? a.dw + int64_t(b.index) * a.C : nullptr : part)
-                          : (only ? a.db ? a.db + int64_t(b.bias) * a.C : nullptr : part + a.C);
-      for (int e = tid; e < per; e += kNormThreads) {
-        const Lane<V, 1> own(e / V, g, a.C);
-        float s = 0.0f;
-        for (int j = 0; j < teams; ++j) s += sums[i * lane_row(V) + j * per + e];
-        if (out && e % V >= own.skip[0]) out[own.k0[0] + e % V] = s;
-      }
+      float* at = a.part + (int64_t(blockIdx.x) * a.part_step + b.wg0) * 2 * a.C;
+      float* out = i < nb ? (only ? a.dw ? a.dw + int64_t(b.index) * a.C : nullptr : at)
+                          : (only ? a.db ? a.db + int64_t(b.bias) * a.C : nullptr : at + a.C);
+      const Lane<V, 1> own(el / V, g, a.C);
+      float s = 0.0f;
+      for (int j = 0; j < parts; ++j) s += sums[i * lane_row(V) + j * per + el];
+      if (out && el % V >= own.skip[0]) out[own.k0[0] + el % V] = s;
     }
   }
 }
