@@ -2616,8 +2616,8 @@ e3_status e3_adamw(int32_t n_params, const e3_param* params, const e3_adamw_args
   const e3_adamw_args& g = *args;
   if (!(g.beta1 >= 0.0 && g.beta1 < 1.0 && g.beta2 >= 0.0 && g.beta2 < 1.0))
     return fail(E3_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-  if (!(g.eps > 0.0) || !(float(g.eps) > 0.0f) || !std::isfinite(float(g.eps)))
-    return fail(E3_ERR_INVALID_ARG, "eps must be positive and finite in float32");
+  if (!(g.eps > 0.0) || !std::isnormal(float(g.eps)))
+    return fail(E3_ERR_INVALID_ARG, "eps must be positive and a normal float32");
   if (!g.lr_dev && !std::isfinite(g.lr)) return fail(E3_ERR_INVALID_ARG, "lr must be finite");
   if (!g.step_dev && g.step < 1) return fail(E3_ERR_INVALID_ARG, "step counts from 1");
   if (g.flags & ~int32_t(E3_ADAMW_SKIP_NONFINITE))

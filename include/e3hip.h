@@ -621,8 +621,10 @@ e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, 
  *   dweight[i][k] = sum_{r,m} dy xh      dbias[j][k] = sum_r dy   (float32)
  * dweight and dbias (either may be NULL: not wanted) are summed through fixed
  * partials in the caller's workspace (e3_layer_norm_workspace_size bytes,
- * 16-byte aligned): reproducible.  weight NULL: 1.  dx may be x or dy, but
- * must not overlap them otherwise.  n_rows = 0 gives zero dweight and dbias.
+ * 16-byte aligned; nothing in it has to be set or outlives the call, but
+ * calls that may overlap need one each): reproducible.  weight NULL: 1.  dx
+ * may be x or dy, but must not overlap them otherwise, and dweight, dbias and
+ * the workspace nothing.  n_rows = 0 gives zero dweight and dbias.
  * Limits and alignment as the forward. */
 e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const void* x,
                                  const float* weight, const void* dy, float eps, int32_t flags,
@@ -661,7 +663,8 @@ e3_status e3_param_check(int32_t n_params, const e3_param* params);
  * clips it: out[0] = norm, out[1] = min(1, max_norm / (norm + 1e-6)), float32
  * on the device (for e3_adamw's grad_scale: no synchronisation).  Squares and
  * sums in 64 bits, through fixed partials in the caller's workspace
- * (e3_grad_norm_workspace_size bytes, 8-byte aligned): reproducible.
+ * (e3_grad_norm_workspace_size bytes, 8-byte aligned, one for each of calls
+ * that may overlap): reproducible.
  * max_norm > 0 (INFINITY: never clips).  A norm that is not finite gives the
  * factor NaN.  Only n, grad and grad_dtype of the tensors are used. */
 e3_status e3_grad_norm_workspace_size(int32_t n_params, const e3_param* params, size_t* bytes);
@@ -690,7 +693,7 @@ e3_status e3_grad_norm(int32_t n_params, const e3_param* params, double max_norm
  * The tensors must pass e3_param_check; overlap is not checked again. */
 enum { E3_ADAMW_SKIP_NONFINITE = 1 };
 typedef struct {
-  double lr, beta1, beta2, eps; /* lr finite; 0 <= beta < 1; eps > 0 */
+  double lr, beta1, beta2, eps; /* lr finite; 0 <= beta < 1; eps > 0, normal in float32 */
   int64_t step;                 /* t, 1 for the first update */
   const int64_t* step_dev;      /* device, or NULL */
   const float* lr_dev;          /* device, or NULL */
@@ -702,7 +705,8 @@ e3_status e3_adamw(int32_t n_params, const e3_param* params, const e3_adamw_args
 
 /* 8-bit moments as float32 (for inspection, checkpoints, another optimizer):
  * m_out[i] and v_out[i] (HOST arrays of device pointers, float32 [n]) of
- * tensor i, whose moments must be codes. */
+ * tensor i, whose moments must be codes; they must overlap nothing of the
+ * list. */
 e3_status e3_adamw_moments(int32_t n_params, const e3_param* params, float* const* m_out,
                            float* const* v_out, void* stream);
 

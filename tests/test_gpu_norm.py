@@ -80,7 +80,7 @@ def test_layer_norm_of_scalars(gpu, C, rows):
     ("0e+1o+2e+3o", 128), ("0e+1o", 8), ("0e+1o+1e+2e+2o+3o+3e", 64), ("0o+0e+0e+1o", 37),
     ("3o+0e", 3), ("2e", 1), ("0e+1o+2e+3o", 300), ("1o+0e", 2050),
     ("0e+1o+2e+3o", 24), ("0e+1o", 50), ("1o+2e", 100), ("0e+4e+1o", 20), ("0e+1o+2e+3o", 1500),
-    ("0e+1o+2e+3o", 2), ("0e", 1100), ("0e", 2500), ("0e", 6), ("1o", 600),
+    ("0e+1o+2e+3o", 2), ("0e+3o", 4096), ("8e+0e", 1024), ("0e", 1100), ("0e", 2500), ("0e", 6), ("1o", 600),
     ("0e+1o+2e+3o+4e+5o+6e+7o+8e", 16), ("8e+0e", 5), ("7o+4e+1o", 512), ("5o+6e", 1024),
 ])
 @pytest.mark.parametrize("rows", [1, 53])
@@ -101,10 +101,33 @@ def test_many_rows(gpu):
     _check(gpu, irreps, *_case(irreps, 5003, 48, 3))
 
 
-def test_many_blocks(gpu):
+@pytest.mark.parametrize("C", [3, 4, 64])
+def test_many_blocks(gpu, C):
     # more blocks than one launch takes, low and high degrees mixed
     irreps = _ir("0e+1o+4e") * 45
-    _check(gpu, irreps, *_case(irreps, 9, 4, 4))
+    _check(gpu, irreps, *_case(irreps, 9, C, 4))
+
+
+@pytest.mark.parametrize("irreps,C,rows", [("0e", 64, 40), ("0e", 64, 4000), ("0e+1o", 9, 700),
+                                           ("0e+1o", 2, 3000), ("0e+1o+2e", 64, 900)])
+def test_gradients_not_wanted(gpu, irreps, C, rows):
+    # dweight, dbias or both left out (NULL): the others are the same
+    import ctypes
+    irreps = _ir(irreps)
+    x, dy, w, _ = (dev(a) for a in _case(irreps, rows, C, 16))
+    ref = gpu.layer_norm_backward(irreps, x, w, dy)
+    st = gpu._irreps_struct(irreps, C)
+    ws = torch.empty(gpu.layer_norm_workspace_size(irreps, rows, C), device="cuda",
+                     dtype=torch.uint8)
+    for want_w, want_b in ((0, 1), (1, 0), (0, 0)):
+        got = [torch.full_like(t, 3.0) for t in ref]
+        at = [got[0].data_ptr(), got[1].data_ptr() if want_w else None,
+              got[2].data_ptr() if want_b else None]
+        assert gpu.lib().e3_layer_norm_backward(
+            ctypes.byref(st), rows, x.data_ptr(), w.data_ptr(), dy.data_ptr(), EPS, 0, *at,
+            ws.data_ptr(), ws.numel(), 0, torch.cuda.current_stream().cuda_stream) == 0
+        for t, r, want in zip(got, ref, (1, want_w, want_b)):
+            assert torch.equal(t, r) if want else torch.all(t == 3.0)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

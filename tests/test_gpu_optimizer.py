@@ -63,11 +63,11 @@ class Net:
             return R.decode(self.m[i], self.v[i], self.ms[i], self.vs[i])
         return self.m[i].astype(np.float64), self.v[i].astype(np.float64)
 
-    def check(self, gpu, t, lr=LR, scale=1.0):
+    def check(self, gpu, t, lr=LR, scale=1.0, **betas):
         for i in range(len(self.p)):
             n = self.p[i].size
             (p, m, v), (tp, tm, tv) = R.adamw(self.p[i], self.g[i], *self.values(i), t, lr,
-                                              float(np.float32(self.decay[i])), scale=scale)
+                                              float(np.float32(self.decay[i])), scale=scale, **betas)
             what = f"tensor {i} ({n} elements, {self.bits[i]} bits)"
             got = host(self.P[i]).astype(np.float64)
             assert np.all(np.abs(got - p) <= tp), (what, np.max(np.abs(got - p) / tp))
@@ -117,6 +117,22 @@ def test_gradients_of_any_size(gpu, scale):
     net = Net(gpu, [5000], 8, 4, scale=scale)
     gpu.adamw(net.list, 3, LR)
     net.check(gpu, 3)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("b1,b2,eps", [(0.0, 0.0, 1e-8), (0.0, 0.99, 1e-3), (0.95, 0.0, 1e-30),
+                                       (0.5, 0.9999, 1.0)])
+def test_other_constants(gpu, b1, b2, eps, bits):
+    net = Net(gpu, [1000, 77], bits, 17)
+    gpu.adamw(net.list, 5, LR, beta1=b1, beta2=b2, eps=eps)
+    net.check(gpu, 5, b1=b1, b2=b2, eps=eps)
+
+
+def test_a_count_below_one_is_one(gpu):
+    a, b = (Net(gpu, [300], 32, 18) for _ in range(2))
+    gpu.adamw(a.list, torch.full((1,), -4, device="cuda", dtype=torch.int64), LR)
+    gpu.adamw(b.list, 1, LR)
+    assert torch.allclose(a.P[0], b.P[0], rtol=1e-6, atol=1e-7)
 
 
 def test_mixed_list(gpu):

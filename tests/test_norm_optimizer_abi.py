@@ -139,7 +139,7 @@ def test_grad_norm_refusals(lib):
 
 @pytest.mark.parametrize("over", [
     dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.5), dict(beta2=float("nan")), dict(eps=0.0),
-    dict(eps=1e-60), dict(eps=float("inf")), dict(lr=float("nan")), dict(step=0), dict(flags=2),
+    dict(eps=1e-60), dict(eps=1e-40), dict(eps=float("inf")), dict(lr=float("nan")), dict(step=0), dict(flags=2),
     dict(flags=1),
 ])
 def test_adamw_refusals(lib, over):
