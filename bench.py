@@ -17,7 +17,8 @@ and mean of the fastest 20%).
 Side measurements (in "kernels", outside the step): the chain from the
 harmonic cotangent dY to per-atom position gradients on the same graph, the
 batched tensor product forward and backward on its 200,000-row workload, the
-per-irrep channel mixing on the matrix cores, and the radial-MLP forms.
+per-irrep channel mixing on the matrix cores, the normalisation and the
+clipped AdamW step, and the radial-MLP forms.
 "configs": the other convolution workloads (tiny 64-atom, water3k 3,000-atom
 with radial-MLP weights, ho20k 20,000-atom bf16 with 23 paths), each with
 algorithmic bytes and the method's flops against the HBM and fp32 VALU peaks
@@ -221,6 +222,48 @@ def linear_measurement(api, S, p, dev, stream):
     log(f"[bench] channel mixing {N}x{d}x{C}: forward {r['ms']*1e3:.1f} us "
         f"({r['tflops']:.1f} TFLOP/s), backward {b['ms']*1e3:.1f} us ({b['tflops']:.1f} TFLOP/s)")
     return {"linear_fp32_mfma": r, "linear_backward_fp32_mfma": b}
+
+
+def training_measurement(api, S, p, dev, stream):
+    """What training adds to the layers: the normalisation of the workload's
+    output features with its gradients, and the clipped AdamW step over the
+    weights of twelve layers (channel mixings, radial MLP, normalisations),
+    moments in 32 and in 8 bits."""
+    import torch
+    ir, N, C = p.out_irreps, p.graph.n_nodes, p.channels
+    g = torch.Generator(device=dev).manual_seed(0)
+    x = torch.randn((N, S.dim(ir), C), device=dev, generator=g)
+    dy = torch.randn((N, S.dim(ir), C), device=dev, generator=g)
+    w, b = torch.ones((len(ir), C), device=dev), torch.zeros((1, C), device=dev)
+    y, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    ws = torch.empty(api.layer_norm_workspace_size(ir, N, C), device=dev, dtype=torch.uint8)
+    f = time_call(lambda: api.layer_norm(ir, x, w, b, out=y), stream, 100)
+    r = time_call(lambda: api.layer_norm_backward(ir, x, w, dy, dx=y, dweight=dw, dbias=db,
+                                                  workspace=ws), stream, 100)
+    for rec, n in ((f, 2), (r, 3)):
+        rec["bytes"] = n * 4 * x.numel()
+        rec["gbs"] = rec["bytes"] / (rec["ms"] * 1e-3) / 1e9
+    del x, dy, y
+    sizes = [len(ir) * C * C, 2 * C * C, 8 * 64, 64 * p.n_paths * C, len(ir) * C, C] * 12
+    params = [torch.randn(n, device=dev, generator=g) for n in sizes]
+    grads = [torch.randn(n, device=dev, generator=g) for n in sizes]
+    out = {"layer_norm": f, "layer_norm_backward": r}
+    for bits in (32, 8):
+        m, v, ms, vs = api.adamw_state(params, bits)
+        ps = api.Params(params, grads, m, v, m_scale=ms, v_scale=vs, weight_decay=0.01)
+
+        def update():
+            norm = api.grad_norm(ps, max_norm=1.0)
+            api.adamw(ps, 1, 1e-4, grad_scale=norm[1:])
+
+        out[f"clipped_adamw_{bits}bit"] = time_call(update, stream, 100)
+        out[f"clipped_adamw_{bits}bit"]["elements"] = sum(sizes)
+    log(f"[bench] normalisation {N}x{S.dim(ir)}x{C}: forward {f['ms']*1e3:.1f} us "
+        f"({f['gbs']:.0f} GB/s), backward {r['ms']*1e3:.1f} us ({r['gbs']:.0f} GB/s); clipped AdamW "
+        f"over {sum(sizes)} weights in {len(sizes)} tensors: "
+        + ", ".join(f"{out[f'clipped_adamw_{k}bit']['ms']*1e3:.1f} us ({k}-bit moments)"
+                    for k in (32, 8)))
+    return out
 
 
 MFMA_F16_PEAK_TFLOPS = 2500.0
@@ -675,6 +718,7 @@ def main():
         del dvec, dpos
         extras.update(tp_measurements(api, S, dev, stream))
         extras.update(linear_measurement(api, S, p, dev, stream))
+        extras.update(training_measurement(api, S, p, dev, stream))
         if p.dtype == "f32":
             extras.update(radial_measurement(api, d, g, rowptr, sender, ev, x, dwo, ws, dev,
                                              stream))

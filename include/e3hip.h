@@ -14,7 +14,9 @@
  * and the chain from the harmonic cotangent to per-atom position gradients
  * (conservative forces F = -dE/dpos, "Ab Initio Accuracy Beyond the Cutoff:
  * Distributed Message-Passing Equivariant Attention at Tens-of-Millions-of-
- * Atom Scale", cited as Tessera, 2.2 Eq.3).
+ * Atom Scale", cited as Tessera, 2.2 Eq.3).  Next to it: the channel mixing
+ * within irreps, the radial edge weights, and for training the normalisation
+ * of irreps features, the norm of all gradients and the AdamW step.
  *
  * Conventions
  *   - An irreps list is a sequence of (l, parity) blocks; a block of degree l
