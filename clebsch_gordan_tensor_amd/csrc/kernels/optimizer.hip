@@ -39,6 +39,7 @@ constexpr int kQBlock = 256;  // elements per scale
 constexpr int kPass = 4 * kParamThreads;  // elements a workgroup takes at once
 constexpr int64_t kMaxWorkgroups = (int64_t(1) << 32) / kParamThreads - 1;  // 2^32 threads a launch
 static_assert(sizeof(ParamList) + sizeof(AdamArgs) <= 4096, "kernel arguments");
+static_assert(sizeof(GradList) + sizeof(double*) <= 4096, "kernel arguments");
 static_assert(kMaxParamElements / kPass < kMaxWorkgroups);
 
 // Four consecutive elements, those at n and beyond 0.  The step streams (61M
@@ -113,11 +114,16 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, ui
 
 // The tensor this workgroup belongs to: a lane per tensor compares, one load
 // deep (walking the list took 0.1 us a tensor).
-__device__ __forceinline__ int tensor_of(const ParamList& l) {
-  static_assert(kParamsPerLaunch <= 64);
+template <int N>
+__device__ __forceinline__ int tensor_of(const int (&wg0)[N], int n) {
   const int lane = threadIdx.x & 63;
-  const bool below = lane < l.n && l.wg0[min(lane, kParamsPerLaunch - 1)] <= int(blockIdx.x);
-  return __popcll(__ballot(below)) - 1;
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 64) {
+    const bool below = i + lane < n && wg0[min(i + lane, N - 1)] <= int(blockIdx.x);
+    before += __popcll(__ballot(below));
+  }
+  return before - 1;
 }
 
 // ------------------------------------------------------- the gradients' norm
@@ -157,14 +163,14 @@ __device__ __forceinline__ double sum_squares(const T* p, int64_t base, int64_t 
 
 // One partial per workgroup; squares and sums in 64 bits, so no gradient of
 // float32's range overflows and the order of summation does not show.
-__global__ void __launch_bounds__(kParamThreads) k_grad_norm(const ParamList l, double* part) {
+__global__ void __launch_bounds__(kParamThreads) k_grad_norm(const GradList l, double* part) {
   __shared__ double s_sum[kParamThreads / 64];
-  const int ti = tensor_of(l);
-  const ParamTensor t = l.t[ti];
+  const int ti = tensor_of(l.wg0, l.n);
+  const int64_t size = l.size[ti], n = size < 0 ? ~size : size;
   const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * l.chunk;
-  const int64_t end = min(t.n, base + l.chunk);
-  double s = t.grad_bf16 ? sum_squares(static_cast<const __bf16*>(t.grad), base, end)
-                         : sum_squares(static_cast<const float*>(t.grad), base, end);
+  const int64_t end = min(n, base + l.chunk);
+  double s = size < 0 ? sum_squares(static_cast<const __bf16*>(l.grad[ti]), base, end)
+                      : sum_squares(static_cast<const float*>(l.grad[ti]), base, end);
   s = wave_sum64(s);
   if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -236,7 +242,7 @@ __device__ __forceinline__ float stepped(float p, float m, float root_v, float l
 __global__ void __launch_bounds__(kParamThreads) k_adamw(const ParamList l, const AdamArgs a) {
   const Step st = step_of(a);
   if (st.skip) return;
-  const int ti = tensor_of(l);
+  const int ti = tensor_of(l.wg0, l.n);
   const ParamTensor t = l.t[ti];
   const int64_t i = int64_t(int(blockIdx.x) - l.wg0[ti]) * kPass + int(threadIdx.x) * 4;
   if (i >= t.n) return;
@@ -334,7 +340,7 @@ __device__ float code_exact(float t, double value, double s, bool tiny) {
 __global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, const AdamArgs a) {
   const Step st = step_of(a);
   if (st.skip) return;
-  const int ti = tensor_of(l);
+  const int ti = tensor_of(l.wg0, l.n);
   const ParamTensor t = l.t[ti];
   const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * l.chunk;
   const int64_t end = min(t.n, base + l.chunk);
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kParamThreads) k_adamw8(const ParamList l, con
 
 // The moments as float32: p and grad hold the destinations of m and v.
 __global__ void __launch_bounds__(kParamThreads) k_moments8(const ParamList l) {
-  const int ti = tensor_of(l);
+  const int ti = tensor_of(l.wg0, l.n);
   const ParamTensor t = l.t[ti];
   const int64_t base = int64_t(int(blockIdx.x) - l.wg0[ti]) * l.chunk;
   const int64_t end = min(t.n, base + l.chunk);
@@ -490,15 +496,27 @@ size_t grad_norm_partials(const ParamTensor* t, int n) {
 
 hipError_t launch_grad_norm(const ParamTensor* t, int n, double max_norm, double* part, float* out,
                             hipStream_t s) {
-  int64_t done = 0;
-  const hipError_t e = for_lists(
-      t, n, chunk_of(t, n, kPass, kNormChunk), [](const ParamTensor&) { return true; },
-      [&](const ParamList& l, unsigned wgs) {
-        hipLaunchKernelGGL(k_grad_norm, dim3(wgs), dim3(kParamThreads), 0, s, l, part + done);
-        done += wgs;
-        return hipGetLastError();
-      });
-  if (e != hipSuccess) return e;
+  GradList l;
+  l.n = 0;
+  l.chunk = int(chunk_of(t, n, kPass, kNormChunk));
+  int64_t done = 0, wgs = 0;
+  for (int i = 0; i <= n; ++i) {
+    const int64_t w = i < n ? (t[i].n + l.chunk - 1) / l.chunk : 0;
+    if (l.n > 0 && (i == n || l.n == kGradsPerLaunch || wgs + w > kMaxWorkgroups)) {
+      hipLaunchKernelGGL(k_grad_norm, dim3(unsigned(wgs)), dim3(kParamThreads), 0, s, l,
+                         part + done);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      done += wgs;
+      l.n = 0;
+      wgs = 0;
+    }
+    if (w == 0) continue;
+    l.wg0[l.n] = int(wgs);
+    l.size[l.n] = t[i].grad_bf16 ? ~t[i].n : t[i].n;
+    l.grad[l.n++] = t[i].grad;
+    wgs += w;
+  }
   hipLaunchKernelGGL(k_grad_norm_total, dim3(1), dim3(1024), 0, s, done, part, max_norm, out);
   return hipGetLastError();
 }

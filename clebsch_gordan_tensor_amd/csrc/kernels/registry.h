@@ -422,6 +422,14 @@ struct ParamList {
   int wg0[kParamsPerLaunch];  // first workgroup of each tensor
   ParamTensor t[kParamsPerLaunch];
 };
+// the gradients alone, for their norm
+constexpr int kGradsPerLaunch = 192;
+struct GradList {
+  int n, chunk;
+  int wg0[kGradsPerLaunch];
+  int64_t size[kGradsPerLaunch];  // elements, complemented where bf16
+  const void* grad[kGradsPerLaunch];
+};
 struct AdamArgs {
   double lr, beta1, beta2;
   int64_t step;

@@ -214,7 +214,8 @@ def test_not_finite(gpu):
 
 
 @pytest.mark.parametrize("grad", ["f32", "bf16"])
-@pytest.mark.parametrize("sizes", [[1], [255, 3], [16384, 16385, 1], [3_000_001, 70000] + [17] * 60])
+@pytest.mark.parametrize("sizes", [[1], [255, 3], [16384, 16385, 1], [3_000_001, 70000] + [17] * 60,
+                                   [n % 977 for n in range(1, 4000, 9)]])
 def test_grad_norm(gpu, sizes, grad):
     rng = np.random.default_rng(len(sizes))
     g = [(rng.standard_normal(n) * 0.1).astype(np.float32) for n in sizes]
