@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import operator
 import os
 from dataclasses import dataclass
 
@@ -1049,6 +1050,9 @@ def _on(device, fn, *args, stream=None):
         _check(status)
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -1153,9 +1157,12 @@ def _column(device, tensors, dtypes):
     list may hold hundreds: the whole column is looked at once)."""
     import torch
     T = torch.Tensor
-    return (all(isinstance(t, T) for t in tensors) and all(map(T.is_contiguous, tensors))
-            and set(map(T.get_device, tensors)) <= {device.index}
-            and [t.dtype for t in tensors] == dtypes)
+    try:
+        return (all(map(T.is_contiguous, tensors))
+                and set(map(T.get_device, tensors)) <= {device.index}
+                and list(map(_dtype_of, tensors)) == dtypes)
+    except TypeError:  # something else than a tensor
+        return False
 
 
 class Params:
