@@ -1053,6 +1053,16 @@ def _on(device, fn, *args, stream=None):
 _dtype_of = operator.attrgetter("dtype")
 
 
+def _new(stream, shape, device, dtype):
+    """Memory for a call on `stream`: of that stream's own, since work still
+    queued on the current one may use what it frees."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, device=device, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=device, dtype=dtype)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -1106,7 +1116,7 @@ def layer_norm(irreps, x, weight=None, bias=None, eps=1e-5, flags=0, out=None, s
     _need_on(dev, weight, "weight", (n_blocks, shape[2]), torch.float32)
     _need_on(dev, bias, "bias", (scalars, shape[2]), torch.float32)
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(stream, shape, dev, x.dtype)
     else:
         _need_on(dev, out, "out", shape, x.dtype)
     _on(dev, lib().e3_layer_norm, C.byref(st), shape[0], x.data_ptr(), _addr(weight), _addr(bias),
@@ -1135,14 +1145,13 @@ def layer_norm_backward(irreps, x, weight, dy, eps=1e-5, flags=0, dx=None, dweig
     _need_on(dev, dbias, "dbias", (scalars, ch), f32)
     _need_on(dev, workspace, "workspace", None, None)
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = _new(stream, shape, dev, x.dtype)
     if dweight is None:
-        dweight = torch.empty((n_blocks, ch), device=dev, dtype=f32)
+        dweight = _new(stream, (n_blocks, ch), dev, f32)
     if dbias is None:
-        dbias = torch.empty((scalars, ch), device=dev, dtype=f32)
+        dbias = _new(stream, (scalars, ch), dev, f32)
     if workspace is None:
-        workspace = torch.empty(_norm_workspace_size(irreps, shape[0], ch), device=dev,
-                                dtype=torch.uint8)
+        workspace = _new(stream, _norm_workspace_size(irreps, shape[0], ch), dev, torch.uint8)
     _on(dev, lib().e3_layer_norm_backward, C.byref(st), shape[0], x.data_ptr(), _addr(weight),
         dy.data_ptr(), eps, flags, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _dtype_code(x),
@@ -1303,9 +1312,9 @@ def grad_norm(params: Params, max_norm=float("inf"), out=None, workspace=None, s
     _need_on(dev, out, "out", (2,), torch.float32)
     _need_on(dev, workspace, "workspace", None, None)
     if out is None:
-        out = torch.empty(2, device=dev, dtype=torch.float32)
+        out = _new(stream, 2, dev, torch.float32)
     if workspace is None:
-        workspace = torch.empty(params.workspace_bytes, device=dev, dtype=torch.uint8)
+        workspace = _new(stream, params.workspace_bytes, dev, torch.uint8)
     _on(dev, lib().e3_grad_norm, len(params), params._arr, max_norm, out.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
     return out
@@ -1352,7 +1361,7 @@ def adamw_moments(params: Params, m_out=None, v_out=None, stream=None):
     outs = []
     for given, name in ((m_out, "m_out"), (v_out, "v_out")):
         if given is None:
-            given = [torch.empty(k, device=dev, dtype=torch.float32) for k in params.sizes]
+            given = [_new(stream, k, dev, torch.float32) for k in params.sizes]
         if len(given) != n:
             raise ValueError(f"{name} has {len(given)} tensors, expected {n}")
         if not (_column(dev, given, [torch.float32] * n)

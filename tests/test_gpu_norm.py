@@ -315,6 +315,30 @@ def test_reproducible_and_streams(gpu):
         assert torch.equal(a, c) and torch.equal(b_, c)
 
 
+def test_memory_of_another_stream(gpu):
+    # what a call on another stream allocates must not be memory that work queued on the current
+    # stream still writes
+    irreps = _ir("0e+1o")
+    x, dy, w, b = (dev(a) for a in _case(irreps, 2000, 64, 17))
+    ref = (gpu.layer_norm(irreps, x, w, b), *gpu.layer_norm_backward(irreps, x, w, dy))
+    norm = gpu.grad_norm(gpu.Params(grads=[x]))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    ws = gpu.layer_norm_workspace_size(irreps, 2000, 64)
+    old = [torch.empty_like(t) for t in (*ref, norm)]
+    old += [torch.empty(n, device="cuda", dtype=torch.uint8) for n in (ws, 8 * 512)]
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for t in old:
+        t.fill_(7)
+    del old, t
+    got = (gpu.layer_norm(irreps, x, w, b, stream=side),
+           *gpu.layer_norm_backward(irreps, x, w, dy, stream=side))
+    got_norm = gpu.grad_norm(gpu.Params(grads=[x]), stream=side)
+    torch.cuda.synchronize()
+    for a, c in zip((*got, got_norm), (*ref, norm)):
+        assert torch.equal(a, c)
+
+
 def test_beyond_32_bit_offsets(gpu):
     # 2^31 + 2^20 elements: the first, middle and last rows
     irreps, C = _ir("0e+1o"), 128
