@@ -132,7 +132,8 @@ def test_gradients_not_wanted(gpu, irreps, C, rows):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("irreps,C", [("0e", 128), ("0e", 13), ("0e", 700), ("0e+1o+2e+3o", 128),
-                                      ("0e+1o", 9), ("0e+1o", 3), ("0e+1o", 300), ("4e+0e", 64)])
+                                      ("0e+1o", 9), ("0e+1o", 3), ("0e+1o", 300), ("4e+0e", 64),
+                                      ("4e+0e", 9), ("6e+0e", 300)])
 def test_a_row_by_itself(gpu, irreps, C, dtype):
     # a row's result is the same wherever it stands, alone or among others, bit for bit
     irreps = _ir(irreps)
@@ -194,9 +195,10 @@ def test_gradient_against_differences(gpu):
         assert abs(num - ref) <= 1e-5 * np.abs(grad * d).sum(), at
 
 
-@pytest.mark.parametrize("C", [5, 128, 1000])
-def test_in_place(gpu, C):
-    irreps = _ir("0e+1o")
+@pytest.mark.parametrize("irreps,C", [(ir, C) for ir in ("0e+1o", "4e+0e") for C in (2, 5, 50, 128, 300, 1000)] +
+                         [("0e+1o", 2050)])
+def test_in_place(gpu, C, irreps):
+    irreps = _ir(irreps)
     x, dy, w, b = _case(irreps, 33, C, 10 + C)
     X, D, W, B = dev(x), dev(dy), dev(w), dev(b)
     y = gpu.layer_norm(irreps, X, W, B)
