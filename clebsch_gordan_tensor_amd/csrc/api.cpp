@@ -2649,9 +2649,11 @@ e3_status e3_adamw_moments(int32_t n_params, const e3_param* params, float* cons
   if (s != E3_OK) return s;
   if (n_params > 0 && (!m_out || !v_out)) return fail(E3_ERR_INVALID_ARG, "null pointer");
   for (int32_t i = 0; i < n_params; ++i) {
+    // an empty tensor is left out; its zero-length scales may have no address
+    if (t[i].n == 0) continue;
     if (!t[i].m_scale)
       return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "its moments are not 8-bit codes");
-    if (t[i].n > 0 && (!m_out[i] || !v_out[i]))
+    if (!m_out[i] || !v_out[i])
       return fail(E3_ERR_INVALID_ARG, tensor_at(i) + "null pointer");
     if (!aligned_to(m_out[i], 4) || !aligned_to(v_out[i], 4))
       return fail(E3_ERR_ALIGNMENT, tensor_at(i) + "outputs must be 4-byte aligned");

@@ -707,8 +707,8 @@ e3_status e3_adamw(int32_t n_params, const e3_param* params, const e3_adamw_args
 
 /* 8-bit moments as float32 (for inspection, checkpoints, another optimizer):
  * m_out[i] and v_out[i] (HOST arrays of device pointers, float32 [n]) of
- * tensor i, whose moments must be codes; they must overlap nothing of the
- * list. */
+ * tensor i, whose moments must be codes (an empty tensor is left out); they
+ * must overlap nothing of the list. */
 e3_status e3_adamw_moments(int32_t n_params, const e3_param* params, float* const* m_out,
                            float* const* v_out, void* stream);
 

@@ -169,6 +169,21 @@ def test_moments_read_back(gpu):
         assert np.array_equal(host(v), rv.astype(np.float32))
 
 
+def test_moments_read_back_with_empty_tensors(gpu):
+    # a list as adamw_state makes it, first, middle and last tensor empty
+    net = Net(gpu, [0, 300, 0, 257, 0], 8, 22)
+    gpu.adamw(net.list, 3, LR)
+    net.m, net.v, net.ms, net.vs = ([host(x) for x in c] for c in (net.M, net.V, net.MS, net.VS))
+    for i, (m, v) in enumerate(zip(*gpu.adamw_moments(net.list))):
+        rm, rv = net.values(i)
+        assert np.array_equal(host(m), rm.astype(np.float32))
+        assert np.array_equal(host(v), rv.astype(np.float32))
+    state = gpu.adamw_state(net.P, 8)
+    fresh = gpu.Params(net.P, net.G, state[0], state[1], m_scale=state[2], v_scale=state[3])
+    assert [m.numel() for m in gpu.adamw_moments(fresh)[0]] == [0, 300, 0, 257, 0]
+    assert not any(t.any() for c in gpu.adamw_moments(fresh) for t in c)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_any_element_alignment(gpu, bits):
     # tensors packed end to end in one buffer each, behind one element

@@ -164,6 +164,16 @@ def test_adamw_moments_refusals(lib):
     assert lib.e3_adamw_moments(0, None, None, None, None) == 0
 
 
+def test_empty_tensors_have_no_moments_to_read(lib):
+    # zero-length scales have no address: an empty tensor is left out, whatever its moments were
+    empty = dict(n=0, p=None, grad=None, m=None, v=None)
+    none = (C.c_void_p * 2)(None, None)
+    assert lib.e3_adamw_moments(*_list(_param(**empty), _param(**empty)), none, none, None) == 0
+    out = (C.c_void_p * 2)(None, AT * 8)
+    assert lib.e3_adamw_moments(*_list(_param(**empty), _param()), out, out, None) == INVALID
+    assert b"tensor 1" in lib.e3_last_error()
+
+
 def test_binding_refuses_host_tensors():
     torch = pytest.importorskip("torch")
     x = torch.zeros((3, 4, 8))
