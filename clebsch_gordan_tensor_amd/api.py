@@ -1174,6 +1174,16 @@ def _column(device, tensors, dtypes):
         return False
 
 
+def _tensors(column, name):
+    """Refuses what is no tensor, such as the None of a parameter without a gradient."""
+    import torch
+    if not all(isinstance(t, torch.Tensor) for t in column):
+        i, t = next((i, t) for i, t in enumerate(column) if not isinstance(t, torch.Tensor))
+        if t is None:
+            raise ValueError(f"{name}[{i}] is required")
+        raise TypeError(f"{name}[{i}] must be a tensor, got {type(t).__name__}")
+
+
 class Params:
     """The tensors of a network's weights with what their update reads and
     writes (lists of equal length; every tensor contiguous, on one GPU):
@@ -1208,6 +1218,7 @@ class Params:
         for name, c in cols.items():
             if c is not None and len(c) != n:
                 raise ValueError(f"{name} has {len(c)} tensors, grads {n}")
+        _tensors(grads, "grads")
         decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
         if len(decay) != n:
             raise ValueError(f"weight_decay has {len(decay)} values, expected {n}")
@@ -1256,6 +1267,7 @@ class Params:
         import torch
         if len(grads) != self._n:
             raise ValueError(f"grads has {len(grads)} tensors, expected {self._n}")
+        _tensors(grads, "grads")
         types = {torch.float32: E3_F32, torch.bfloat16: E3_BF16}
         shapes = [g.shape if p is None else p.shape for g, p in zip(grads, self._keep["params"])]
         if not (_column(self.device, grads, [g.dtype for g in grads])

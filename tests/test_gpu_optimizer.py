@@ -343,6 +343,18 @@ def test_new_gradients_each_step(gpu):
         net.check(gpu, t)
 
 
+def test_new_gradients_without_one_are_refused(gpu):
+    # the list works on with the gradients it had
+    net = Net(gpu, [300, 20], [8, 32], 23)
+    with pytest.raises(ValueError, match=r"grads\[1\] is required"):
+        net.list.set_grads([torch.ones(300, device="cuda"), None])
+    gpu.adamw(net.list, 2, LR)
+    net.check(gpu, 2)
+    only = gpu.Params(grads=net.G)
+    with pytest.raises(ValueError, match=r"grads\[0\] is required"):
+        only.set_grads([None, net.G[1]])
+
+
 def test_long_tensor(gpu):
     # past 2^31 elements: the ends against the same values in a short list
     n, k = 2 ** 31 + 515, 1027

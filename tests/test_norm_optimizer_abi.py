@@ -191,6 +191,18 @@ def test_binding_refuses_host_tensors():
         api.adamw_state([x], 16)
 
 
+def test_a_parameter_without_a_gradient_is_named():
+    torch = pytest.importorskip("torch")
+    g = torch.zeros(3)
+    for grads, error, text in (([None], ValueError, r"grads\[0\] is required"),
+                               ([g, None], ValueError, r"grads\[1\] is required"),
+                               ([g, 2.0], TypeError, r"grads\[1\] must be a tensor")):
+        with pytest.raises(error, match=text):
+            api.Params(grads=grads)
+        with pytest.raises(error, match=text):
+            api.Params(params=[g] * len(grads), grads=grads, m=[g] * len(grads), v=[g] * len(grads))
+
+
 # --------------------------------------------------- the 64-bit forms themselves
 
 def test_norm_gradients_against_differences():
