@@ -181,6 +181,13 @@ __device__ __forceinline__ void load_weights(const float* p, const Lane<V, K>& l
     for (int v = 0; v < V; ++v) w[i][v] = p ? p[ln.k0[i] + v] : other;
 }
 
+// 1 / sqrt(t), t a mean square + eps; NaN (infinity x 0) where t is not finite:
+// an infinity, or squares past float32's range.  The root alone would answer
+// these with 0, and every finite value of the segment with it.
+__device__ __forceinline__ float inv_root(float t) {
+  return fmaf(t, 0.0f, __builtin_amdgcn_rsqf(t));
+}
+
 // Rows a team takes at once: of scalars two, so that their loads are under way
 // together and their sums share the joining steps.
 constexpr int rows_at_once(int nc, int k) { return nc == 1 && k == 1 ? 2 : 1; }
@@ -267,7 +274,7 @@ __device__ __forceinline__ void fwd_step(const Block<T, V, K>& b, const Rows<U>&
   team_sum<TEAM>(s, b.group, lds, phase);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const float rstd = __builtin_amdgcn_rsqf(fmaf(s[u], inv, b.eps));
+    const float rstd = inv_root(fmaf(s[u], inv, b.eps));
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -322,7 +329,7 @@ __device__ __forceinline__ void bwd_step(const Block<T, V, K>& b, const Rows<U>&
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const float* q = s + u * S;
-    const float rstd = __builtin_amdgcn_rsqf(fmaf(q[0], inv, b.eps));
+    const float rstd = inv_root(fmaf(q[0], inv, b.eps));
     const float along = q[1] * inv * rstd;
     float mg = 0.0f;
     if constexpr (NC == 1) mg = b.centered ? q[2] * inv : 0.0f;
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rows(const NormArgs a, in
           }
         }
         wave_team_sum(s, g);
-        const float rstd = __builtin_amdgcn_rsqf(s[0] * inv + a.eps);
+        const float rstd = inv_root(s[0] * inv + a.eps);
         if (lane == 0 && q + tid / g < rows)
           stats[r * nb + i] = {mu, rstd, s[1] * inv * rstd, b.centered ? s[2] * inv : 0.0f};
       }

@@ -605,8 +605,10 @@ e3_status e3_linear_backward(const e3_irreps* in, const e3_irreps* out, int64_t 
  * the storage type; a row's result does not depend on the other rows.  C up to 4096 (1024 when a degree is above 3), degrees up
  * to 8, at most 1024 blocks; eps a positive normal float; pointers aligned to
  * their element.
- * y may be x, but must not overlap it otherwise.  A row that holds an
- * infinity or NaN gives NaN in that block and leaves the others alone. */
+ * y may be x, but must not overlap it otherwise.  A block of a row whose sum
+ * of xc^2 is not finite in float32 (it holds an infinity, a NaN or values past
+ * about 1e19) gives NaN in all of that block; other rows and blocks are left
+ * alone. */
 enum { E3_NORM_UNCENTERED = 1 };
 e3_status e3_layer_norm(const e3_irreps* irreps, int64_t n_rows, const void* x,
                         const float* weight, const float* bias, float eps, int32_t flags, void* y,
@@ -626,7 +628,9 @@ e3_status e3_layer_norm_workspace_size(const e3_irreps* irreps, int64_t n_rows, 
  * 16-byte aligned; nothing in it has to be set or outlives the call, but
  * calls that may overlap need one each): reproducible.  weight NULL: 1.  dx
  * may be x or dy, but must not overlap them otherwise, and dweight, dbias and
- * the workspace nothing.  n_rows = 0 gives zero dweight and dbias.
+ * the workspace nothing.  n_rows = 0 gives zero dweight and dbias.  A block of
+ * a row that the forward answers with NaN has NaN in its dx and in all of its
+ * dweight.
  * Limits and alignment as the forward. */
 e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const void* x,
                                  const float* weight, const void* dy, float eps, int32_t flags,

@@ -260,6 +260,39 @@ def test_rows_apart(gpu):
     assert not np.isfinite(got[5, 0, 3])
 
 
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("irreps,C", [("0e", 64), ("0e", 1001), ("0e", 2050), ("0e+1o", 3),
+                                      ("0e+1o", 9), ("0e+0o", 128), ("0e+1o", 300),
+                                      ("0e+1o", 600), ("4e+0e", 64), ("4e+0e", 9)])
+def test_a_block_that_is_not_finite(gpu, irreps, C, dtype, flags):
+    # an infinity, a NaN or values whose squares leave float32's range, in the last row: NaN all
+    # over their block of that row and in its weight's gradient, nothing else changes
+    irreps, rows = _ir(irreps), 37
+    x, dy, w, b = _case(irreps, rows, C, C + 1, dtype)
+    D, W, B = dev(dy, dtype), dev(w), dev(b)
+
+    def both(X):
+        return (gpu.layer_norm(irreps, X, W, B, flags=flags),
+                *gpu.layer_norm_backward(irreps, X, W, D, flags=flags))
+
+    y, dx, dw, db = both(dev(x, dtype))
+    assert all(torch.isfinite(t).all() for t in (y, dx, dw, db))
+    for i, (at, nc, _) in enumerate(R.blocks_of(irreps)):
+        for value in (np.inf, -np.inf, np.nan, 1e30, -3e38):
+            X = dev(x, dtype)
+            X[-1, at + nc - 1, C // 2] = value
+            got = both(X)
+            hit = torch.zeros(x.shape, dtype=torch.bool, device="cuda")
+            hit[-1, at:at + nc] = True
+            for t, r in zip(got[:2], (y, dx)):
+                assert torch.equal(t[~hit], r[~hit]), (i, value)
+                assert torch.isnan(t[hit]).all(), (i, value)
+            others = [k for k in range(len(irreps)) if k != i]
+            assert torch.isnan(got[2][i]).all() and torch.equal(got[2][others], dw[others])
+            assert torch.equal(got[3], db)
+
+
 def test_refused(gpu):
     irreps = _ir("0e+1o")
     x, dy, w, b = (dev(a) for a in _case(irreps, 6, 16, 14))
