@@ -70,6 +70,57 @@ def norm_backward(irreps, x, w, dy, eps, centered=True):
     return (dx, dw, db), (tx + U * np.abs(dx), tw, tb)
 
 
+# dweight and dbias over many rows, each workgroup taking several turns over them:
+# (irreps, channels, storage type, rows, channels of a component row that a lane holds, roundings
+# that a term of the sums passes through, at most).  The last, term by term: adds of a lane over
+# its rows and components, joins of lanes and teams, adds of every 64th partial, 32 + 1 last ones.
+LONG_SUMS = [
+    # a block a workgroup: 170, 512 and 853 of them, 8 teams of 32 lanes; 8, 9, 10 + 1 + 4 + 14 + 33
+    ("0e+1o+2e", 128, "f32", 10007, 4, 62),
+    # scalars: 256 workgroups, 8 teams of two rows; 10 + 1 + 4 + 4 + 33
+    ("0e", 128, "f32", 20011, 4, 52),
+    # four vectors a lane, 4 teams; 5 + 4 + 4 + 33
+    ("0e", 1001, "f32", 5003, 16, 46),
+    # a team of four wavefronts; 12 + 4 + 33
+    ("0e", 2050, "bf16", 3001, 16, 49),
+    # whole rows: 2048 workgroups, 16 or 8 teams, two turns; 3 + 2 + 4 + 4 + 32 + 33
+    ("0e+1o", 60, "f32", 40003, 4, 78),
+    ("0e+1o", 100, "bf16", 20011, 4, 78),
+    # staged rows, 64 (128 in bf16) a piece in 9 groups: 8 (15) + 3 + 1 + 6 + 16 + 33
+    ("0e+1o+2e", 3, "f32", 70001, 4, 67),
+    ("0e+1o+2e", 3, "bf16", 140003, 4, 74),
+]
+
+
+def long_sums(irreps, x, dy, eps, lane, depth, centered=True):
+    """[(dweight terms of every row [rows][C], dweight, its bound)] of the
+    blocks and the same of dbias for the 0e ones."""
+    dw, db = [], []
+    for at, nc, bias in blocks_of(irreps):
+        c = centered and bias >= 0
+        xh, _, e = _block(x, at, nc, c, eps)
+        d = dy[:, at:at + nc].astype(np.float64)
+        # xh: sums over what a lane holds of the segment, then at most 6 + 4 joins and 6 other
+        # roundings (the root halves the error of its argument)
+        segment = lane * nc + 16
+        tol = depth * U * np.abs(d * xh).sum((0, 1)) + segment * U * (np.abs(d) * e).sum((0, 1))
+        terms = (d * xh).sum(1)
+        dw.append((terms, terms.sum(0), tol))
+        if bias >= 0:
+            db.append((d[:, 0], d.sum((0, 1)), depth * U * np.abs(d).sum((0, 1))))
+    return dw, db
+
+
+def long_case(irreps, C, dtype, rows):
+    """x and dy of a case of LONG_SUMS."""
+    from clebsch_gordan_tensor_amd import synth as S
+    rng = np.random.default_rng(rows + C)
+    dim = sum(2 * l + 1 for l, _ in irreps)
+    x = rng.standard_normal((rows, dim, C)) * rng.uniform(0.1, 3.0, (rows, 1, 1)) + 0.2
+    x, dy = x.astype(np.float32), rng.standard_normal((rows, dim, C)).astype(np.float32)
+    return (S.round_bf16(x), S.round_bf16(dy)) if dtype == "bf16" else (x, dy)
+
+
 # ------------------------------------------------------------------ optimizer
 
 def decode(m, v, ms, vs):

@@ -101,6 +101,22 @@ def test_many_rows(gpu):
     _check(gpu, irreps, *_case(irreps, 5003, 48, 3))
 
 
+@pytest.mark.parametrize("case", R.LONG_SUMS, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}")
+def test_long_sums(gpu, case):
+    # every kernel over more rows than its workgroups take in one turn, bounds that see a lost row
+    ir, C, dtype, rows, lane, depth = case
+    irreps = _ir(ir)
+    x, dy = R.long_case(irreps, C, dtype, rows)
+    w = (1 + 0.3 * np.random.default_rng(C).standard_normal((len(irreps), C))).astype(np.float32)
+    dx, dweight, dbias = gpu.layer_norm_backward(irreps, dev(x, dtype), dev(w), dev(dy, dtype),
+                                                 eps=EPS)
+    dw, db = R.long_sums(irreps, x, dy, EPS, lane, depth)
+    for got, sums, what in ((dweight, dw, "dweight"), (dbias, db, "dbias")):
+        _within(got, *(np.stack([s[k] for s in sums]) for k in (1, 2)), what)
+    (ref, _, _), (tol, _, _) = R.norm_backward(irreps, x, w, dy, EPS)
+    _within(dx, ref, tol, "dx", dtype)
+
+
 @pytest.mark.parametrize("C", [3, 4, 64])
 def test_many_blocks(gpu, C):
     # more blocks than one launch takes, low and high degrees mixed

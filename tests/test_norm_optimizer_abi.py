@@ -220,6 +220,22 @@ def test_norm_gradients_against_differences():
             assert abs((f(*up) - f(*down)) / 2e-5 - (g * d).sum()) <= 1e-7 * np.abs(g * d).sum()
 
 
+@pytest.mark.parametrize("case", R.LONG_SUMS, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}")
+def test_bounds_of_long_sums_see_a_lost_row(case):
+    # a sum over rows that misses one row, or all of them, is outside the bound it is held to
+    ir, C, dtype, rows, lane, depth = case
+    irreps = S.parse_irreps(ir)[1]
+    dw, db = R.long_sums(irreps, *R.long_case(irreps, C, dtype, rows), 1e-5, lane, depth)
+    for sums in (dw, db):
+        total, tol = (np.concatenate([s[k] for s in sums]) for k in (1, 2))
+        assert np.mean(np.abs(total) > tol) >= 0.9
+        for row in (0, rows // 2, rows - 1):
+            lost = np.concatenate([s[0][row] for s in sums])
+            seen = np.mean(np.abs(lost) > tol)
+            print(f"{ir} C {C}: row {row} seen in {seen:.2f} of {lost.size} sums")
+            assert seen > 0
+
+
 def test_norm_is_equivariant():
     # rotating the components of every block rotates the result; so does the inversion
     from tests.test_oracle_cg import _rand_rot, wigner_d  # fitted from scipy's harmonics
