@@ -161,6 +161,40 @@ def test_all_alike_and_zero_blocks(gpu):
     assert not np.delete(m[512:768], 88).any() and m[600] < 0 and (v[768:] >= 0).all()
 
 
+def test_values_of_uneven_runs(gpu):
+    # every value of a run's moments after a first step: one gradient alone, gradients of one size,
+    # and gradients whose squares are below float32's smallest value
+    net = Net(gpu, [1024], 8, 7, zeros=True)
+    g = np.zeros(1024, np.float32)
+    g[256:512], g[600], g[768:] = 0.25, -3.0, 1e-30
+    net.G[0].copy_(dev(g))
+    gpu.adamw(net.list, 1, LR)
+    m, v = (host(t[0]).astype(np.float64) for t in gpu.adamw_moments(net.list))
+    g = g.astype(np.float64)
+    # the largest value of a run has the largest code: the scale's rounding and that of the value
+    # read back, in v's scale twice (it is squared), and of the maximum in float32
+    want_m, want_v = 0.1 * g, 0.001 * g * g
+    want_v[768:] = 0.0
+    assert np.all(np.abs(m - want_m) <= 3 * R.U * np.abs(want_m))
+    assert np.all(np.abs(v - want_v) <= 4 * R.U * want_v)
+
+
+def test_long_read_back(gpu):
+    # more than 2048 x 1024 elements: every workgroup reads several pieces; ragged tensors
+    rng = np.random.default_rng(25)
+    sizes = [2_400_003, 1, 1_000_257]
+    f = lambda a: [dev(t) for t in a]  # noqa: E731
+    m = [rng.integers(-127, 128, n).astype(np.int8) for n in sizes]
+    v = [rng.integers(0, 256, n).astype(np.uint8) for n in sizes]
+    ms, vs = ([rng.uniform(1e-9, 1e-3, (n + 255) // 256).astype(np.float32) for n in sizes]
+              for _ in range(2))
+    p, g = ([torch.zeros(n, device="cuda") for n in sizes] for _ in range(2))
+    net = gpu.Params(p, g, f(m), f(v), m_scale=f(ms), v_scale=f(vs))
+    for i, got in enumerate(zip(*gpu.adamw_moments(net))):
+        for a, r in zip(got, R.decode(m[i], v[i], ms[i], vs[i])):
+            assert np.array_equal(host(a), r.astype(np.float32)), i
+
+
 def test_moments_read_back(gpu):
     net = Net(gpu, [1, 300, 70001], 8, 8)
     for i, (m, v) in enumerate(zip(*gpu.adamw_moments(net.list))):
@@ -271,6 +305,23 @@ def test_scale_and_skip(gpu, bits):
     assert all(torch.equal(a, b) for a, b in zip(kept, net.P + net.M + net.V))
 
 
+def test_skip_leaves_the_scales(gpu):
+    # larger gradients than before: a step would change the scales of every run, a skipped one none
+    net = Net(gpu, [5000, 70, 0], 8, 24)
+    for g in net.G:
+        g.mul_(1e3)
+    every = [t for c in (net.P, net.M, net.V, net.MS, net.VS) for t in c]
+    kept = [t.clone() for t in every]
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        scale = torch.full((1,), bad, device="cuda")
+        gpu.adamw(net.list, 5, LR, grad_scale=scale, flags=gpu.E3_ADAMW_SKIP_NONFINITE)
+        assert all(torch.equal(a, b) for a, b in zip(kept, every))
+    gpu.adamw(net.list, 5, LR, grad_scale=torch.ones(1, device="cuda"),
+              flags=gpu.E3_ADAMW_SKIP_NONFINITE)
+    for scales, before in ((net.MS, kept[9:12]), (net.VS, kept[12:15])):
+        assert all((a != b).all() for a, b in zip(scales, before))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_step_and_lr_on_the_device(gpu, bits):
     a, b = (Net(gpu, [3000, 12], bits, 12) for _ in range(2))
@@ -374,6 +425,18 @@ def test_long_tensor(gpu):
         assert torch.equal(sv[0][:whole], v[0][lo:lo + whole])
     out = host(gpu.grad_norm(gpu.Params(grads=[G])))
     assert abs(out[0] - np.sqrt(n)) <= 1e-3 * np.sqrt(n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_of_a_long_tensor(gpu, dtype):
+    # past 2^31 elements: 64-bit sums of slices of the same values; a lost slice of 65536 would be
+    # 3e-5 / 2 of the norm, the bound is float32's rounding of it
+    n = 2 ** 31 + 515 if dtype == "bf16" else 2 ** 28 + 515
+    G = torch.empty(n, device="cuda", dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    G.normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    total = sum(float(G[i:i + 2 ** 27].double().square().sum()) for i in range(0, n, 2 ** 27))
+    out = host(gpu.grad_norm(gpu.Params(grads=[G])))
+    assert abs(out[0] - np.sqrt(total)) <= 1.001 * R.U * np.sqrt(total)
 
 
 def _training(gpu, seed):
