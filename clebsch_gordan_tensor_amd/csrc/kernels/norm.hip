@@ -431,7 +431,12 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_fwd(const NormArgs a) {
 }
 
 // Wavefronts on a SIMD of the backward for scalars, by registers held to it;
-// as many of its workgroups are resident on a compute unit.
+// as many of its workgroups are resident on a compute unit.  At k = 1 (and k =
+// 2, v = 4) 2 to 11 registers spill under these caps, and one wavefront less,
+// without spills, is faster (us, caps as here and one less): float32, 128
+// channels of 150,000 rows 52 and 50, 512 of 40,000 53 and 52; bf16 35 and 29.5,
+// 38 and 32.  Without spills there is nothing in it (1000 channels of 20,000
+// rows 50.5 and 50.7, in bf16 38 and 38).
 constexpr int scalar_waves(int v, int k) {
   return v == 8 ? (k == 1 ? 4 : k == 2 ? 3 : 2) : k == 1 ? 6 : k == 2 ? 5 : 2;
 }
@@ -882,12 +887,15 @@ Shape shape_of(int C, int top, int esize) {
 
 // Workgroups of every block, in proportion to its components: a few for every
 // one that is resident, so that blocks of different lengths even out (64,000
-// rows of 128x(0e+1o+2e+3o), us: forward 1536 workgroups 202, 2048 192, 2560
-// 197, 4096 203; backward 768 340, 1536 299, 1792 303, 2304 313), but a single
+// rows of 128x(0e+1o+2e+3o), us: forward 1536 workgroups 202, 1792 202, 2048
+// 195.5, 2560 196.3, 4096 203; other shapes take 2048 and 2560 alike to 5%
+// either way: 3,000 rows 12.0 and 12.7, 10,000 rows of 300 channels in bf16
+// 45.6 and 44.4; backward 768 340, 1536 299, 1792 303, 2304 313), but a single
 // block's exactly as many as are resident.  Each of the backward's leaves 8 C
-// bytes of partials to write and read again: past 256 it has at least 8 turns
-// over its rows, or 128 bytes of every channel (1001 scalar channels, 20,011
-// rows: 512 workgroups 52 us, 556 62, 768 56, 1024 59).
+// bytes of partials to write and read again: past 256 each of its teams has at
+// least 8 rows (4 turns where a team takes two at once), or 128 bytes of every
+// channel (1001 scalar channels, 20,011 rows: 512 workgroups 52 us, 556 62,
+// 768 56, 1024 59).
 int plan(NormArgs& a, const NormBlock* blocks, int n_blocks, int top, bool bwd, int esize) {
   const Shape sh = shape_of(a.C, top, esize);
   const int teams = kNormThreads / sh.group;

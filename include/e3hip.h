@@ -593,8 +593,9 @@ e3_status e3_linear_backward(const e3_irreps* in, const e3_irreps* out, int64_t 
 /* Normalisation of irreps features (a layer norm that commutes with rotations
  * and inversion, next to e3_linear), and its gradients.  For every row r and
  * block i of `irreps` (degree l, K = (2l+1) C values x[r][i, m][k]):
- *   xc   = x - (mean over the channels)  for 0e blocks, x for the others (no
- *          other block has a mean that a rotation or the inversion leaves)
+ *   xc   = x - (mean over the channels)  for 0e blocks, x for the others (the
+ *          mean of another block turns with it and could be taken off as well;
+ *          that 0e blocks alone are centred, and biased, is the convention)
  *   rstd = 1 / sqrt(sum_{m,k} xc^2 / K + eps)
  *   y    = xc rstd weight[i][k] (+ bias[j][k] for the j-th 0e block)
  * A list of one 0e block is the ordinary layer norm over C channels; with
@@ -602,10 +603,10 @@ e3_status e3_linear_backward(const e3_irreps* in, const e3_irreps* out, int64_t 
  * x, y [n_rows][dim][C] in the storage type, every block of multiplicity C;
  * weight [n_blocks][C] and bias [number of 0e blocks][C] float32, either may
  * be NULL (1 and 0).  Statistics and products in float32, one rounding to
- * the storage type; a row's result does not depend on the other rows.  C up to 4096 (1024 when a degree is above 3), degrees up
- * to 8, at most 1024 blocks; eps a positive normal float; pointers aligned to
- * their element.
- * y may be x, but must not overlap it otherwise.  A block of a row whose sum
+ * the storage type; a row's result does not depend on the other rows.  C up
+ * to 4096 (1024 when a degree is above 3), degrees up to 8, at most 1024
+ * blocks; eps a positive normal float; pointers aligned to their element.
+ * y may be x, but must not overlap it, weight or bias otherwise.  A block of a row whose sum
  * of xc^2 is not finite in float32 (it holds an infinity, a NaN or values past
  * about 1e19) gives NaN in all of that block; other rows and blocks are left
  * alone. */
