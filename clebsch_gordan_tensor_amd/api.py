@@ -1177,11 +1177,12 @@ def _column(device, tensors, dtypes):
 def _tensors(column, name):
     """Refuses what is no tensor, such as the None of a parameter without a gradient."""
     import torch
-    if not all(isinstance(t, torch.Tensor) for t in column):
-        i, t = next((i, t) for i, t in enumerate(column) if not isinstance(t, torch.Tensor))
-        if t is None:
-            raise ValueError(f"{name}[{i}] is required")
-        raise TypeError(f"{name}[{i}] must be a tensor, got {type(t).__name__}")
+    if all(issubclass(c, torch.Tensor) for c in set(map(type, column))):
+        return
+    i, t = next((i, t) for i, t in enumerate(column) if not isinstance(t, torch.Tensor))
+    if t is None:
+        raise ValueError(f"{name}[{i}] is required")
+    raise TypeError(f"{name}[{i}] must be a tensor, got {type(t).__name__}")
 
 
 class Params:
