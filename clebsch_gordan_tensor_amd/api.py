@@ -63,6 +63,8 @@ EXPORTS = ["e3_num_paths", "e3_path_info", "e3_supported", "e3_cg_block",
            "e3_layer_norm", "e3_layer_norm_workspace_size", "e3_layer_norm_backward",
            "e3_param_check", "e3_grad_norm_workspace_size", "e3_grad_norm", "e3_adamw",
            "e3_adamw_moments",
+           "e3_group_index_size", "e3_group_index_at", "e3_group_index", "e3_linear_grouped",
+           "e3_linear_grouped_workspace_size", "e3_linear_grouped_backward",
            "e3_release_all",
            "e3_last_error"]
 E3_GEN_FORWARD, E3_GEN_DX, E3_GEN_DW, E3_GEN_DY, E3_GEN_GEMM = 0, 1, 2, 3, 4
@@ -163,6 +165,14 @@ def lib():
     L.e3_layer_norm_workspace_size.argtypes = [ip, i64, C.POINTER(sz)]
     L.e3_layer_norm_backward.argtypes = [ip, i64, vp, vp, vp, C.c_float, i32, vp, vp, vp, vp, sz,
                                          C.c_int, vp]
+    szp = C.POINTER(sz)
+    L.e3_group_index_size.argtypes = [i64, i32, szp]
+    L.e3_group_index_at.argtypes = [i64, i32, szp, szp]
+    L.e3_group_index.argtypes = [i64, i32, vp, vp, sz, vp]
+    L.e3_linear_grouped.argtypes = [ip, ip, i64, i32, vp, sz, vp, vp, vp, C.c_int, vp]
+    L.e3_linear_grouped_workspace_size.argtypes = [ip, ip, i64, i32, szp]
+    L.e3_linear_grouped_backward.argtypes = [ip, ip, i64, i32, vp, sz, vp, vp, vp, vp, vp, vp, sz,
+                                             C.c_int, vp]
     pp = C.POINTER(_Param)
     L.e3_param_check.argtypes = [i32, pp]
     L.e3_grad_norm_workspace_size.argtypes = [i32, pp, C.POINTER(sz)]
@@ -1157,6 +1167,158 @@ def layer_norm_backward(irreps, x, weight, dy, eps=1e-5, flags=0, dx=None, dweig
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _dtype_code(x),
         stream=stream)
     return dx, dweight, dbias
+
+
+# ------------------------------------------------------------- grouped rows
+
+@functools.lru_cache(maxsize=256)
+def _index_sizes(rows, n_groups):
+    """(bytes, byte of the offsets, byte of the order) of an index."""
+    b, off, order = C.c_size_t(), C.c_size_t(), C.c_size_t()
+    _check(lib().e3_group_index_size(rows, n_groups, C.byref(b)))
+    _check(lib().e3_group_index_at(rows, n_groups, C.byref(off), C.byref(order)))
+    return b.value, off.value, order.value
+
+
+class RowGroups:
+    """The index of group_rows: rows in n_groups groups.  ``buffer`` is its
+    memory, ``order`` (int32 [rows]) lists the rows by group and
+    ``offsets`` (int32 [n_groups + 1]) says where each group begins; what
+    follows offsets[-1] has no group."""
+
+    def __init__(self, buffer, rows, n_groups):
+        self.buffer, self.rows, self.n_groups = buffer, rows, n_groups
+
+    def _words(self, at, n):
+        import torch
+        return self.buffer[at:at + 4 * n].view(torch.int32)
+
+    @property
+    def offsets(self):
+        return self._words(_index_sizes(self.rows, self.n_groups)[1], self.n_groups + 1)
+
+    @property
+    def order(self):
+        return self._words(_index_sizes(self.rows, self.n_groups)[2], self.rows)
+
+
+def group_rows(group, n_groups: int, index=None, stream=None) -> RowGroups:
+    """The index of rows by group from their ids (int32 [rows]); ids outside
+    [0, n_groups) belong to none.  index: a RowGroups of the same sizes to
+    write again (its graph-captured readers see the new one)."""
+    import torch
+    _need(group, "group", dtype=torch.int32)
+    if group.dim() != 1:
+        raise ValueError(f"group has shape {tuple(group.shape)}, expected [rows]")
+    rows, dev = group.shape[0], group.device
+    nb = _index_sizes(rows, n_groups)[0]
+    if index is None:
+        index = RowGroups(_new(stream, nb, dev, torch.uint8), rows, n_groups)
+    else:
+        _index_args(dev, index, rows, n_groups)
+    _on(dev, lib().e3_group_index, rows, n_groups, group.data_ptr(), index.buffer.data_ptr(), nb,
+        stream=stream)
+    return index
+
+
+def _index_args(device, index, rows, n_groups):
+    """(pointer, bytes) of an index after its checks; None is a single group's."""
+    if index is None:
+        return None, 0
+    if not isinstance(index, RowGroups):
+        raise TypeError("index must be of group_rows")
+    if (index.rows, index.n_groups) != (rows, n_groups):
+        raise ValueError(f"the index is of {index.rows} rows in {index.n_groups} groups, "
+                         f"expected {rows} in {n_groups}")
+    if index.buffer.device != device:
+        raise ValueError(f"the index is on {index.buffer.device}, expected {device}")
+    return index.buffer.data_ptr(), index.buffer.numel()
+
+
+@functools.lru_cache(maxsize=256)
+def _mix_spec(into, out, cin, cout):
+    """(in struct, out struct, components in and out, pairs) of a channel mixing."""
+    return (_irreps_struct(into, cin), _irreps_struct(out, cout), synth.dim(into), synth.dim(out),
+            sum(a == b for a in into for b in out))
+
+
+def _mix_x(in_irreps, out_irreps, x, W, name="W"):
+    """(in, out, spec) after the checks of x [rows][din][Cin] and W
+    [groups][pairs][Cin][Cout]."""
+    _need(x, "x")
+    _need(W, name)
+    if x.dim() != 3 or W.dim() != 4:
+        raise ValueError(f"x and {name} have shapes {tuple(x.shape)} and {tuple(W.shape)}, expected "
+                         "[rows][components][Cin] and [groups][pairs][Cin][Cout]")
+    into, out = tuple(map(tuple, in_irreps)), tuple(map(tuple, out_irreps))
+    spec = _mix_spec(into, out, x.shape[2], W.shape[3])
+    if x.shape[1] != spec[2]:
+        raise ValueError(f"x has {x.shape[1]} components, the input irreps {spec[2]}")
+    if tuple(W.shape[1:3]) != (spec[4], x.shape[2]):
+        raise ValueError(f"{name} has shape {tuple(W.shape)}, expected {spec[4]} pairs of "
+                         f"{x.shape[2]} input channels")
+    return into, out, spec
+
+
+def linear_grouped(in_irreps, out_irreps, index, x, W, out=None, stream=None):
+    """y [rows][dout][Cout] = channel mixing of x [rows][din][Cin] with the
+    weights W [groups][pairs][Cin][Cout] (x's type) of each row's group; rows
+    without a group get 0.  index: of group_rows, or None for one group."""
+    _, _, (a, b, _, dout, _) = _mix_x(in_irreps, out_irreps, x, W)
+    dev, rows, shape = x.device, x.shape[0], (x.shape[0], dout, W.shape[3])
+    _need_on(dev, W, "W", None, x.dtype)
+    at, nb = _index_args(dev, index, rows, W.shape[0])
+    if out is None:
+        out = _new(stream, shape, dev, x.dtype)
+    else:
+        _need_on(dev, out, "out", shape, x.dtype)
+    _on(dev, lib().e3_linear_grouped, C.byref(a), C.byref(b), rows, W.shape[0], at, nb,
+        x.data_ptr(), W.data_ptr(), out.data_ptr(), _dtype_code(x), stream=stream)
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _mix_workspace_size(into, out, cin, cout, rows, n_groups):
+    nb = C.c_size_t()
+    a, b = _mix_spec(into, out, cin, cout)[:2]
+    _check(lib().e3_linear_grouped_workspace_size(C.byref(a), C.byref(b), rows, n_groups,
+                                                  C.byref(nb)))
+    return nb.value
+
+
+def linear_grouped_workspace_size(in_irreps, out_irreps, cin, cout, rows: int,
+                                  n_groups: int) -> int:
+    """Bytes of linear_grouped_backward's workspace."""
+    return _mix_workspace_size(tuple(map(tuple, in_irreps)), tuple(map(tuple, out_irreps)), cin,
+                               cout, rows, n_groups)
+
+
+def linear_grouped_backward(in_irreps, out_irreps, index, x, W, dy, dx=None, dW=None,
+                            workspace=None, stream=None):
+    """(dx, dW [groups][pairs][Cin][Cout] float32) of linear_grouped for the
+    cotangent dy [rows][dout][Cout]."""
+    import torch
+    into, out, (a, b, _, dout, _) = _mix_x(in_irreps, out_irreps, x, W)
+    dev, rows, n_groups, cout = x.device, x.shape[0], W.shape[0], W.shape[3]
+    _need_on(dev, W, "W", None, x.dtype)
+    _need(dy, "dy")
+    _need_on(dev, dy, "dy", (rows, dout, cout), x.dtype)
+    _need_on(dev, dx, "dx", x.shape, x.dtype)
+    _need_on(dev, dW, "dW", W.shape, torch.float32)
+    _need_on(dev, workspace, "workspace", None, None)
+    at, nb = _index_args(dev, index, rows, n_groups)
+    if dx is None:
+        dx = _new(stream, x.shape, dev, x.dtype)
+    if dW is None:
+        dW = _new(stream, W.shape, dev, torch.float32)
+    if workspace is None:
+        workspace = _new(stream, _mix_workspace_size(into, out, x.shape[2], cout, rows, n_groups),
+                         dev, torch.uint8)
+    _on(dev, lib().e3_linear_grouped_backward, C.byref(a), C.byref(b), rows, n_groups, at, nb,
+        x.data_ptr(), W.data_ptr(), dy.data_ptr(), dx.data_ptr(), dW.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _dtype_code(x),
+        stream=stream)
+    return dx, dW
 
 
 # ---------------------------------------------------------------- optimizer

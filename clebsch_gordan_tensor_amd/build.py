@@ -33,6 +33,8 @@ HIP_SOURCES = [
     "kernels/generic.hip",
     "kernels/gemm.hip",
     "kernels/norm.hip",
+    "kernels/group.hip",
+    "kernels/grouped.hip",
     "kernels/optimizer.hip",
     "api.cpp",
     "host/cg_ladder.cpp",

@@ -32,6 +32,16 @@ e3_status ok() {
   return E3_OK;
 }
 
+// Runs a call's host part; what it throws (out of memory) becomes a status.
+template <class F>
+e3_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(E3_ERR_INVALID_ARG, e.what());
+  }
+}
+
 constexpr int kGenericLmax = 8;  // coefficient tables of the generic tensor product
 constexpr int kTableHarmonicsLmax = 6;  // harmonics the coefficient-table kernels compute
 
@@ -2498,6 +2508,246 @@ e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const 
   return hip_status(e3k::launch_norm(true, a, n.blocks.data(), nb, dtype == E3_BF16,
                                      hipStream_t(stream)),
                     "layer_norm_backward");
+}
+
+namespace {
+
+constexpr int kMixChannels = 8192;
+
+e3_status check_groups(int64_t n_rows, int32_t n_groups) {
+  if (n_rows < 0) return fail(E3_ERR_INVALID_ARG, "n_rows < 0");
+  if (n_rows > INT32_MAX) return fail(E3_ERR_UNSUPPORTED, "grouped rows: at most 2^31 - 1");
+  if (n_groups < 1) return fail(E3_ERR_INVALID_ARG, "n_groups < 1");
+  if (n_groups > e3k::kMaxGroups)
+    return fail(E3_ERR_UNSUPPORTED, "at most " + std::to_string(e3k::kMaxGroups) + " groups");
+  return E3_OK;
+}
+
+// The index of a call on grouped rows; none is needed for a single group.
+e3_status check_index(int64_t n_rows, int32_t n_groups, const void* index, size_t bytes) {
+  const e3_status s = check_groups(n_rows, n_groups);
+  if (s != E3_OK) return s;
+  if (!index)
+    return n_groups == 1 ? E3_OK : fail(E3_ERR_INVALID_ARG, "several groups need an index");
+  const size_t need = 4 * size_t(e3k::group_layout(n_rows, n_groups).words);
+  if (bytes < need)
+    return fail(E3_ERR_WORKSPACE, "the index of " + std::to_string(n_rows) + " rows in " +
+                                      std::to_string(n_groups) + " groups has " +
+                                      std::to_string(need) + " bytes");
+  if (!aligned16(index)) return fail(E3_ERR_ALIGNMENT, "the index must be 16-byte aligned");
+  return E3_OK;
+}
+
+// Block lists of a grouped or 8-bit channel mixing, with the pairs of blocks
+// of equal type, input block by input block.
+struct Mix {
+  int cin = 0, cout = 0, din = 0, dout = 0;
+  std::vector<e3k::MixBlock> in, out;  // offset and components
+  struct Pair {
+    int i, o;
+  };
+  std::vector<Pair> pairs;
+
+  // What each block of the result sums over, forward or (dx) backward.
+  e3k::MixList list(bool backward) const {
+    e3k::MixList l{};
+    const auto& to = backward ? in : out;
+    const auto& from = backward ? out : in;
+    for (size_t b = 0; b < to.size(); ++b) {
+      e3k::MixBlock& k = l.blk[l.n_blocks++];
+      k = to[b];
+      k.src0 = l.n_src;
+      for (size_t p = 0; p < pairs.size(); ++p)
+        if (size_t(backward ? pairs[p].i : pairs[p].o) == b) {
+          l.src[l.n_src++] = {from[size_t(backward ? pairs[p].o : pairs[p].i)].out_off, int(p)};
+          ++k.n_src;
+        }
+    }
+    return l;
+  }
+};
+
+e3_status parse_mix(const e3_irreps* in, const e3_irreps* out, int64_t n_rows, int step,
+                    Mix& m) {
+  std::vector<e3k::IrSpec> li, lo;
+  for (const e3_irreps* l : {in, out})
+    if (l && l->n > e3k::kMixBlocks)
+      return fail(E3_ERR_UNSUPPORTED, "at most " + std::to_string(e3k::kMixBlocks) + " blocks");
+  const e3_status s = parse_linear(in, out, li, lo, m.cin, m.cout);
+  if (s != E3_OK) return s;
+  if (m.cin % step != 0 || m.cout % step != 0 || m.cin > kMixChannels || m.cout > kMixChannels)
+    return fail(E3_ERR_UNSUPPORTED, "Cin and Cout must be multiples of " + std::to_string(step) +
+                                        " up to " + std::to_string(kMixChannels));
+  for (auto& a : li) {
+    if (a.l > 8) return fail(E3_ERR_UNSUPPORTED, "degrees up to 8");
+    m.in.push_back({m.din, 2 * a.l + 1, 0, 0, 0});
+    m.din += 2 * a.l + 1;
+  }
+  for (auto& a : lo) {
+    if (a.l > 8) return fail(E3_ERR_UNSUPPORTED, "degrees up to 8");
+    m.out.push_back({m.dout, 2 * a.l + 1, 0, 0, 0});
+    m.dout += 2 * a.l + 1;
+  }
+  for (size_t i = 0; i < li.size(); ++i)
+    for (size_t o = 0; o < lo.size(); ++o)
+      if (li[i].l == lo[o].l && li[i].p == lo[o].p) m.pairs.push_back({int(i), int(o)});
+  if (m.pairs.size() > size_t(e3k::kMixSources))
+    return fail(E3_ERR_UNSUPPORTED, "at most " + std::to_string(e3k::kMixSources) +
+                                        " pairs of blocks");
+  if (n_rows > (int64_t(1) << 36) / std::max(m.din, m.dout))
+    return fail(E3_ERR_UNSUPPORTED, "n_rows too large");
+  return E3_OK;
+}
+
+uint64_t features_bytes(int64_t n_rows, int dim, int channels, int esize) {
+  return uint64_t(n_rows) * uint64_t(dim) * uint64_t(channels) * uint64_t(esize);
+}
+
+}  // namespace
+
+e3_status e3_group_index_size(int64_t n_rows, int32_t n_groups, size_t* bytes) {
+  const e3_status s = check_groups(n_rows, n_groups);
+  if (s != E3_OK) return s;
+  if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
+  *bytes = 4 * size_t(e3k::group_layout(n_rows, n_groups).words);
+  return ok();
+}
+
+e3_status e3_group_index_at(int64_t n_rows, int32_t n_groups, size_t* offsets, size_t* order) {
+  const e3_status s = check_groups(n_rows, n_groups);
+  if (s != E3_OK) return s;
+  if (!offsets || !order) return fail(E3_ERR_INVALID_ARG, "offsets or order is null");
+  const e3k::GroupLayout l = e3k::group_layout(n_rows, n_groups);
+  *offsets = 4 * size_t(l.offsets);
+  *order = 4 * size_t(l.order);
+  return ok();
+}
+
+e3_status e3_group_index(int64_t n_rows, int32_t n_groups, const int32_t* group, void* index,
+                         size_t bytes, void* stream) {
+  e3_status s = check_groups(n_rows, n_groups);
+  if (s != E3_OK) return s;
+  if (!index || (n_rows > 0 && !group)) return fail(E3_ERR_INVALID_ARG, "null pointer");
+  if ((s = check_index(n_rows, n_groups, index, bytes)) != E3_OK) return s;
+  if (!aligned_to(group, 4)) return fail(E3_ERR_ALIGNMENT, "group must be aligned to its element");
+  if (overlap(range(group, uint64_t(n_rows) * 4),
+              range(index, 4 * uint64_t(e3k::group_layout(n_rows, n_groups).words))))
+    return fail(E3_ERR_INVALID_ARG, "group and the index overlap");
+  return hip_status(e3k::launch_group_index(int(n_rows), n_groups, group,
+                                            static_cast<int*>(index), hipStream_t(stream)),
+                    "group_index");
+}
+
+e3_status e3_linear_grouped(const e3_irreps* in, const e3_irreps* out, int64_t n_rows,
+                            int32_t n_groups, const void* index, size_t index_bytes, const void* x,
+                            const void* W, void* y, e3_dtype dtype, void* stream) {
+  return guarded([&] {
+    Mix m;
+    e3_status s;
+    if ((s = check_index(n_rows, n_groups, index, index_bytes)) != E3_OK ||
+        (s = parse_mix(in, out, n_rows, 8, m)) != E3_OK)
+      return s;
+    if (dtype != E3_F32 && dtype != E3_BF16) return fail(E3_ERR_INVALID_ARG, "unknown dtype");
+    if (n_rows == 0) return ok();
+    if (!x || !y || (!m.pairs.empty() && !W)) return fail(E3_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(x) || !aligned16(y) || !aligned16(W))
+      return fail(E3_ERR_ALIGNMENT, "x, W and y must be 16-byte aligned");
+    const int esize = dtype == E3_BF16 ? 2 : 4;
+    const Range ry = range(y, features_bytes(n_rows, m.dout, m.cout, esize));
+    if (overlap(ry, range(x, features_bytes(n_rows, m.din, m.cin, esize))) ||
+        overlap(ry, range(W, uint64_t(n_groups) * m.pairs.size() * m.cin * m.cout * esize)) ||
+        overlap(ry, range(index, index ? index_bytes : 0)))
+      return fail(E3_ERR_INVALID_ARG, "y overlaps x, W or the index");
+    const e3k::GroupLayout l = e3k::group_layout(n_rows, n_groups);
+    const e3k::MixArgs a{n_rows, n_groups, m.din, m.dout, m.cin, m.cout, int(m.pairs.size()), 0,
+                         static_cast<const int*>(index), int(l.offsets), int(l.order), x, W, y};
+    return hip_status(e3k::launch_mix(a, m.list(false), dtype == E3_BF16, hipStream_t(stream)),
+                      "linear_grouped");
+  });
+}
+
+namespace {
+
+std::vector<e3k::MixPair> mix_pairs(const Mix& m) {
+  std::vector<e3k::MixPair> p;
+  for (const auto& q : m.pairs)
+    p.push_back({m.in[size_t(q.i)].out_off, m.out[size_t(q.o)].out_off, m.in[size_t(q.i)].deg});
+  return p;
+}
+
+size_t mix_workspace(int64_t n_rows, int32_t n_groups, const Mix& m) {
+  const auto p = mix_pairs(m);
+  return 4 * e3k::mix_dw_part_floats(n_rows, n_groups, m.cin, m.cout, p.data(), int(p.size()));
+}
+
+}  // namespace
+
+e3_status e3_linear_grouped_workspace_size(const e3_irreps* in, const e3_irreps* out,
+                                           int64_t n_rows, int32_t n_groups, size_t* bytes) {
+  return guarded([&] {
+    Mix m;
+    e3_status s;
+    if ((s = check_groups(n_rows, n_groups)) != E3_OK ||
+        (s = parse_mix(in, out, n_rows, 8, m)) != E3_OK)
+      return s;
+    if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
+    *bytes = mix_workspace(n_rows, n_groups, m);
+    return ok();
+  });
+}
+
+e3_status e3_linear_grouped_backward(const e3_irreps* in, const e3_irreps* out, int64_t n_rows,
+                                     int32_t n_groups, const void* index, size_t index_bytes,
+                                     const void* x, const void* W, const void* dy, void* dx,
+                                     float* dW, void* workspace, size_t ws_bytes, e3_dtype dtype,
+                                     void* stream) {
+  return guarded([&] {
+    Mix m;
+    e3_status s;
+    if ((s = check_index(n_rows, n_groups, index, index_bytes)) != E3_OK ||
+        (s = parse_mix(in, out, n_rows, 8, m)) != E3_OK)
+      return s;
+    if (dtype != E3_F32 && dtype != E3_BF16) return fail(E3_ERR_INVALID_ARG, "unknown dtype");
+    const bool pairs = !m.pairs.empty();
+    if (n_rows > 0 && (!x || !dy || (dx && pairs && !W)))
+      return fail(E3_ERR_INVALID_ARG, "null pointer");
+    const size_t need = dW ? mix_workspace(n_rows, n_groups, m) : 0;
+    if (need > 0 && (!workspace || ws_bytes < need))
+      return fail(E3_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+    if (!aligned16(x) || !aligned16(W) || !aligned16(dy) || !aligned16(dx) || !aligned16(dW) ||
+        (need > 0 && !aligned16(workspace)))
+      return fail(E3_ERR_ALIGNMENT, "x, W, dy, dx, dW and the workspace must be 16-byte aligned");
+    const int esize = dtype == E3_BF16 ? 2 : 4;
+    const uint64_t weights = uint64_t(n_groups) * m.pairs.size() * m.cin * m.cout;
+    const Range rx = range(x, features_bytes(n_rows, m.din, m.cin, esize)),
+                rdy = range(dy, features_bytes(n_rows, m.dout, m.cout, esize)),
+                rdx = range(dx, dx ? rx.bytes : 0), rW = range(W, W ? weights * esize : 0),
+                rdW = range(dW, dW ? weights * 4 : 0), rws = range(workspace, need),
+                ri = range(index, index ? index_bytes : 0);
+    for (const Range& w : {rdx, rdW, rws})
+      for (const Range& r : {rx, rdy, rW, ri})
+        if (overlap(w, r))
+          return fail(E3_ERR_INVALID_ARG, "dx, dW or the workspace overlaps an input");
+    if (overlap(rdx, rdW) || overlap(rdx, rws) || overlap(rdW, rws))
+      return fail(E3_ERR_INVALID_ARG, "dx, dW and the workspace overlap");
+    const e3k::GroupLayout l = e3k::group_layout(n_rows, n_groups);
+    const int* idx = static_cast<const int*>(index);
+    const int np = int(m.pairs.size()), bf = dtype == E3_BF16;
+    if (dx && n_rows > 0) {
+      const e3k::MixArgs a{n_rows, n_groups, m.dout, m.din, m.cout, m.cin, np, 1,
+                           idx, int(l.offsets), int(l.order), dy, W, dx};
+      if ((s = hip_status(e3k::launch_mix(a, m.list(true), bf, hipStream_t(stream)),
+                          "linear_grouped_backward")) != E3_OK)
+        return s;
+    }
+    if (!dW || !pairs) return ok();
+    const e3k::MixDwArgs a{n_rows, n_groups, m.din, m.dout, m.cin, m.cout, np, idx,
+                           int(l.offsets), int(l.order), x, dy, dW,
+                           static_cast<float*>(workspace)};
+    const auto p = mix_pairs(m);
+    return hip_status(e3k::launch_mix_dw(a, p.data(), bf, hipStream_t(stream)),
+                      "linear_grouped_backward");
+  });
 }
 
 namespace {

@@ -1,0 +1,260 @@
+// Index of rows by group: `order` lists the rows of group 0, then those of
+// group 1 and so on, in their own order within each, then the rows that have
+// no group (an id outside [0, n_groups)); `offsets` says where each begins.
+//
+// A stable counting sort.  A chunk of rows is a workgroup's; each of its
+// wavefronts counts its own consecutive rows per group (LDS), so a row's place
+// is: where its group begins + the group's rows in earlier chunks + in earlier
+// wavefronts + in earlier lanes.  The lanes of a wavefront that share a group
+// find each other by one ballot per bit of the id.  Counts are whole numbers:
+// the order of the LDS atomics does not show.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "registry.h"
+
+namespace e3k {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kPerLane = 8;                         // rows of a lane
+constexpr int kChunk = kThreads * kPerLane;         // rows of a workgroup
+
+__device__ __forceinline__ int key_of(const int* group, int64_t r, int n_groups) {
+  const int g = group[r];
+  return unsigned(g) < unsigned(n_groups) ? g : n_groups;
+}
+
+// Lanes of this wavefront with the same key, the inactive ones left out.
+__device__ __forceinline__ uint64_t same_key(int key, int bits, bool active) {
+  uint64_t m = __ballot(active);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot((key >> b) & 1);
+    m &= (key >> b) & 1 ? set : ~set;
+  }
+  return m;
+}
+
+// Adds the wavefront's lanes to count[key]; returns the count before this lane.
+__device__ __forceinline__ int place(int* count, int key, int bits, bool active) {
+  const uint64_t same = same_key(key, bits, active);
+  const int lane = threadIdx.x & 63;
+  const int first = active ? __ffsll((unsigned long long)same) - 1 : lane;
+  int old = 0;
+  if (active && lane == first) old = atomicAdd(count + key, __popcll(same));
+  old = __shfl(old, first);
+  return old + __popcll(same & ((uint64_t(1) << lane) - 1));
+}
+
+// Exclusive prefix sums of v[0..n) in LDS by the whole workgroup, n <= 1025;
+// `part` holds a value for each thread.
+__device__ __forceinline__ void prefix(int* v, int n, int* part) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int per = (n + threads - 1) / threads;
+  int s = 0;
+  for (int j = 0; j < per; ++j) {
+    const int i = tid * per + j;
+    if (i < n) s += v[i];
+  }
+  part[tid] = s;
+  __syncthreads();
+  for (int o = 1; o < threads; o <<= 1) {
+    const int t = tid >= o ? part[tid - o] : 0;
+    __syncthreads();
+    part[tid] += t;
+    __syncthreads();
+  }
+  s = part[tid] - s;
+  for (int j = 0; j < per; ++j) {
+    const int i = tid * per + j;
+    if (i < n) {
+      const int t = v[i];
+      v[i] = s;
+      s += t;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void write_header(const GroupArgs& a) {
+  if (threadIdx.x == 0) {
+    a.index[0] = kGroupMagic;
+    a.index[1] = a.n_rows;
+    a.index[2] = a.n_groups;
+  }
+}
+
+// hist[g][chunk]: rows of group g in the chunk.
+__global__ void __launch_bounds__(kThreads) k_group_count(const GroupArgs a) {
+  __shared__ int s_n[kMaxGroups + 1];
+  const int G = a.n_groups;
+  for (int g = threadIdx.x; g <= G; g += kThreads) s_n[g] = 0;
+  __syncthreads();
+  const int64_t r0 = int64_t(blockIdx.x) * kChunk;
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) {
+    const int64_t r = r0 + j * kThreads + threadIdx.x;
+    if (r < a.n_rows) atomicAdd(s_n + key_of(a.group, r, G), 1);
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g <= G; g += kThreads)
+    a.hist[int64_t(g) * a.n_chunks + blockIdx.x] = s_n[g];
+}
+
+// A workgroup a group: hist becomes the rows of the group in earlier chunks,
+// total[g] those in all.
+__global__ void __launch_bounds__(kThreads) k_group_scan(const GroupArgs a) {
+  __shared__ int s_part[kThreads];
+  int* h = a.hist + int64_t(blockIdx.x) * a.n_chunks;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  int before = 0;
+  for (int c0 = 0; c0 < a.n_chunks; c0 += kThreads) {
+    const int c = c0 + tid;
+    const int n = c < a.n_chunks ? h[c] : 0;
+    int s = n;  // inclusive over the wavefront
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(s, o);
+      if (lane >= o) s += t;
+    }
+    __syncthreads();
+    if (lane == 63) s_part[w] = s;
+    __syncthreads();
+    int left = before;
+    for (int j = 0; j < kWaves; ++j) {
+      if (j < w) left += s_part[j];
+      before += s_part[j];
+    }
+    if (c < a.n_chunks) h[c] = left + s - n;
+  }
+  if (tid == 0) a.total[blockIdx.x] = before;
+}
+
+__global__ void __launch_bounds__(kThreads) k_group_place(const GroupArgs a) {
+  __shared__ int s_at[kWaves][kMaxGroups + 1];  // next place of each group in each wavefront
+  __shared__ int s_start[kMaxGroups + 1];
+  __shared__ int s_part[kThreads];
+  const int G = a.n_groups, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  for (int g = tid; g <= G; g += kThreads) {
+    s_start[g] = a.total[g];
+    for (int j = 0; j < kWaves; ++j) s_at[j][g] = 0;
+  }
+  __syncthreads();
+  prefix(s_start, G + 1, s_part);
+  if (blockIdx.x == 0) {
+    for (int g = tid; g <= G; g += kThreads) a.offsets[g] = s_start[g];
+    write_header(a);
+  }
+  const int64_t r0 = int64_t(blockIdx.x) * kChunk + w * 64 * kPerLane + lane;
+  int key[kPerLane];
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) {
+    const int64_t r = r0 + j * 64;
+    key[j] = r < a.n_rows ? key_of(a.group, r, G) : -1;
+    if (key[j] >= 0) atomicAdd(&s_at[w][key[j]], 1);
+  }
+  __syncthreads();
+  for (int g = tid; g <= G; g += kThreads) {
+    int at = s_start[g] + a.hist[int64_t(g) * a.n_chunks + blockIdx.x];
+    for (int j = 0; j < kWaves; ++j) {
+      const int n = s_at[j][g];
+      s_at[j][g] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) {
+    const int p = place(s_at[w], max(key[j], 0), a.bits, key[j] >= 0);
+    if (key[j] >= 0) a.order[p] = int(r0 + j * 64);
+  }
+}
+
+// Everything in one workgroup, for few rows: one launch instead of three.
+constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallRows = 8192;
+__global__ void __launch_bounds__(kSmallThreads) k_group_small(const GroupArgs a) {
+  __shared__ int s_at[kSmallWaves][kMaxGroups + 1];
+  __shared__ int s_start[kMaxGroups + 1];
+  __shared__ int s_part[kSmallThreads];
+  const int G = a.n_groups, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  for (int g = tid; g <= G; g += kSmallThreads)
+    for (int j = 0; j < kSmallWaves; ++j) s_at[j][g] = 0;
+  __syncthreads();
+  const int per = (a.n_rows + kSmallThreads - 1) / kSmallThreads;  // rows of a lane
+  const int r0 = w * 64 * per + lane;
+  for (int j = 0; j < per; ++j) {
+    const int r = r0 + j * 64;
+    if (r < a.n_rows) atomicAdd(&s_at[w][key_of(a.group, r, G)], 1);
+  }
+  __syncthreads();
+  for (int g = tid; g <= G; g += kSmallThreads) {
+    int n = 0;
+    for (int j = 0; j < kSmallWaves; ++j) n += s_at[j][g];
+    s_start[g] = n;
+  }
+  __syncthreads();
+  prefix(s_start, G + 1, s_part);
+  for (int g = tid; g <= G; g += kSmallThreads) {
+    int at = s_start[g];
+    a.offsets[g] = at;
+    for (int j = 0; j < kSmallWaves; ++j) {
+      const int n = s_at[j][g];
+      s_at[j][g] = at;
+      at += n;
+    }
+  }
+  write_header(a);
+  __syncthreads();
+  for (int j = 0; j < per; ++j) {
+    const int r = r0 + j * 64;
+    const bool in = r < a.n_rows;
+    const int key = in ? key_of(a.group, r, G) : 0;
+    const int p = place(s_at[w], key, a.bits, in);
+    if (in) a.order[p] = r;
+  }
+}
+
+}  // namespace
+
+GroupLayout group_layout(int64_t n_rows, int n_groups) {
+  const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };  // words of 64 bytes
+  GroupLayout l;
+  l.n_chunks = (n_rows + kChunk - 1) / kChunk;
+  l.offsets = 16;
+  l.order = l.offsets + up(n_groups + 1);
+  l.total = l.order + up(n_rows);
+  l.hist = l.total + up(n_groups + 1);
+  l.words = l.hist + (n_rows > kSmallRows ? up(l.n_chunks * (n_groups + 1)) : 0);
+  return l;
+}
+
+hipError_t launch_group_index(int n_rows, int n_groups, const int* group, int* index,
+                              hipStream_t s) {
+  const GroupLayout l = group_layout(n_rows, n_groups);
+  GroupArgs a{};
+  a.n_rows = n_rows;
+  a.n_groups = n_groups;
+  a.n_chunks = int(l.n_chunks);
+  while ((n_groups >> a.bits) != 0) ++a.bits;
+  a.group = group;
+  a.index = index;
+  a.offsets = index + l.offsets;
+  a.order = index + l.order;
+  a.total = index + l.total;
+  a.hist = index + l.hist;
+  if (n_rows <= kSmallRows) {
+    hipLaunchKernelGGL(k_group_small, dim3(1), dim3(kSmallThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_group_count, dim3(unsigned(a.n_chunks)), dim3(kThreads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_group_scan, dim3(unsigned(n_groups + 1)), dim3(kThreads), 0, s, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(k_group_place, dim3(unsigned(a.n_chunks)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace e3k

@@ -1,0 +1,525 @@
+// Channel mixing within each irrep (e3j A.3 Eq.5) with weights per group, and
+// its gradients: for the rows r of group g (chemical element, expert)
+//   y[r][o, m][k]  = sum over sources i of sum_k' x[r][i, m][k'] W[g][io][k'][k]
+//   dx: the same product over dy with W transposed
+//   dW[g][io]      = sum over the group's r and m of x[r][i, m]^T dy[r][o, m].
+// Rows stand in any order; the index of e3_group_index lists them by group,
+// and the kernels gather and scatter through it.  The rows of the products are
+// the (r, m) of an output block, cut into tiles that belong to one group.
+//
+// All products run on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16, fp32
+// accumulation).  A float32 operand is split into three bf16 parts, a = a1 +
+// a2 + a3 with each part the rest rounded to nearest: 24 bits and the range of
+// float32.  Of the nine products of two split operands the six largest are
+// kept; what is left out is below 2^-26 of a product.  Six bf16 products cost
+// 6/16 of a float32 one's matrix-core time.
+//
+// Layout of the operands (A[i][k]: lane i + 16 (k / 8) holds 8 consecutive k;
+// B[k][j] likewise; D[i][j]: register r of lane j + 16 h is i = 4 h + r): W is
+// taken as A and the rows of x as B, so that a lane ends with consecutive
+// columns of one row of y and stores 16 bytes at once.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.h"
+#include "group_tiles.h"
+#include "registry.h"
+
+namespace e3k {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;   // 4 wavefronts, 64 x 64 of the tile each
+constexpr int kTile = 128;      // rows and columns of a workgroup's tile
+
+// Chunk of the contraction in LDS, parts of an operand; rows are padded by 16
+// bytes, so that the 16-byte reads of 16 lanes in consecutive rows meet every
+// bank once.
+template <class T>
+struct Chunk;
+template <>
+struct Chunk<float> {
+  static constexpr int K = 32, PARTS = 3, LD = 40;
+};
+template <>
+struct Chunk<bf16_t> {
+  static constexpr int K = 64, PARTS = 1, LD = 72;
+};
+
+// Parts of 4 consecutive values.
+__device__ __forceinline__ void split3(const f32x4 v, bf16x4 (&p)[3]) {
+  p[0] = __builtin_convertvector(v, bf16x4);
+  f32x4 r = v - __builtin_convertvector(p[0], f32x4);
+  p[1] = __builtin_convertvector(r, bf16x4);
+  r -= __builtin_convertvector(p[1], f32x4);
+  p[2] = __builtin_convertvector(r, bf16x4);
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// The products of split operands, smallest first.
+template <int PARTS>
+__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[PARTS], const bf16x8 (&b)[PARTS],
+                                         f32x4 c) {
+  if constexpr (PARTS == 3) {
+    c = mfma(a[2], b[0], c);
+    c = mfma(a[0], b[2], c);
+    c = mfma(a[1], b[1], c);
+    c = mfma(a[1], b[0], c);
+    c = mfma(a[0], b[1], c);
+  }
+  return mfma(a[0], b[0], c);
+}
+
+// ------------------------------------------------------------ the mixing
+
+// Where column n of a tile lies in LDS: for bf16 results the columns of two
+// 16-column products alternate by fours, so that a lane's 4 + 4 results are 8
+// consecutive columns (16 bytes).
+template <class T>
+__device__ __forceinline__ int column_slot(int n) {
+  if constexpr (std::is_same_v<T, float>) return n;
+  else return (n & ~31) | ((n >> 2) & 1) << 4 | ((n >> 3) & 3) << 2 | (n & 3);
+}
+
+template <class T, bool WT>
+__global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList l) {
+  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS, LD = Chunk<T>::LD;
+  constexpr int VEC = 16 / sizeof(T);     // elements of a 16-byte load
+  constexpr int TPR = BK / VEC;           // threads of a row of a chunk: 8
+  constexpr int PASS = kThreads / TPR;    // rows of a pass: 32
+  constexpr int NP = kTile / PASS;        // passes: 4
+  static_assert(TPR == 8 && NP == 4);
+  __shared__ __bf16 s_x[PARTS][kTile][LD];
+  __shared__ __bf16 s_w[PARTS][kTile][LD];
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  int bi = 0;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  const MixBlock blk = l.blk[bi];
+  GroupTile tile;
+  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
+                 int64_t(blockIdx.x) - blk.wg0, tile))
+    return;
+  const int* order = a.index ? a.index + a.order + tile.first : nullptr;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
+  const int col0 = int(blockIdx.y) * kTile;
+  const int n_rows = int(min(int64_t(kTile), tile.rows - tile.at));
+  // row r of the tile: component m0 + r of the rows from `from` on
+  const int64_t from = tile.at / blk.deg;
+  const unsigned m0 = unsigned(tile.at - from * blk.deg);
+  const auto row_of = [&](int r, int& m) {
+    const unsigned c = m0 + unsigned(r), d = c / unsigned(blk.deg);
+    m = int(c - d * unsigned(blk.deg));
+    const int64_t p = from + d;
+    return order ? int64_t(order[p]) : p;
+  };
+
+  f32x4 acc[4][4];  // [columns][rows] of 16
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+
+  // the rows this thread stages, and its 16 bytes of them
+  const int piece = tid % TPR, r0 = tid / TPR;
+  const T* xrow[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int r = r0 + j * PASS;
+    int m;
+    const int64_t row = row_of(min(r, n_rows - 1), m);
+    xrow[j] = r < n_rows ? static_cast<const T*>(a.x) + (row * a.din + m) * a.cin + piece * VEC
+                         : nullptr;
+  }
+  const int n_src = tile.group < a.n_groups ? blk.n_src : 0;
+  const int chunks = (a.cin + BK - 1) / BK;
+  const T* W0 = static_cast<const T*>(a.W) + int64_t(tile.group) * a.pairs * a.cin * a.cout;
+
+  u32x4 xv[NP], wv[NP];
+  const auto fetch = [&](int step) {
+    const int src = step / chunks, k0 = (step - src * chunks) * BK;
+    const MixSource sc = l.src[blk.src0 + src];
+    const T* W = W0 + int64_t(sc.pair) * a.cin * a.cout;
+    const bool in = k0 + piece * VEC < a.cin;
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+      xv[j] = xrow[j] && in
+                  ? *reinterpret_cast<const u32x4*>(xrow[j] + int64_t(sc.in_off) * a.cin + k0)
+                  : u32x4{};
+    if constexpr (WT) {  // rows of W are columns here, k along them
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int n = col0 + r0 + j * PASS;
+        wv[j] = n < a.cout && in ? *reinterpret_cast<const u32x4*>(W + int64_t(n) * a.cin + k0 + piece * VEC)
+                                 : u32x4{};
+      }
+    } else {  // VEC columns of NP consecutive k
+      constexpr int CT = kTile / VEC;  // threads of a row of W
+      const int n = col0 + tid % CT * VEC, k = k0 + tid / CT * NP;
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        wv[j] = n < a.cout && k + j < a.cin
+                    ? *reinterpret_cast<const u32x4*>(W + int64_t(k + j) * a.cout + n)
+                    : u32x4{};
+    }
+  };
+  // 16 bytes along k into row r of an operand in LDS
+  const auto stage_row = [&](__bf16 (&s)[PARTS][kTile][LD], int r, u32x4 v) {
+    if constexpr (PARTS == 3) {
+      bf16x4 p[3];
+      split3(__builtin_bit_cast(f32x4, v), p);
+#pragma unroll
+      for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s[t][r][piece * VEC]) = p[t];
+    } else {
+      *reinterpret_cast<u32x4*>(&s[0][r][piece * VEC]) = v;
+    }
+  };
+  const auto stage = [&]() {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) stage_row(s_x, r0 + j * PASS, xv[j]);
+    if constexpr (WT) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) stage_row(s_w, column_slot<T>(r0 + j * PASS), wv[j]);
+    } else {
+      constexpr int CT = kTile / VEC;
+      const int n = tid % CT * VEC, k = tid / CT * NP;
+      if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < NP; ++j) v[j] = __builtin_bit_cast(f32x4, wv[j])[e];
+          bf16x4 p[3];
+          split3(v, p);
+#pragma unroll
+          for (int t = 0; t < 3; ++t)
+            *reinterpret_cast<bf16x4*>(&s_w[t][column_slot<T>(n + e)][k]) = p[t];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          bf16x4 v;
+#pragma unroll
+          for (int j = 0; j < NP; ++j) v[j] = __builtin_bit_cast(bf16x8, wv[j])[e];
+          *reinterpret_cast<bf16x4*>(&s_w[0][column_slot<T>(n + e)][k]) = v;
+        }
+      }
+    }
+  };
+
+  const int steps = n_src * chunks;
+  if (steps > 0) fetch(0);
+  for (int step = 0; step < steps; ++step) {
+    __syncthreads();  // the last chunk's reads are done
+    stage();
+    __syncthreads();
+    if (step + 1 < steps) fetch(step + 1);
+#pragma unroll
+    for (int kk = 0; kk < BK / 32; ++kk) {
+      bf16x8 xf[4][PARTS];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t)
+          xf[j][t] = *reinterpret_cast<const bf16x8*>(
+              &s_x[t][wm * 64 + j * 16 + q][kk * 32 + h * 8]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bf16x8 wf[PARTS];
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t)
+          wf[t] = *reinterpret_cast<const bf16x8*>(
+              &s_w[t][wn * 64 + i * 16 + q][kk * 32 + h * 8]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = product<PARTS>(wf, xf[j], acc[i][j]);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = wm * 64 + j * 16 + q;
+    if (r >= n_rows) continue;
+    int m;
+    const int64_t row = row_of(r, m);
+    T* y = static_cast<T*>(a.y) + (row * a.dout + blk.out_off + m) * a.cout;
+    if constexpr (PARTS == 3) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = col0 + wn * 64 + i * 16 + h * 4;
+        if (n < a.cout) *reinterpret_cast<f32x4*>(y + n) = acc[i][j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const int n = col0 + wn * 64 + i * 16 + h * 8;
+        bf16x8 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = __bf16(acc[i][j][e]);
+          v[4 + e] = __bf16(acc[i + 1][j][e]);
+        }
+        if (n < a.cout) *reinterpret_cast<bf16x8*>(y + n) = v;
+      }
+    }
+  }
+}
+
+template <class T>
+hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
+  int64_t wgs = 0;
+  for (int i = 0; i < l.n_blocks; ++i) {
+    l.blk[i].wg0 = int(wgs);
+    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTile, a.index != nullptr);
+    if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
+  }
+  const dim3 grid(unsigned(wgs), unsigned((a.cout + kTile - 1) / kTile));
+  if (a.w_trans) hipLaunchKernelGGL((k_mix<T, true>), grid, dim3(kThreads), 0, s, a, l);
+  else hipLaunchKernelGGL((k_mix<T, false>), grid, dim3(kThreads), 0, s, a, l);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------- weight gradients
+
+struct MixDwList {
+  int n_pairs;
+  MixPair p[kMixSources];
+};
+
+// Rows of a workgroup's part of the sum, 0 for all of a group's at once (then
+// there are no partials): enough workgroups to fill the chip.
+constexpr int kDwTarget = 1024;
+int64_t dw_rows(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* p, int n_pairs) {
+  const int64_t tiles = int64_t((cin + kTile - 1) / kTile) * ((cout + kTile - 1) / kTile);
+  int64_t comps = 0;
+  for (int i = 0; i < n_pairs; ++i) comps += p[i].deg;
+  const int64_t want = kDwTarget / tiles;  // parts of the sums, all pairs together
+  const int64_t rows = n_rows * comps;     // rows of all pairs
+  if (want <= int64_t(n_groups) * n_pairs || rows <= 512 * int64_t(n_groups) * n_pairs) return 0;
+  return std::max<int64_t>(256, (rows / want + 63) / 64 * 64);
+}
+
+// Channel of slot (e, c) of a tile: VEC c + e; slot = e (128 / VEC) + c, so
+// that neighbouring threads write neighbouring rows of LDS.
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const MixDwList l,
+                                                     int64_t part_rows, int slots) {
+  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS, LD = Chunk<T>::LD;
+  constexpr int VEC = 16 / sizeof(T), CT = kTile / VEC, NP = 4;
+  static_assert(kThreads / CT * NP == BK);
+  __shared__ __bf16 s_x[PARTS][kTile][LD];
+  __shared__ __bf16 s_y[PARTS][kTile][LD];
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const int* offsets = a.index ? a.index + a.offsets : nullptr;
+  const int pi = int(blockIdx.z);
+  const MixPair p = l.p[pi];
+  GroupTile tile;
+  int64_t n;  // rows of this workgroup
+  if (part_rows > 0) {
+    if (!find_tile(offsets, a.n_groups, a.n_rows, p.deg, part_rows, blockIdx.x, tile) ||
+        tile.group >= a.n_groups)
+      return;
+    n = min(part_rows, tile.rows - tile.at);
+  } else {
+    const int g = int(blockIdx.x);
+    const int64_t lo = offsets ? offsets[g] : 0, hi = offsets ? offsets[g + 1] : a.n_rows;
+    tile = {g, lo, (hi - lo) * p.deg, 0};
+    n = tile.rows;
+  }
+  const int* order = a.index ? a.index + a.order + tile.first : nullptr;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
+  const int col_tiles = (a.cout + kTile - 1) / kTile;
+  const int a0 = int(blockIdx.y) / col_tiles * kTile, b0 = int(blockIdx.y) % col_tiles * kTile;
+
+  f32x4 acc[4][4];  // [input channels][output channels]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+
+  // this thread's VEC channels of NP consecutive rows of a chunk
+  const int c = tid % CT, k = tid / CT * NP;
+  const bool in_x = a0 + c * VEC < a.cin, in_y = b0 + c * VEC < a.cout;
+  u32x4 xv[NP], yv[NP];
+  const auto fetch = [&](int64_t k0) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int64_t r = tile.at + k0 + k + j;  // of the group's rows
+      const bool valid = k0 + k + j < n;
+      const int64_t at = valid ? r / p.deg : 0;
+      const int m = valid ? int(r - at * p.deg) : 0;
+      const int64_t row = valid ? (order ? int64_t(order[at]) : at) : 0;
+      xv[j] = valid && in_x ? *reinterpret_cast<const u32x4*>(
+                                  static_cast<const T*>(a.x) +
+                                  (row * a.din + p.in_off + m) * a.cin + a0 + c * VEC)
+                            : u32x4{};
+      yv[j] = valid && in_y ? *reinterpret_cast<const u32x4*>(
+                                  static_cast<const T*>(a.dy) +
+                                  (row * a.dout + p.out_off + m) * a.cout + b0 + c * VEC)
+                            : u32x4{};
+    }
+  };
+  const auto stage = [&](__bf16 (&s)[PARTS][kTile][LD], const u32x4 (&v)[NP]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if constexpr (PARTS == 3) {
+        f32x4 t;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) t[j] = __builtin_bit_cast(f32x4, v[j])[e];
+        bf16x4 part[3];
+        split3(t, part);
+#pragma unroll
+        for (int u = 0; u < 3; ++u) *reinterpret_cast<bf16x4*>(&s[u][e * CT + c][k]) = part[u];
+      } else {
+        bf16x4 t;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) t[j] = __builtin_bit_cast(bf16x8, v[j])[e];
+        *reinterpret_cast<bf16x4*>(&s[0][e * CT + c][k]) = t;
+      }
+    }
+  };
+  // LDS row of lane q of product i of this wavefront's 64 channels, and the
+  // channel: a lane's four products are four consecutive channels
+  const auto slot_of = [&](int w, int i, int lane16) {
+    if constexpr (PARTS == 3) return i * CT + w * 16 + lane16;
+    else return (i + 4 * (lane16 >> 3)) * CT + w * 8 + (lane16 & 7);
+  };
+  const auto channel_of = [&](int w, int lane16) {  // of product 0
+    if constexpr (PARTS == 3) return (w * 16 + lane16) * 4;
+    else return (w * 8 + (lane16 & 7)) * 8 + 4 * (lane16 >> 3);
+  };
+
+  if (n > 0) fetch(0);
+  for (int64_t k0 = 0; k0 < n; k0 += BK) {
+    __syncthreads();
+    stage(s_x, xv);
+    stage(s_y, yv);
+    __syncthreads();
+    if (k0 + BK < n) fetch(k0 + BK);
+#pragma unroll
+    for (int kk = 0; kk < BK / 32; ++kk) {
+      bf16x8 yf[4][PARTS];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t)
+          yf[j][t] = *reinterpret_cast<const bf16x8*>(
+              &s_y[t][slot_of(wn, j, q)][kk * 32 + h * 8]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bf16x8 xf[PARTS];
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t)
+          xf[t] = *reinterpret_cast<const bf16x8*>(&s_x[t][slot_of(wm, i, q)][kk * 32 + h * 8]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = product<PARTS>(xf, yf[j], acc[i][j]);
+      }
+    }
+  }
+
+  const int64_t size = int64_t(a.cin) * a.cout;
+  float* out = part_rows > 0
+                   ? a.part + (int64_t(pi) * slots + blockIdx.x) * size
+                   : a.dW + (int64_t(tile.group) * a.pairs + pi) * size;
+  const int col = b0 + channel_of(wn, q);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = a0 + channel_of(wm, 4 * h + r) + i;
+      f32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = acc[i][j][r];
+      if (row < a.cin && col < a.cout) *reinterpret_cast<f32x4*>(out + int64_t(row) * a.cout + col) = v;
+    }
+  }
+}
+
+// dW from the partials of every group, in their order: a workgroup per 1024
+// elements of a (group, pair).
+__global__ void __launch_bounds__(256) k_mix_dw_sum(const MixDwArgs a, const MixDwList l,
+                                                    int64_t part_rows, int slots) {
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const int g = int(blockIdx.y), pi = int(blockIdx.z), deg = l.p[pi].deg;
+  const int64_t size = int64_t(a.cin) * a.cout;
+  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  // the group's first slot: tiles of the groups before it
+  __shared__ int s_first;
+  if (threadIdx.x == 0) s_first = 0;
+  __syncthreads();
+  const auto tiles = [&](int i) {
+    if (!a.index) return int((a.n_rows * deg + part_rows - 1) / part_rows);
+    const int* offsets = a.index + a.offsets;
+    return int((int64_t(offsets[i + 1] - offsets[i]) * deg + part_rows - 1) / part_rows);
+  };
+  int mine = 0;
+  for (int i = threadIdx.x; i < g; i += 256) mine += tiles(i);
+  if (mine) atomicAdd(&s_first, mine);
+  __syncthreads();
+  const int first = s_first, n = tiles(g);
+  if (e >= size) return;
+  const float* part = a.part + (int64_t(pi) * slots + first) * size + e;
+  f32x4 s{};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) s += *reinterpret_cast<const f32x4*>(part + i * size);
+  *reinterpret_cast<f32x4*>(a.dW + (int64_t(g) * a.pairs + pi) * size + e) = s;
+}
+
+int dw_slots(int64_t n_rows, int n_groups, int64_t rows, const MixPair* p, int n_pairs,
+             bool grouped) {
+  int64_t most = 0;
+  for (int i = 0; i < n_pairs; ++i)
+    most = std::max(most, most_tiles(n_rows, n_groups, p[i].deg, rows, grouped));
+  return int(most);
+}
+
+template <class T>
+hipError_t launch_mix_dw_t(const MixDwArgs& a, const MixPair* p, hipStream_t s) {
+  MixDwList l;
+  l.n_pairs = a.pairs;
+  for (int i = 0; i < a.pairs; ++i) l.p[i] = p[i];
+  const int64_t rows = dw_rows(a.n_rows, a.n_groups, a.cin, a.cout, p, a.pairs);
+  const int slots = rows > 0 ? dw_slots(a.n_rows, a.n_groups, rows, p, a.pairs, a.index != nullptr)
+                             : a.n_groups;
+  const unsigned tiles = unsigned((a.cin + kTile - 1) / kTile) *
+                         unsigned((a.cout + kTile - 1) / kTile);
+  hipLaunchKernelGGL((k_mix_dw<T>), dim3(unsigned(slots), tiles, unsigned(a.pairs)),
+                     dim3(kThreads), 0, s, a, l, rows, slots);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || rows == 0) return e;
+  hipLaunchKernelGGL(k_mix_dw_sum,
+                     dim3(unsigned((int64_t(a.cin) * a.cout + 1023) / 1024),
+                          unsigned(a.n_groups), unsigned(a.pairs)),
+                     dim3(256), 0, s, a, l, rows, slots);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mix(const MixArgs& a, const MixList& l, int bf16, hipStream_t s) {
+  return bf16 ? launch_mix_t<bf16_t>(a, l, s) : launch_mix_t<float>(a, l, s);
+}
+
+size_t mix_dw_part_floats(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* p,
+                          int n_pairs) {
+  const int64_t rows = dw_rows(n_rows, n_groups, cin, cout, p, n_pairs);
+  if (rows == 0) return 0;
+  return size_t(dw_slots(n_rows, n_groups, rows, p, n_pairs, true)) * n_pairs * cin * cout;
+}
+
+hipError_t launch_mix_dw(const MixDwArgs& a, const MixPair* p, int bf16, hipStream_t s) {
+  return bf16 ? launch_mix_dw_t<bf16_t>(a, p, s) : launch_mix_dw_t<float>(a, p, s);
+}
+
+}  // namespace e3k

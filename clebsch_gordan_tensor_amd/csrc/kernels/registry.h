@@ -445,6 +445,75 @@ hipError_t launch_grad_norm(const ParamTensor* t, int n, double max_norm, double
 hipError_t launch_adamw(const ParamTensor* t, int n, const AdamArgs& a, hipStream_t s);
 hipError_t launch_moments8(const ParamTensor* t, int n, hipStream_t s);
 
+// Index of rows by group (group.hip), in int32 words of the caller's buffer:
+// a header (magic, rows, groups), where every group begins, the rows in order,
+// and scratch of the sort (totals, counts per group and chunk).
+constexpr int kMaxGroups = 1024;
+constexpr int kGroupMagic = 0x65336769;
+struct GroupLayout {
+  int64_t n_chunks, offsets, order, total, hist, words;
+};
+GroupLayout group_layout(int64_t n_rows, int n_groups);
+struct GroupArgs {
+  int n_rows, n_groups, n_chunks;
+  int bits;  // of n_groups, the key of rows without a group
+  const int* group;
+  int* index;
+  int* offsets;
+  int* order;
+  int* total;
+  int* hist;
+};
+hipError_t launch_group_index(int n_rows, int n_groups, const int* group, int* index,
+                              hipStream_t s);
+
+// Channel mixing with weights per group (grouped.hip): for every output block
+// the sources it sums over, an input block and the pair's weight matrix each.
+constexpr int kMixBlocks = 32, kMixSources = 256;
+struct MixSource {
+  int in_off, pair;
+};
+struct MixBlock {
+  int out_off, deg;  // first component, components
+  int src0, n_src;
+  int wg0;           // first row tile of the launch
+};
+struct MixList {
+  int n_blocks, n_src;
+  MixBlock blk[kMixBlocks];
+  MixSource src[kMixSources];
+};
+struct MixArgs {
+  int64_t n_rows;
+  int n_groups, din, dout, cin, cout, pairs;
+  int w_trans;       // W holds [cout][cin] matrices (the backward's W^T)
+  const int* index;  // of e3_group_index, or null: one group, rows as they are
+  int offsets, order;  // where these lie in the index
+  const void* x;
+  const void* W;     // [groups][pairs][cin][cout], storage type
+  void* y;
+};
+hipError_t launch_mix(const MixArgs& a, const MixList& l, int bf16, hipStream_t s);
+
+// Weight gradient dW [groups][pairs][cin][cout] = sum of x^T dy over the rows
+// of a group.
+struct MixDwArgs {
+  int64_t n_rows;
+  int n_groups, din, dout, cin, cout, pairs;
+  const int* index;
+  int offsets, order;
+  const void* x;
+  const void* dy;
+  float* dW;
+  float* part;  // mix_dw_part_floats floats
+};
+struct MixPair {
+  int in_off, out_off, deg;
+};
+size_t mix_dw_part_floats(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* p,
+                          int n_pairs);
+hipError_t launch_mix_dw(const MixDwArgs& a, const MixPair* p, int bf16, hipStream_t s);
+
 // Workspace layout of the transposed edge index (int32 words).
 struct TransposeLayout {
   int64_t npad, colptr, cursor, tmp_e, tmp_b, perm, recv, padlist, order, flag, pos, key, order2,

@@ -638,6 +638,59 @@ e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const 
                                  void* dx, float* dweight, float* dbias, void* workspace,
                                  size_t ws_bytes, e3_dtype dtype, void* stream);
 
+/* Rows by group, for weights that differ from group to group (a group is a
+ * chemical element, or an expert): from group[r] (int32, device) of n_rows
+ * rows, an index that lists the rows of group 0, of group 1 and so on, in
+ * ascending order within each, and last those whose id lies outside [0,
+ * n_groups), which belong to none.  The caller owns the index
+ * (e3_group_index_size bytes, 16-byte aligned); it is built once for a
+ * system's atoms, or again for every batch, and read by the calls below.  At
+ * the bytes that e3_group_index_at gives (host only) it holds, int32,
+ *   offsets[n_groups + 1]   where each group begins in the order, and its end
+ *   order[n_rows]           the rows
+ * n_groups up to 1024, n_rows below 2^31. */
+e3_status e3_group_index_size(int64_t n_rows, int32_t n_groups, size_t* bytes);
+e3_status e3_group_index_at(int64_t n_rows, int32_t n_groups, size_t* offsets, size_t* order);
+e3_status e3_group_index(int64_t n_rows, int32_t n_groups, const int32_t* group, void* index,
+                         size_t bytes, void* stream);
+
+/* Channel mixing (as e3_linear) with the weights of each row's group g(r):
+ *   y[r][o, m][k] = sum over input blocks i with (l_i, p_i) = (l_o, p_o) of
+ *                   sum_{k'} x[r][i, m][k'] W[g(r)][io][k'][k].
+ * W [n_groups][pairs][Cin][Cout], the pairs in e3_linear's order, in the
+ * storage type (for bf16 the copies that e3_adamw writes).  index: of
+ * e3_group_index for this n_rows and n_groups (with an index of other sizes
+ * the call changes nothing); NULL for a single group.  Rows without a group
+ * get 0.  Cin and Cout multiples of 8 up to 8192, degrees up to 8, at most 32
+ * blocks on a side and 256 pairs; x, W, y 16-byte aligned, y overlapping
+ * nothing.  float32 products keep 24 bits of both factors (three bf16 parts
+ * each on the bf16 matrix cores); a component row of x that holds a value
+ * that is not finite in bf16 (past 3.39e38) gives NaN throughout its row of
+ * y, and such a weight in its column.  Sums are float32, in an order that does not
+ * depend on the other rows. */
+e3_status e3_linear_grouped(const e3_irreps* in, const e3_irreps* out, int64_t n_rows,
+                            int32_t n_groups, const void* index, size_t index_bytes, const void* x,
+                            const void* W, void* y, e3_dtype dtype, void* stream);
+
+/* Backward of e3_linear_grouped for the cotangent dy [n_rows][dout][Cout]:
+ *   dx[r][i, m][k']     = sum over output blocks o of the type of i of
+ *                         sum_k dy[r][o, m][k] W[g(r)][io][k'][k]
+ *   dW[g][io][k'][k]    = sum over the rows r of group g and over m of
+ *                         x[r][i, m][k'] dy[r][o, m][k]     float32, like W
+ * dx in the storage type; either of dx and dW may be NULL (not wanted).  Rows
+ * without a group get dx = 0, a group without rows dW = 0.  dW is summed
+ * through fixed partials in the caller's workspace
+ * (e3_linear_grouped_workspace_size bytes, which may be none; 16-byte
+ * aligned; one for each of calls that may overlap): reproducible.  Limits as
+ * the forward. */
+e3_status e3_linear_grouped_workspace_size(const e3_irreps* in, const e3_irreps* out,
+                                           int64_t n_rows, int32_t n_groups, size_t* bytes);
+e3_status e3_linear_grouped_backward(const e3_irreps* in, const e3_irreps* out, int64_t n_rows,
+                                     int32_t n_groups, const void* index, size_t index_bytes,
+                                     const void* x, const void* W, const void* dy, void* dx,
+                                     float* dW, void* workspace, size_t ws_bytes, e3_dtype dtype,
+                                     void* stream);
+
 /* One tensor of a network's weights with what its update reads and writes:
  * the optimizer calls take a HOST array of at most 65536 of these (device
  * pointers inside; read during the call only).  Every pointer needs its element's alignment.
