@@ -65,6 +65,8 @@ EXPORTS = ["e3_num_paths", "e3_path_info", "e3_supported", "e3_cg_block",
            "e3_adamw_moments",
            "e3_group_index_size", "e3_group_index_at", "e3_group_index", "e3_linear_grouped",
            "e3_linear_grouped_workspace_size", "e3_linear_grouped_backward",
+           "e3_layer_norm_residual", "e3_layer_norm_residual_backward", "e3_layer_norm_fp8",
+           "e3_quantize_fp8", "e3_linear_fp8_pack_size", "e3_linear_fp8_pack", "e3_linear_fp8",
            "e3_release_all",
            "e3_last_error"]
 E3_GEN_FORWARD, E3_GEN_DX, E3_GEN_DW, E3_GEN_DY, E3_GEN_GEMM = 0, 1, 2, 3, 4
@@ -173,6 +175,15 @@ def lib():
     L.e3_linear_grouped_workspace_size.argtypes = [ip, ip, i64, i32, szp]
     L.e3_linear_grouped_backward.argtypes = [ip, ip, i64, i32, vp, sz, vp, vp, vp, vp, vp, vp, sz,
                                              C.c_int, vp]
+    f32 = C.c_float
+    L.e3_layer_norm_residual.argtypes = [ip, i64, vp, vp, vp, vp, f32, i32, vp, vp, C.c_int, vp]
+    L.e3_layer_norm_residual_backward.argtypes = [ip, i64, vp, vp, vp, vp, f32, i32, vp, vp, vp, vp,
+                                                  sz, C.c_int, vp]
+    L.e3_layer_norm_fp8.argtypes = [ip, i64, vp, vp, vp, vp, f32, i32, vp, vp, vp, C.c_int, vp]
+    L.e3_quantize_fp8.argtypes = [i64, i32, vp, vp, vp, C.c_int, vp]
+    L.e3_linear_fp8_pack_size.argtypes = [ip, ip, i32, szp]
+    L.e3_linear_fp8_pack.argtypes = [ip, ip, i32, vp, vp, sz, vp]
+    L.e3_linear_fp8.argtypes = [ip, ip, i64, i32, vp, sz, vp, vp, vp, sz, vp, C.c_int, vp]
     pp = C.POINTER(_Param)
     L.e3_param_check.argtypes = [i32, pp]
     L.e3_grad_norm_workspace_size.argtypes = [i32, pp, C.POINTER(sz)]
@@ -1169,6 +1180,108 @@ def layer_norm_backward(irreps, x, weight, dy, eps=1e-5, flags=0, dx=None, dweig
     return dx, dweight, dbias
 
 
+def layer_norm_residual(irreps, x, residual, weight=None, bias=None, eps=1e-5, flags=0, h=None,
+                        out=None, stream=None):
+    """(y, h): h = x + residual in x's type, y = layer_norm(h) in one pass.
+    h or out may be x or residual."""
+    import torch
+    irreps, (st, _, n_blocks, scalars) = _norm_x(irreps, x)
+    dev, shape = x.device, x.shape
+    _need(residual, "residual")
+    _need_on(dev, residual, "residual", shape, x.dtype)
+    _need_on(dev, weight, "weight", (n_blocks, shape[2]), torch.float32)
+    _need_on(dev, bias, "bias", (scalars, shape[2]), torch.float32)
+    _need_on(dev, h, "h", shape, x.dtype)
+    _need_on(dev, out, "out", shape, x.dtype)
+    if h is None:
+        h = _new(stream, shape, dev, x.dtype)
+    if out is None:
+        out = _new(stream, shape, dev, x.dtype)
+    _on(dev, lib().e3_layer_norm_residual, C.byref(st), shape[0], x.data_ptr(),
+        residual.data_ptr(), _addr(weight), _addr(bias), eps, flags, h.data_ptr(), out.data_ptr(),
+        _dtype_code(x), stream=stream)
+    return out, h
+
+
+def layer_norm_residual_backward(irreps, h, weight, dy, dh, eps=1e-5, flags=0, dx=None,
+                                 dweight=None, dbias=None, workspace=None, stream=None):
+    """(dx, dweight [blocks][C], dbias [0e blocks][C]) of layer_norm_residual
+    for the cotangents dy of y and dh of h; dx is the gradient of x and of the
+    residual.  dx may be h, dy or dh."""
+    import torch
+    irreps, (st, _, n_blocks, scalars) = _norm_x(irreps, h)
+    dev, shape, f32 = h.device, h.shape, torch.float32
+    ch = shape[2]
+    _need_on(dev, weight, "weight", (n_blocks, ch), f32)
+    for t, name in ((dy, "dy"), (dh, "dh")):
+        _need(t, name)
+        _need_on(dev, t, name, shape, h.dtype)
+    _need_on(dev, dx, "dx", shape, h.dtype)
+    _need_on(dev, dweight, "dweight", (n_blocks, ch), f32)
+    _need_on(dev, dbias, "dbias", (scalars, ch), f32)
+    _need_on(dev, workspace, "workspace", None, None)
+    if dx is None:
+        dx = _new(stream, shape, dev, h.dtype)
+    if dweight is None:
+        dweight = _new(stream, (n_blocks, ch), dev, f32)
+    if dbias is None:
+        dbias = _new(stream, (scalars, ch), dev, f32)
+    if workspace is None:
+        workspace = _new(stream, _norm_workspace_size(irreps, shape[0], ch), dev, torch.uint8)
+    _on(dev, lib().e3_layer_norm_residual_backward, C.byref(st), shape[0], h.data_ptr(),
+        _addr(weight), dy.data_ptr(), dh.data_ptr(), eps, flags, dx.data_ptr(),
+        dweight.data_ptr(), dbias.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _dtype_code(h), stream=stream)
+    return dx, dweight, dbias
+
+
+# ------------------------------------------------------------ 8-bit features
+
+def _fp8_out(dev, shape, q, scale, stream):
+    """Codes (torch.float8_e4m3fn) and scales for features of a shape."""
+    import torch
+    runs = (*shape[:-1], -(-shape[-1] // 128))
+    _need_on(dev, q, "q", shape, torch.float8_e4m3fn)
+    _need_on(dev, scale, "scale", runs, torch.float32)
+    return (_new(stream, shape, dev, torch.float8_e4m3fn) if q is None else q,
+            _new(stream, runs, dev, torch.float32) if scale is None else scale)
+
+
+def quantize_fp8(x, q=None, scale=None, stream=None):
+    """(q, scale): x [...][C] in 8 bits (torch.float8_e4m3fn) with a scale for
+    every 128 channels, [...][ceil(C / 128)]; x stands as q times its run's
+    scale."""
+    _need(x, "x")
+    if x.dim() == 0:
+        raise ValueError("x needs a channel axis")
+    dev = x.device
+    q, scale = _fp8_out(dev, x.shape, q, scale, stream)
+    _on(dev, lib().e3_quantize_fp8, x.numel() // max(1, x.shape[-1]), x.shape[-1], x.data_ptr(),
+        q.data_ptr(), scale.data_ptr(), _dtype_code(x), stream=stream)
+    return q, scale
+
+
+def layer_norm_fp8(irreps, x, residual=None, weight=None, bias=None, eps=1e-5, flags=0, h=None,
+                   q=None, scale=None, stream=None):
+    """(q, scale, h) of layer_norm_residual with the normalised features in 8
+    bits (as quantize_fp8 gives them), or (q, scale) of layer_norm without a
+    residual."""
+    import torch
+    irreps, (st, _, n_blocks, scalars) = _norm_x(irreps, x)
+    dev, shape = x.device, x.shape
+    _need_on(dev, residual, "residual", shape, x.dtype)
+    _need_on(dev, weight, "weight", (n_blocks, shape[2]), torch.float32)
+    _need_on(dev, bias, "bias", (scalars, shape[2]), torch.float32)
+    _need_on(dev, h, "h", shape, x.dtype)
+    if residual is not None and h is None:
+        h = _new(stream, shape, dev, x.dtype)
+    q, scale = _fp8_out(dev, shape, q, scale, stream)
+    _on(dev, lib().e3_layer_norm_fp8, C.byref(st), shape[0], x.data_ptr(), _addr(residual),
+        _addr(weight), _addr(bias), eps, flags, _addr(h), q.data_ptr(), scale.data_ptr(),
+        _dtype_code(x), stream=stream)
+    return (q, scale) if residual is None else (q, scale, h)
+
+
 # ------------------------------------------------------------- grouped rows
 
 @functools.lru_cache(maxsize=256)
@@ -1319,6 +1432,79 @@ def linear_grouped_backward(in_irreps, out_irreps, index, x, W, dy, dx=None, dW=
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _dtype_code(x),
         stream=stream)
     return dx, dW
+
+
+class Fp8Weights:
+    """Weights of linear_fp8_pack: ``buffer`` holds the 8-bit form of
+    [groups][pairs][cin][cout] of them."""
+
+    def __init__(self, buffer, groups, pairs, cin, cout):
+        self.buffer, self.groups, self.pairs, self.cin, self.cout = buffer, groups, pairs, cin, cout
+
+
+@functools.lru_cache(maxsize=256)
+def _pack_size(into, out, cin, cout, groups):
+    nb = C.c_size_t()
+    a, b = _mix_spec(into, out, cin, cout)[:2]
+    _check(lib().e3_linear_fp8_pack_size(C.byref(a), C.byref(b), groups, C.byref(nb)))
+    return nb.value
+
+
+def linear_fp8_pack(in_irreps, out_irreps, W, packed=None, stream=None) -> Fp8Weights:
+    """The 8-bit form of weights W [groups][pairs][Cin][Cout] (float32), a
+    scale for every 128 x 128 of them, laid out for linear_fp8.  packed: a
+    Fp8Weights of the same sizes to write again."""
+    import torch
+    _need(W, "W", dtype=torch.float32)
+    if W.dim() != 4:
+        raise ValueError(f"W has shape {tuple(W.shape)}, expected [groups][pairs][Cin][Cout]")
+    groups, pairs, cin, cout = W.shape
+    into, out = tuple(map(tuple, in_irreps)), tuple(map(tuple, out_irreps))
+    a, b, _, _, n = _mix_spec(into, out, cin, cout)
+    if pairs != n:
+        raise ValueError(f"W has {pairs} pairs, the irreps {n}")
+    dev, nb = W.device, _pack_size(into, out, cin, cout, groups)
+    if packed is None:
+        packed = Fp8Weights(_new(stream, nb, dev, torch.uint8), *W.shape)
+    elif (packed.groups, packed.pairs, packed.cin, packed.cout) != tuple(W.shape):
+        raise ValueError("the packed weights are of other sizes than W")
+    _need_on(dev, packed.buffer, "packed", None, None)
+    _on(dev, lib().e3_linear_fp8_pack, C.byref(a), C.byref(b), groups, W.data_ptr(),
+        packed.buffer.data_ptr(), packed.buffer.numel(), stream=stream)
+    return packed
+
+
+def linear_fp8(in_irreps, out_irreps, q, scale, packed, index=None, dtype=None, out=None,
+               stream=None):
+    """y [rows][dout][Cout] (dtype: torch.bfloat16, the default, or float32) =
+    channel mixing of 8-bit features q [rows][din][Cin] and their scales (of
+    quantize_fp8 or layer_norm_fp8) with packed weights; index: of
+    group_rows, where the weights differ by group."""
+    import torch
+    _need(q, "q", dtype=torch.float8_e4m3fn)
+    if not isinstance(packed, Fp8Weights):
+        raise TypeError("packed must be of linear_fp8_pack")
+    if q.dim() != 3 or q.shape[2] != packed.cin:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [rows][components]"
+                         f"[{packed.cin}]")
+    into, out_ir = tuple(map(tuple, in_irreps)), tuple(map(tuple, out_irreps))
+    a, b, din, dout, pairs = _mix_spec(into, out_ir, packed.cin, packed.cout)
+    if q.shape[1] != din or pairs != packed.pairs:
+        raise ValueError("q or the packed weights do not match the irreps")
+    dev, rows = q.device, q.shape[0]
+    _need_on(dev, scale, "scale", (rows, din, -(-packed.cin // 128)), torch.float32)
+    _need(scale, "scale")
+    _need_on(dev, packed.buffer, "packed", None, None)
+    at, nb = _index_args(dev, index, rows, packed.groups)
+    shape = (rows, dout, packed.cout)
+    if out is None:
+        out = _new(stream, shape, dev, dtype or torch.bfloat16)
+    else:
+        _need_on(dev, out, "out", shape, dtype or out.dtype)
+    _on(dev, lib().e3_linear_fp8, C.byref(a), C.byref(b), rows, packed.groups, at, nb,
+        q.data_ptr(), scale.data_ptr(), packed.buffer.data_ptr(), packed.buffer.numel(),
+        out.data_ptr(), _dtype_code(out), stream=stream)
+    return out
 
 
 # ---------------------------------------------------------------- optimizer

@@ -33,8 +33,11 @@ HIP_SOURCES = [
     "kernels/generic.hip",
     "kernels/gemm.hip",
     "kernels/norm.hip",
+    "kernels/norm_residual.hip",
+    "kernels/norm_fp8.hip",
     "kernels/group.hip",
     "kernels/grouped.hip",
+    "kernels/fp8.hip",
     "kernels/optimizer.hip",
     "api.cpp",
     "host/cg_ladder.cpp",

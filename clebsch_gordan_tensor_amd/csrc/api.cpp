@@ -16,6 +16,7 @@
 
 #include "e3hip.h"
 #include "host/cg_ladder.h"
+#include "kernels/fp8.h"
 #include "kernels/registry.h"
 
 namespace {
@@ -2747,6 +2748,230 @@ e3_status e3_linear_grouped_backward(const e3_irreps* in, const e3_irreps* out, 
     const auto p = mix_pairs(m);
     return hip_status(e3k::launch_mix_dw(a, p.data(), bf, hipStream_t(stream)),
                       "linear_grouped_backward");
+  });
+}
+
+e3_status e3_layer_norm_residual(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                                 const void* residual, const float* weight, const float* bias,
+                                 float eps, int32_t flags, void* h, void* y, e3_dtype dtype,
+                                 void* stream) {
+  return guarded([&] {
+    Norm n;
+    e3_status s;
+    if ((s = parse_norm(irreps, n_rows, flags, n)) != E3_OK || (s = norm_args(eps, dtype)) != E3_OK)
+      return s;
+    if (n_rows == 0) return ok();
+    if (!x || !residual || !h || !y) return fail(E3_ERR_INVALID_ARG, "null pointer");
+    const unsigned esize = dtype == E3_BF16 ? 2 : 4;
+    if (!aligned_to(x, esize) || !aligned_to(residual, esize) || !aligned_to(h, esize) ||
+        !aligned_to(y, esize) || !aligned_to(weight, 4) || !aligned_to(bias, 4))
+      return fail(E3_ERR_ALIGNMENT,
+                  "x, residual, h, y, weight and bias must be aligned to their elements");
+    const uint64_t bytes = uint64_t(n_rows) * n.dim * n.C * esize;
+    for (const void* out : {static_cast<const void*>(h), static_cast<const void*>(y)})
+      for (const void* in : {x, residual})
+        if (partly_overlaps(out, in, bytes))
+          return fail(E3_ERR_INVALID_ARG, "h or y overlaps x or residual without being it");
+    if (overlap(range(h, bytes), range(y, bytes)))
+      return fail(E3_ERR_INVALID_ARG, "h and y overlap");
+    e3k::NormArgs a{};
+    a.n_rows = n_rows;
+    a.dim = n.dim;
+    a.C = n.C;
+    a.x = x;
+    a.add = residual;
+    a.h = h;
+    a.y = y;
+    a.w = weight;
+    a.b = bias;
+    a.eps = eps;
+    return hip_status(e3k::launch_norm(false, a, n.blocks.data(), int(n.blocks.size()),
+                                       dtype == E3_BF16, hipStream_t(stream)),
+                      "layer_norm_residual");
+  });
+}
+
+e3_status e3_layer_norm_residual_backward(const e3_irreps* irreps, int64_t n_rows, const void* h,
+                                          const float* weight, const void* dy, const void* dh,
+                                          float eps, int32_t flags, void* dx, float* dweight,
+                                          float* dbias, void* workspace, size_t ws_bytes,
+                                          e3_dtype dtype, void* stream) {
+  return guarded([&] {
+    Norm n;
+    e3_status s;
+    if ((s = parse_norm(irreps, n_rows, flags, n)) != E3_OK || (s = norm_args(eps, dtype)) != E3_OK)
+      return s;
+    const size_t need = norm_workspace(n, n_rows);
+    if (!workspace || ws_bytes < need)
+      return fail(E3_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+    if (n_rows > 0 && (!h || !dy || !dh || !dx)) return fail(E3_ERR_INVALID_ARG, "null pointer");
+    const unsigned esize = dtype == E3_BF16 ? 2 : 4;
+    if (!aligned16(workspace)) return fail(E3_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    if (!aligned_to(h, esize) || !aligned_to(dy, esize) || !aligned_to(dh, esize) ||
+        !aligned_to(dx, esize) || !aligned_to(weight, 4) || !aligned_to(dweight, 4) ||
+        !aligned_to(dbias, 4))
+      return fail(E3_ERR_ALIGNMENT, "h, dy, dh, dx, weight, dweight and dbias must be aligned to "
+                                    "their elements");
+    const uint64_t bytes = uint64_t(n_rows) * n.dim * n.C * esize;
+    if (partly_overlaps(dx, h, bytes) || partly_overlaps(dx, dy, bytes) ||
+        partly_overlaps(dx, dh, bytes))
+      return fail(E3_ERR_INVALID_ARG, "dx overlaps h, dy or dh without being it");
+    e3k::NormArgs a{};
+    a.n_rows = n_rows;
+    a.dim = n.dim;
+    a.C = n.C;
+    a.x = h;
+    a.dy = dy;
+    a.add = dh;
+    a.y = dx;
+    a.w = weight;
+    a.dw = dweight;
+    a.db = dbias;
+    a.part = static_cast<float*>(workspace);
+    a.eps = eps;
+    if (n_rows == 0) a.add = workspace;  // selects the kernels, is not read
+    return hip_status(e3k::launch_norm(true, a, n.blocks.data(), int(n.blocks.size()),
+                                       dtype == E3_BF16, hipStream_t(stream)),
+                      "layer_norm_residual_backward");
+  });
+}
+
+e3_status e3_layer_norm_fp8(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                            const void* residual, const float* weight, const float* bias, float eps,
+                            int32_t flags, void* h, void* q, float* scale, e3_dtype dtype,
+                            void* stream) {
+  return guarded([&] {
+    Norm n;
+    e3_status s;
+    if ((s = parse_norm(irreps, n_rows, flags, n)) != E3_OK || (s = norm_args(eps, dtype)) != E3_OK)
+      return s;
+    if (n.C % 16 != 0)
+      return fail(E3_ERR_UNSUPPORTED, "8-bit features need a multiple of 16 channels");
+    if (n_rows == 0) return ok();
+    if (!x || !q || !scale || !residual != !h) return fail(E3_ERR_INVALID_ARG, "null pointer");
+    const unsigned esize = dtype == E3_BF16 ? 2 : 4;
+    if (!aligned_to(x, esize) || !aligned_to(residual, esize) || !aligned_to(h, esize) ||
+        !aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(scale, 4))
+      return fail(E3_ERR_ALIGNMENT,
+                  "x, residual, h, weight, bias and scale must be aligned to their elements");
+    if (!aligned16(q)) return fail(E3_ERR_ALIGNMENT, "q must be 16-byte aligned");
+    const uint64_t n_q = uint64_t(n_rows) * n.dim * n.C, bytes = n_q * esize;
+    const Range rq = range(q, n_q),
+                rs = range(scale, uint64_t(n_rows) * n.dim * e3k::fp8_runs(n.C) * 4);
+    if (h && (partly_overlaps(h, x, bytes) || partly_overlaps(h, residual, bytes)))
+      return fail(E3_ERR_INVALID_ARG, "h overlaps x or residual without being it");
+    for (const void* p : {x, residual, static_cast<const void*>(h)})
+      if (p && (overlap(rq, range(p, bytes)) || overlap(rs, range(p, bytes))))
+        return fail(E3_ERR_INVALID_ARG, "q or scale overlaps x, residual or h");
+    if (overlap(rq, rs)) return fail(E3_ERR_INVALID_ARG, "q and scale overlap");
+    e3k::NormArgs a{};
+    a.n_rows = n_rows;
+    a.dim = n.dim;
+    a.C = n.C;
+    a.x = x;
+    a.add = residual;
+    a.h = h;
+    a.q = q;
+    a.scale = scale;
+    a.w = weight;
+    a.b = bias;
+    a.eps = eps;
+    return hip_status(e3k::launch_norm_fp8(a, n.blocks.data(), int(n.blocks.size()),
+                                           dtype == E3_BF16, hipStream_t(stream)),
+                      "layer_norm_fp8");
+  });
+}
+
+e3_status e3_quantize_fp8(int64_t n_rows, int32_t channels, const void* x, void* q, float* scale,
+                          e3_dtype dtype, void* stream) {
+  if (dtype != E3_F32 && dtype != E3_BF16) return fail(E3_ERR_INVALID_ARG, "unknown dtype");
+  if (n_rows < 0) return fail(E3_ERR_INVALID_ARG, "n_rows < 0");
+  if (channels < 1) return fail(E3_ERR_INVALID_ARG, "channels < 1");
+  if (channels % 16 != 0 || channels > kMixChannels)
+    return fail(E3_ERR_UNSUPPORTED, "8-bit features need a multiple of 16 channels, up to 8192");
+  if (n_rows > (int64_t(1) << 56) / channels) return fail(E3_ERR_UNSUPPORTED, "n_rows too large");
+  if (n_rows == 0) return ok();
+  if (!x || !q || !scale) return fail(E3_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(q) || !aligned_to(scale, 4))
+    return fail(E3_ERR_ALIGNMENT, "x and q must be 16-byte aligned, scale to its element");
+  const Range rx = range(x, uint64_t(n_rows) * channels * (dtype == E3_BF16 ? 2 : 4)),
+              rq = range(q, uint64_t(n_rows) * channels),
+              rs = range(scale, uint64_t(n_rows) * e3k::fp8_runs(channels) * 4);
+  if (overlap(rx, rq) || overlap(rx, rs) || overlap(rq, rs))
+    return fail(E3_ERR_INVALID_ARG, "x, q and scale overlap");
+  return hip_status(e3k::launch_fp8_quantize(n_rows, channels, x, dtype == E3_BF16, q, scale,
+                                             hipStream_t(stream)),
+                    "quantize_fp8");
+}
+
+e3_status e3_linear_fp8_pack_size(const e3_irreps* in, const e3_irreps* out, int32_t n_groups,
+                                  size_t* bytes) {
+  return guarded([&] {
+    Mix m;
+    e3_status s;
+    if ((s = check_groups(0, n_groups)) != E3_OK || (s = parse_mix(in, out, 0, 16, m)) != E3_OK)
+      return s;
+    if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
+    *bytes = size_t(e3k::fp8_layout(n_groups, int(m.pairs.size()), m.cin, m.cout).bytes);
+    return ok();
+  });
+}
+
+e3_status e3_linear_fp8_pack(const e3_irreps* in, const e3_irreps* out, int32_t n_groups,
+                             const float* W, void* packed, size_t bytes, void* stream) {
+  return guarded([&] {
+    Mix m;
+    e3_status s;
+    if ((s = check_groups(0, n_groups)) != E3_OK || (s = parse_mix(in, out, 0, 16, m)) != E3_OK)
+      return s;
+    const int pairs = int(m.pairs.size());
+    const size_t need = size_t(e3k::fp8_layout(n_groups, pairs, m.cin, m.cout).bytes);
+    if (!packed || bytes < need)
+      return fail(E3_ERR_WORKSPACE, "the packed weights have " + std::to_string(need) + " bytes");
+    if (pairs == 0) return ok();
+    if (!W) return fail(E3_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(W) || !aligned16(packed))
+      return fail(E3_ERR_ALIGNMENT, "W and the packed weights must be 16-byte aligned");
+    if (overlap(range(W, uint64_t(n_groups) * pairs * m.cin * m.cout * 4), range(packed, need)))
+      return fail(E3_ERR_INVALID_ARG, "W and the packed weights overlap");
+    return hip_status(e3k::launch_fp8_pack(n_groups, pairs, m.cin, m.cout, W, packed,
+                                           hipStream_t(stream)),
+                      "linear_fp8_pack");
+  });
+}
+
+e3_status e3_linear_fp8(const e3_irreps* in, const e3_irreps* out, int64_t n_rows,
+                        int32_t n_groups, const void* index, size_t index_bytes, const void* q,
+                        const float* scale, const void* packed, size_t packed_bytes, void* y,
+                        e3_dtype dtype, void* stream) {
+  return guarded([&] {
+    Mix m;
+    e3_status s;
+    if ((s = check_index(n_rows, n_groups, index, index_bytes)) != E3_OK ||
+        (s = parse_mix(in, out, n_rows, 16, m)) != E3_OK)
+      return s;
+    if (dtype != E3_F32 && dtype != E3_BF16) return fail(E3_ERR_INVALID_ARG, "unknown dtype");
+    const int pairs = int(m.pairs.size());
+    const size_t need = size_t(e3k::fp8_layout(n_groups, pairs, m.cin, m.cout).bytes);
+    if (pairs > 0 && (!packed || packed_bytes < need))
+      return fail(E3_ERR_WORKSPACE, "the packed weights have " + std::to_string(need) + " bytes");
+    if (n_rows == 0) return ok();
+    if (!q || !scale || !y) return fail(E3_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(q) || !aligned16(packed) || !aligned16(y) || !aligned_to(scale, 4))
+      return fail(E3_ERR_ALIGNMENT, "q, the packed weights and y must be 16-byte aligned, scale to "
+                                    "its element");
+    const Range ry = range(y, features_bytes(n_rows, m.dout, m.cout, dtype == E3_BF16 ? 2 : 4));
+    if (overlap(ry, range(q, features_bytes(n_rows, m.din, m.cin, 1))) ||
+        overlap(ry, range(scale, features_bytes(n_rows, m.din, e3k::fp8_runs(m.cin), 4))) ||
+        overlap(ry, range(packed, packed ? packed_bytes : 0)) ||
+        overlap(ry, range(index, index ? index_bytes : 0)))
+      return fail(E3_ERR_INVALID_ARG, "y overlaps an input");
+    const e3k::GroupLayout l = e3k::group_layout(n_rows, n_groups);
+    const e3k::Fp8MixArgs a{n_rows, n_groups, m.din, m.dout, m.cin, m.cout, pairs,
+                            static_cast<const int*>(index), int(l.offsets), int(l.order), q, scale,
+                            packed, y};
+    return hip_status(e3k::launch_fp8_mix(a, m.list(false), dtype == E3_BF16, hipStream_t(stream)),
+                      "linear_fp8");
   });
 }
 

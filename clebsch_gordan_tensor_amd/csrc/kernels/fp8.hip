@@ -1,0 +1,362 @@
+// Channel mixing of 8-bit features with 8-bit weights (e4m3), next to the
+// quantisation of both: with s_x a scale for 128 channels of a component row
+// of x and s_W one for 128 x 128 weights,
+//   y[r][n] = sum over blocks b of 128 channels of
+//             s_x[r][b] s_W[b][n / 128] sum_{k in b} x8[r][k] W8[k][n].
+// The inner sum of a block enters the float32 result by one multiply-add with
+// the product of the two scales, which the columns of a block and a lane's row
+// share.  It is formed
+//   for bf16 y by one instruction, v_mfma_f32_16x16x128_f8f6f4.  Within 8
+//     consecutive products that drops what lies below 2^-13 of the largest one
+//     (measured, and so does v_mfma_f32_16x16x32_fp8_fp8); the eights are added
+//     in float32.  On normal values the sums are off by 1.5e-5 (root mean
+//     square, relative), a hundredth of the rounding to bf16 that follows;
+//   for float32 y from the codes' values in bf16, which are exact, by four
+//     v_mfma_f32_16x16x32_bf16 (2e-8 off on the same values).
+//
+// Operands: a lane q + 16 h holds 32 bytes of row (or column) q, the bytes
+// 16 h .. 16 h + 15 of either half of the block; which k these are does not
+// matter as long as both operands agree.  W is taken as A: register r of lane
+// q + 16 h is column 4 h + r of row q.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.h"
+#include "fp8.h"
+#include "group_tiles.h"
+#include "registry.h"
+
+namespace e3k {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;
+
+// ------------------------------------------------------------ quantisation
+
+// A run of 128 channels of a row: 32 lanes of 4 (float32) or 16 of 8 (bf16).
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+    k_fp8_quantize(int64_t n_runs, int runs, int C, const T* __restrict__ x,
+                   uint8_t* __restrict__ q, float* __restrict__ scale) {
+  constexpr int V = 16 / sizeof(T), L = kFp8Run / V;
+  const int lane = threadIdx.x % L;
+  for (int64_t t = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / L; t < n_runs;
+       t += int64_t(gridDim.x) * (kThreads / L)) {
+    const int64_t row = t / runs;
+    const int k = int(t - row * runs) * kFp8Run + lane * V;
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    if (k < C) load_ch<T, V>(x + row * C + k, v);
+    float top = fp8_top(v);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) top = fp8_max(top, __shfl_xor(top, o));
+    const Fp8Scale s(top);
+    if (k < C) fp8_store<V, false>(q + row * C + k, v, s);
+    if (lane == 0) scale[t] = s.scale;
+  }
+}
+
+// A block of 128 x 128 weights a workgroup: thread (c, k) takes 4 columns of
+// 16 consecutive k, whose codes it stores side by side.
+__global__ void __launch_bounds__(kThreads)
+    k_fp8_pack(int pairs, int groups, int cin, int cout, Fp8Layout l, const float* __restrict__ W,
+               uint8_t* __restrict__ packed) {
+  __shared__ float s_top[kThreads / 64];
+  const int64_t mat = blockIdx.x / l.in_blocks;
+  const int kb = int(blockIdx.x % l.in_blocks), nb = int(blockIdx.y), tid = threadIdx.x;
+  if (kb == 0 && nb == 0 && mat == 0 && tid == 0) {
+    int* header = reinterpret_cast<int*>(packed);
+    header[0] = kFp8Magic;
+    header[1] = cin;
+    header[2] = cout;
+    header[3] = pairs;
+    header[4] = groups;
+  }
+  const int n = nb * 128 + tid % 32 * 4, k0 = kb * 128 + tid / 32 * 16;
+  const float* w = W + mat * cin * cout;
+  f32x4 v[16];
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    v[j] = k0 + j < cin && n < cout
+               ? *reinterpret_cast<const f32x4*>(w + int64_t(k0 + j) * cout + n)
+               : f32x4{};
+    const float t[4] = {v[j][0], v[j][1], v[j][2], v[j][3]};
+    top = fp8_max(top, fp8_top(t));
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) top = fp8_max(top, __shfl_xor(top, o));
+  if ((tid & 63) == 0) s_top[tid >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kThreads / 64; ++j) top = fp8_max(top, s_top[j]);
+  const Fp8Scale s(top);
+  if (tid == 0)
+    reinterpret_cast<float*>(packed + l.scales)[(mat * l.out_blocks + nb) * l.in_blocks + kb] =
+        s.scale;
+  if (n >= cout) return;
+  uint8_t* out = packed + l.codes + (mat * cout + n) * (int64_t(l.in_blocks) * 128) + k0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    u32x4 c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = fp8_codes(v[4 * j][e], v[4 * j + 1][e], v[4 * j + 2][e], v[4 * j + 3][e], s);
+    *reinterpret_cast<u32x4*>(out + int64_t(e) * l.in_blocks * 128) = c;
+  }
+}
+
+// --------------------------------------------------------------- the mixing
+
+// A block's operand of one row or column: the codes, or their values.
+struct Values {
+  bf16x8 v[4];
+};
+template <class T>
+struct Operand {
+  using type = i32x8;
+  __device__ __forceinline__ static i32x8 of(i32x8 c) { return c; }
+};
+template <>
+struct Operand<float> {
+  using type = Values;
+  __device__ __forceinline__ static Values of(i32x8 c) {
+    Values r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false);
+      const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true);
+      r.v[i / 2][i % 2 * 4] = lo[0];
+      r.v[i / 2][i % 2 * 4 + 1] = lo[1];
+      r.v[i / 2][i % 2 * 4 + 2] = hi[0];
+      r.v[i / 2][i % 2 * 4 + 3] = hi[1];
+    }
+    return r;
+  }
+};
+__device__ __forceinline__ f32x4 product(const i32x8& a, const i32x8& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 product(const Values& a, const Values& b) {
+  f32x4 c{};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+
+// Slot of column n of a tile: as the results are stored 16 bytes at once, for
+// bf16 two products' columns alternate by fours.
+template <class T>
+__device__ __forceinline__ int column_slot(int n) {
+  if constexpr (std::is_same_v<T, float>) return n;
+  else return (n & ~31) | ((n >> 2) & 1) << 4 | ((n >> 3) & 3) << 2 | (n & 3);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const MixList l,
+                                                      const Fp8Layout at) {
+  constexpr int LD = 128 + 16;
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[kTile][LD];
+  __shared__ __attribute__((aligned(16))) uint8_t s_w[kTile][LD];
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const int* header = static_cast<const int*>(a.packed);
+  if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
+      header[3] != a.pairs || header[4] != a.n_groups)
+    return;  // packed for another call
+  int bi = 0;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  const MixBlock blk = l.blk[bi];
+  GroupTile tile;
+  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
+                 int64_t(blockIdx.x) - blk.wg0, tile))
+    return;
+  const int* order = a.index ? a.index + a.order + tile.first : nullptr;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
+  const int col0 = int(blockIdx.y) * kTile;
+  const int n_rows = int(min(int64_t(kTile), tile.rows - tile.at));
+  const int64_t from = tile.at / blk.deg;
+  const unsigned m0 = unsigned(tile.at - from * blk.deg);
+  const auto row_of = [&](int r, int& m) {
+    const unsigned c = m0 + unsigned(r), d = c / unsigned(blk.deg);
+    m = int(c - d * unsigned(blk.deg));
+    const int64_t p = from + d;
+    return order ? int64_t(order[p]) : p;
+  };
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+
+  const int piece = tid % 8, r0 = tid / 8;  // 16 bytes of 4 rows
+  const int runs = at.in_blocks;
+  const uint8_t* xrow[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = r0 + j * 32;
+    int m;
+    const int64_t row = row_of(min(r, n_rows - 1), m);
+    xrow[j] = r < n_rows ? static_cast<const uint8_t*>(a.q) + (row * a.din + m) * a.cin + piece * 16
+                         : nullptr;
+  }
+  // the rows this lane ends with, and where their scales are
+  int64_t row[4];
+  int comp[4];
+  const float* srow[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    row[j] = row_of(min(wm * 64 + j * 16 + q, n_rows - 1), comp[j]);
+    srow[j] = a.scale + (row[j] * a.din + comp[j]) * runs;
+  }
+  const int n_src = tile.group < a.n_groups ? blk.n_src : 0;
+  const uint8_t* packed = static_cast<const uint8_t*>(a.packed);
+  const int64_t kpad = int64_t(runs) * 128;
+
+  u32x4 xv[4], wv[4];
+  float sx[4], sw;
+  const auto fetch = [&](int step) {
+    const int src = step / runs, b = step - src * runs;
+    const MixSource sc = l.src[blk.src0 + src];
+    const int64_t mat = int64_t(tile.group) * a.pairs + sc.pair;
+    const bool in = b * 128 + piece * 16 < a.cin;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      xv[j] = xrow[j] && in
+                  ? *reinterpret_cast<const u32x4*>(xrow[j] + int64_t(sc.in_off) * a.cin + b * 128)
+                  : u32x4{};
+      const int n = col0 + r0 + j * 32;
+      wv[j] = n < a.cout ? *reinterpret_cast<const u32x4*>(packed + at.codes +
+                                                           (mat * a.cout + n) * kpad + b * 128 +
+                                                           piece * 16)
+                         : u32x4{};
+      sx[j] = srow[j][sc.in_off * runs + b];
+    }
+    sw = reinterpret_cast<const float*>(packed + at.scales)[(mat * at.out_blocks + blockIdx.y) *
+                                                                runs + b];
+  };
+  const int steps = n_src * runs;
+  if (steps > 0) fetch(0);
+  for (int step = 0; step < steps; ++step) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      *reinterpret_cast<u32x4*>(&s_x[r0 + j * 32][piece * 16]) = xv[j];
+      *reinterpret_cast<u32x4*>(&s_w[column_slot<T>(r0 + j * 32)][piece * 16]) = wv[j];
+    }
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = sx[j] * sw;
+    __syncthreads();
+    if (step + 1 < steps) fetch(step + 1);
+    const auto operand = [&](const uint8_t (&s)[kTile][LD], int r) {
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(&s[r][h * 16]);
+      const u32x4 hi = *reinterpret_cast<const u32x4*>(&s[r][64 + h * 16]);
+      return Operand<T>::of(i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
+                                  int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])});
+    };
+    typename Operand<T>::type xf[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xf[j] = operand(s_x, wm * 64 + j * 16 + q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto wf = operand(s_w, wn * 64 + i * 16 + q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 t = product(wf, xf[j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[r], f[j], acc[i][j][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (wm * 64 + j * 16 + q >= n_rows) continue;
+    T* y = static_cast<T*>(a.y) + (row[j] * a.dout + blk.out_off + comp[j]) * a.cout;
+    if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = col0 + wn * 64 + i * 16 + h * 4;
+        if (n < a.cout) *reinterpret_cast<f32x4*>(y + n) = acc[i][j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const int n = col0 + wn * 64 + i * 16 + h * 8;
+        bf16x8 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = __bf16(acc[i][j][e]);
+          v[4 + e] = __bf16(acc[i + 1][j][e]);
+        }
+        if (n < a.cout) *reinterpret_cast<bf16x8*>(y + n) = v;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+Fp8Layout fp8_layout(int n_groups, int pairs, int cin, int cout) {
+  Fp8Layout l;
+  l.in_blocks = fp8_runs(cin);
+  l.out_blocks = fp8_runs(cout);
+  const int64_t mats = int64_t(n_groups) * pairs;
+  l.scales = 64;
+  l.codes = l.scales + (mats * l.in_blocks * l.out_blocks * 4 + 63) / 64 * 64;
+  l.bytes = l.codes + mats * cout * l.in_blocks * 128;
+  return l;
+}
+
+hipError_t launch_fp8_pack(int n_groups, int pairs, int cin, int cout, const float* W, void* packed,
+                           hipStream_t s) {
+  const Fp8Layout l = fp8_layout(n_groups, pairs, cin, cout);
+  hipLaunchKernelGGL(k_fp8_pack,
+                     dim3(unsigned(l.in_blocks) * n_groups * pairs, unsigned(l.out_blocks)),
+                     dim3(kThreads), 0, s, pairs, n_groups, cin, cout, l, W,
+                     static_cast<uint8_t*>(packed));
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_quantize(int64_t n_rows, int C, const void* x, int bf16, void* q,
+                               float* scale, hipStream_t s) {
+  const int runs = fp8_runs(C);
+  const int64_t n = n_rows * runs;
+  const auto go = [&](auto t) {
+    using T = decltype(t);
+    constexpr int per = kThreads / (kFp8Run * int(sizeof(T)) / 16);  // runs of a workgroup
+    const int64_t wgs = std::min<int64_t>((n + per - 1) / per, 1 << 20);
+    hipLaunchKernelGGL((k_fp8_quantize<T>), dim3(unsigned(wgs)), dim3(kThreads), 0, s, n, runs, C,
+                       static_cast<const T*>(x), static_cast<uint8_t*>(q), scale);
+    return hipGetLastError();
+  };
+  return bf16 ? go(bf16_t{}) : go(float{});
+}
+
+hipError_t launch_fp8_mix(const Fp8MixArgs& a, const MixList& list, int bf16, hipStream_t s) {
+  MixList l = list;
+  int64_t wgs = 0;
+  for (int i = 0; i < l.n_blocks; ++i) {
+    l.blk[i].wg0 = int(wgs);
+    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTile, a.index != nullptr);
+  }
+  if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
+  const Fp8Layout at = fp8_layout(a.n_groups, a.pairs, a.cin, a.cout);
+  const dim3 grid(unsigned(wgs), unsigned((a.cout + kTile - 1) / kTile));
+  if (bf16) hipLaunchKernelGGL((k_fp8_mix<bf16_t>), grid, dim3(kThreads), 0, s, a, l, at);
+  else hipLaunchKernelGGL((k_fp8_mix<float>), grid, dim3(kThreads), 0, s, a, l, at);
+  return hipGetLastError();
+}
+
+}  // namespace e3k

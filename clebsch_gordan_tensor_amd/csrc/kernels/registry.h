@@ -389,6 +389,10 @@ struct NormArgs {
   float* db;
   float* part;   // backward: partials [slot][dw, db][C]
   int part_step; // a block's partials lie in slots wg0, wg0 + part_step, ...
+  const void* add; // forward: the residual; backward: the cotangent along it; or null
+  void* h;         // forward: x + residual
+  void* q;         // launch_norm_fp8: the results, and the scales of their runs
+  float* scale;
   float eps;
   NormBlock blk[kNormMaxBlocks];
 };
@@ -397,6 +401,10 @@ size_t norm_part_floats(int64_t n_rows, int dim, int C, const NormBlock* blocks,
                         int esize);
 hipError_t launch_norm(bool bwd, const NormArgs& a, const NormBlock* blocks, int n_blocks,
                        int bf16, hipStream_t s);
+hipError_t launch_norm_residual(bool bwd, const NormArgs& a, const NormBlock* blocks, int n_blocks,
+                                int bf16, hipStream_t s);
+hipError_t launch_norm_fp8(const NormArgs& a, const NormBlock* blocks, int n_blocks, int bf16,
+                           hipStream_t s);
 
 // Lists of parameter tensors (optimizer.hip), passed in the kernel arguments
 // (4 KB at most).
@@ -513,6 +521,32 @@ struct MixPair {
 size_t mix_dw_part_floats(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* p,
                           int n_pairs);
 hipError_t launch_mix_dw(const MixDwArgs& a, const MixPair* p, int bf16, hipStream_t s);
+
+// 8-bit features and weights (fp8.hip).  Packed weights: a header of 64 bytes
+// (magic, cin, cout, pairs, groups), the scales of their 128 x 128 blocks
+// [groups][pairs][output blocks][input blocks], then the codes
+// [groups][pairs][cout][cin rounded up to 128].
+constexpr int kFp8Magic = 0x65336638;
+struct Fp8Layout {
+  int in_blocks, out_blocks;
+  int64_t scales, codes, bytes;  // byte offsets
+};
+Fp8Layout fp8_layout(int n_groups, int pairs, int cin, int cout);
+hipError_t launch_fp8_pack(int n_groups, int pairs, int cin, int cout, const float* W, void* packed,
+                           hipStream_t s);
+hipError_t launch_fp8_quantize(int64_t n_rows, int C, const void* x, int bf16, void* q,
+                               float* scale, hipStream_t s);
+struct Fp8MixArgs {
+  int64_t n_rows;
+  int n_groups, din, dout, cin, cout, pairs;
+  const int* index;
+  int offsets, order;
+  const void* q;
+  const float* scale;  // [rows][din][runs of 128 channels]
+  const void* packed;
+  void* y;
+};
+hipError_t launch_fp8_mix(const Fp8MixArgs& a, const MixList& l, int bf16, hipStream_t s);
 
 // Workspace layout of the transposed edge index (int32 words).
 struct TransposeLayout {

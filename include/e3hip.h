@@ -638,6 +638,52 @@ e3_status e3_layer_norm_backward(const e3_irreps* irreps, int64_t n_rows, const 
                                  void* dx, float* dweight, float* dbias, void* workspace,
                                  size_t ws_bytes, e3_dtype dtype, void* stream);
 
+/* The normalisation (as e3_layer_norm) of x + residual, for networks whose
+ * layers add to their features:
+ *   h = x + residual, added in float32 and rounded to the storage type
+ *   y = e3_layer_norm(h)
+ * x, residual, h, y [n_rows][dim][C] in the storage type.  h or y may be x or
+ * residual, but must not overlap them otherwise, nor each other.  Bitwise
+ * e3_layer_norm's y of the same h; everything else as there. */
+e3_status e3_layer_norm_residual(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                                 const void* residual, const float* weight, const float* bias,
+                                 float eps, int32_t flags, void* h, void* y, e3_dtype dtype,
+                                 void* stream);
+
+/* Its backward for the cotangents dy of y and dh of h: dx is the gradient of
+ * x and of residual alike,
+ *   dx = dh + (dx of e3_layer_norm_backward for h and dy)
+ * added in float32; dweight, dbias and the workspace (of
+ * e3_layer_norm_workspace_size) as there.  dx may be h, dy or dh, but must not
+ * overlap them otherwise. */
+e3_status e3_layer_norm_residual_backward(const e3_irreps* irreps, int64_t n_rows, const void* h,
+                                          const float* weight, const void* dy, const void* dh,
+                                          float eps, int32_t flags, void* dx, float* dweight,
+                                          float* dbias, void* workspace, size_t ws_bytes,
+                                          e3_dtype dtype, void* stream);
+
+/* Features in 8 bits, for simulation: e4m3 codes (4 bits of exponent, 3 of
+ * mantissa, no infinities, largest 448) q [n_rows][dim][C], a byte each, with
+ * a float32 scale for every 128 consecutive channels of a component row (the
+ * last run may be shorter), scale [n_rows][dim][ceil(C / 128)]:
+ *   scale = max(max |v| (1/448), 2^-126) over the run, in float32;
+ *   q = v / scale, the float32 quotient rounded to nearest (ties to even).
+ * v stands as q scale.
+ * A run that holds a value that is not finite has the scale NaN.  C a multiple
+ * of 16; q 16-byte aligned.
+ *   e3_quantize_fp8: of x [n_rows][channels] (for features n_rows is rows x
+ *     components; channels up to 8192; x 16-byte aligned).
+ *   e3_layer_norm_fp8: of the normalised features, which are not rounded to the
+ *     storage type before; with a residual (both residual and h given) of
+ *     e3_layer_norm_residual's, h written as there, or without (both NULL).
+ *     Limits of e3_layer_norm. */
+e3_status e3_quantize_fp8(int64_t n_rows, int32_t channels, const void* x, void* q, float* scale,
+                          e3_dtype dtype, void* stream);
+e3_status e3_layer_norm_fp8(const e3_irreps* irreps, int64_t n_rows, const void* x,
+                            const void* residual, const float* weight, const float* bias, float eps,
+                            int32_t flags, void* h, void* q, float* scale, e3_dtype dtype,
+                            void* stream);
+
 /* Rows by group, for weights that differ from group to group (a group is a
  * chemical element, or an expert): from group[r] (int32, device) of n_rows
  * rows, an index that lists the rows of group 0, of group 1 and so on, in
@@ -690,6 +736,32 @@ e3_status e3_linear_grouped_backward(const e3_irreps* in, const e3_irreps* out, 
                                      const void* x, const void* W, const void* dy, void* dx,
                                      float* dW, void* workspace, size_t ws_bytes, e3_dtype dtype,
                                      void* stream);
+
+/* Channel mixing (as e3_linear_grouped, forward only) of 8-bit features with
+ * 8-bit weights:
+ *   y[r][o, m][n] = sum over input blocks i of the type of o and over runs b of
+ *     scale[r][i, m][b] s_W[b][n / 128] sum_{k in b} q[r][i, m][k] W8[k][n]
+ *   e3_linear_fp8_pack: lays out float32 weights W [n_groups][pairs][Cin][Cout]
+ *     once, in the caller's memory (e3_linear_fp8_pack_size bytes, 16-byte
+ *     aligned): e4m3 codes with a scale for every 128 x 128 of them, formed as
+ *     for features; a block that holds a weight that is not finite stands as NaN.
+ *   e3_linear_fp8: q and scale of e3_quantize_fp8 or e3_layer_norm_fp8, y
+ *     [n_rows][dout][Cout] of type dtype; index as for e3_linear_grouped (NULL
+ *     for a single group).  Weights packed for other sizes change nothing.
+ * For float32 y the products are exact and the sums float32; for bf16 y the
+ * sums of 8 consecutive products drop what lies below 2^-13 of the largest one
+ * (the 8-bit matrix cores), far below the rounding of y.
+ * Cin and Cout multiples of 16 up to 8192; otherwise e3_linear_grouped's
+ * limits.  scale x s_W is formed in float32: features and weights whose scales
+ * multiply to less than 2^-126 lose digits. */
+e3_status e3_linear_fp8_pack_size(const e3_irreps* in, const e3_irreps* out, int32_t n_groups,
+                                  size_t* bytes);
+e3_status e3_linear_fp8_pack(const e3_irreps* in, const e3_irreps* out, int32_t n_groups,
+                             const float* W, void* packed, size_t bytes, void* stream);
+e3_status e3_linear_fp8(const e3_irreps* in, const e3_irreps* out, int64_t n_rows,
+                        int32_t n_groups, const void* index, size_t index_bytes, const void* q,
+                        const float* scale, const void* packed, size_t packed_bytes, void* y,
+                        e3_dtype dtype, void* stream);
 
 /* One tensor of a network's weights with what its update reads and writes:
  * the optimizer calls take a HOST array of at most 65536 of these (device
