@@ -321,17 +321,23 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
   __shared__ __bf16 s_y[PARTS][kTile][LD];
   if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
   const int* offsets = a.index ? a.index + a.offsets : nullptr;
-  const int pi = int(blockIdx.z);
+  const int pi = int(blockIdx.y);
   const MixPair p = l.p[pi];
+  // tiles of dW: neighbouring workgroups are on different XCDs, each of which
+  // takes neighbouring tiles, whose rows of x and dy meet in its L2
+  const int tiles = ((a.cin + kTile - 1) / kTile) * ((a.cout + kTile - 1) / kTile);
+  int tile_of = int(blockIdx.x) % tiles;
+  if (tiles % 8 == 0) tile_of = tile_of % 8 * (tiles / 8) + tile_of / 8;
+  const int slot = int(blockIdx.x) / tiles;
   GroupTile tile;
   int64_t n;  // rows of this workgroup
   if (part_rows > 0) {
-    if (!find_tile(offsets, a.n_groups, a.n_rows, p.deg, part_rows, blockIdx.x, tile) ||
+    if (!find_tile(offsets, a.n_groups, a.n_rows, p.deg, part_rows, slot, tile) ||
         tile.group >= a.n_groups)
       return;
     n = min(part_rows, tile.rows - tile.at);
   } else {
-    const int g = int(blockIdx.x);
+    const int g = slot;
     const int64_t lo = offsets ? offsets[g] : 0, hi = offsets ? offsets[g + 1] : a.n_rows;
     tile = {g, lo, (hi - lo) * p.deg, 0};
     n = tile.rows;
@@ -339,8 +345,8 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
   const int* order = a.index ? a.index + a.order + tile.first : nullptr;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
-  const int col_tiles = (a.cout + kTile - 1) / kTile;
-  const int a0 = int(blockIdx.y) / col_tiles * kTile, b0 = int(blockIdx.y) % col_tiles * kTile;
+  const int row_tiles = (a.cin + kTile - 1) / kTile;
+  const int a0 = tile_of % row_tiles * kTile, b0 = tile_of / row_tiles * kTile;
 
   f32x4 acc[4][4];  // [input channels][output channels]
 #pragma unroll
@@ -348,29 +354,51 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
 
-  // this thread's VEC channels of NP consecutive rows of a chunk
+  // this thread's VEC channels of NP consecutive rows of a chunk.  Channels
+  // and rows past the end are read at the last ones' place and then cleared.
   const int c = tid % CT, k = tid / CT * NP;
   const bool in_x = a0 + c * VEC < a.cin, in_y = b0 + c * VEC < a.cout;
-  u32x4 xv[NP], yv[NP];
-  const auto fetch = [&](int64_t k0) {
+  const T* x0 = static_cast<const T*>(a.x) + int64_t(p.in_off) * a.cin + (in_x ? a0 + c * VEC : 0);
+  const T* y0 = static_cast<const T*>(a.dy) + int64_t(p.out_off) * a.cout + (in_y ? b0 + c * VEC : 0);
+  const int last = int((tile.at + n - 1) / p.deg);  // last of the group's rows
+  const int step_at = BK / p.deg, step_m = BK % p.deg;
+  int at[NP], m[NP], row[NP];  // of the chunk whose rows are asked for next
+  if (n > 0) {
+    const int64_t from = tile.at / p.deg;
+    const unsigned m0 = unsigned(tile.at - from * p.deg);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int64_t r = tile.at + k0 + k + j;  // of the group's rows
-      const bool valid = k0 + k + j < n;
-      const int64_t at = valid ? r / p.deg : 0;
-      const int m = valid ? int(r - at * p.deg) : 0;
-      const int64_t row = valid ? (order ? int64_t(order[at]) : at) : 0;
-      xv[j] = valid && in_x ? *reinterpret_cast<const u32x4*>(
-                                  static_cast<const T*>(a.x) +
-                                  (row * a.din + p.in_off + m) * a.cin + a0 + c * VEC)
-                            : u32x4{};
-      yv[j] = valid && in_y ? *reinterpret_cast<const u32x4*>(
-                                  static_cast<const T*>(a.dy) +
-                                  (row * a.dout + p.out_off + m) * a.cout + b0 + c * VEC)
-                            : u32x4{};
+      const unsigned u = m0 + unsigned(k + j), d = u / unsigned(p.deg);
+      at[j] = int(from) + int(d);
+      m[j] = int(u - d * unsigned(p.deg));
+    }
+  }
+  // a chunk's rows in memory are asked for a chunk ahead of their channels
+  const auto find = [&]() {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int t = min(at[j], last);
+      row[j] = order ? order[t] : t;
     }
   };
-  const auto stage = [&](__bf16 (&s)[PARTS][kTile][LD], const u32x4 (&v)[NP]) {
+  u32x4 xv[NP], yv[NP];
+  const auto fetch = [&]() {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      xv[j] = *reinterpret_cast<const u32x4*>(x0 + (int64_t(row[j]) * a.din + m[j]) * a.cin);
+      yv[j] = *reinterpret_cast<const u32x4*>(y0 + (int64_t(row[j]) * a.dout + m[j]) * a.cout);
+      at[j] += step_at;
+      m[j] += step_m;
+      if (m[j] >= p.deg) {
+        m[j] -= p.deg;
+        ++at[j];
+      }
+    }
+  };
+  const auto stage = [&](__bf16 (&s)[PARTS][kTile][LD], u32x4 (&v)[NP], bool in, int64_t left) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+      if (!in || k + j >= left) v[j] = u32x4{};
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       if constexpr (PARTS == 3) {
@@ -400,13 +428,20 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
     else return (w * 8 + (lane16 & 7)) * 8 + 4 * (lane16 >> 3);
   };
 
-  if (n > 0) fetch(0);
+  if (n > 0) {
+    find();
+    fetch();
+    find();
+  }
   for (int64_t k0 = 0; k0 < n; k0 += BK) {
     __syncthreads();
-    stage(s_x, xv);
-    stage(s_y, yv);
+    stage(s_x, xv, in_x, n - k0);
+    stage(s_y, yv, in_y, n - k0);
     __syncthreads();
-    if (k0 + BK < n) fetch(k0 + BK);
+    if (k0 + BK < n) {
+      fetch();
+      find();
+    }
 #pragma unroll
     for (int kk = 0; kk < BK / 32; ++kk) {
       bf16x8 yf[4][PARTS];
@@ -430,7 +465,7 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
 
   const int64_t size = int64_t(a.cin) * a.cout;
   float* out = part_rows > 0
-                   ? a.part + (int64_t(pi) * slots + blockIdx.x) * size
+                   ? a.part + (int64_t(pi) * slots + slot) * size
                    : a.dW + (int64_t(tile.group) * a.pairs + pi) * size;
   const int col = b0 + channel_of(wn, q);
 #pragma unroll
@@ -494,7 +529,7 @@ hipError_t launch_mix_dw_t(const MixDwArgs& a, const MixPair* p, hipStream_t s) 
                              : a.n_groups;
   const unsigned tiles = unsigned((a.cin + kTile - 1) / kTile) *
                          unsigned((a.cout + kTile - 1) / kTile);
-  hipLaunchKernelGGL((k_mix_dw<T>), dim3(unsigned(slots), tiles, unsigned(a.pairs)),
+  hipLaunchKernelGGL((k_mix_dw<T>), dim3(unsigned(slots) * tiles, unsigned(a.pairs)),
                      dim3(kThreads), 0, s, a, l, rows, slots);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || rows == 0) return e;
