@@ -275,8 +275,233 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
   }
 }
 
+// The mixing where every block has one source and its rows of W are short (K =
+// 32 NK channels at most): a wavefront holds 32 columns of W in registers, in
+// parts, and a workgroup walks over its group's rows, 64 at a time.  Their x
+// passes through LDS once, split there; the next 64 rows are under way in
+// registers meanwhile, and where they lie is known two tiles ahead.  CW of the
+// 4 wavefronts share the tile's rows, 4 / CW its columns... as many as cover
+// the output channels.
+constexpr int kStreamRows = 64;
+
+template <class T, bool WT, int NK, int CW>
+__global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, const MixList l,
+                                                            int chunk) {
+  constexpr int PARTS = Chunk<T>::PARTS, K = 32 * NK, LD = K + 8;
+  constexpr int VEC = 16 / sizeof(T), TPR = K / VEC, PASS = kThreads / TPR;
+  constexpr int NP = kStreamRows / PASS, RT = CW;  // row tiles of a wavefront
+  static_assert(NP >= 1);
+  __shared__ __bf16 s_x[PARTS][kStreamRows][LD];
+  __shared__ int2 s_row[3][kStreamRows];  // row and component
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  int bi = 0;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  const MixBlock blk = l.blk[bi];
+  GroupTile tile;
+  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, chunk,
+                 int64_t(blockIdx.x) - blk.wg0, tile))
+    return;
+  const int* order = a.index ? a.index + a.order + tile.first : nullptr;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int q = lane & 15, h = lane >> 4, wn = wave % CW, wm = wave / CW;
+  const int col0 = int(blockIdx.y) * (32 * CW) + wn * 32;
+  const int n = int(min(int64_t(chunk), tile.rows - tile.at));
+  const int deg = blk.deg;
+
+  // where the rows are: thread r keeps to row r of the tiles
+  int at = 0, m = 0;
+  const int last = int((tile.at + n - 1) / deg), step_at = kStreamRows / deg,
+            step_m = kStreamRows % deg;
+  if (tid < kStreamRows) {
+    const int64_t from = tile.at / deg;
+    const unsigned u = unsigned(tile.at - from * deg) + unsigned(tid), d = u / unsigned(deg);
+    at = int(from) + int(d);
+    m = int(u - d * unsigned(deg));
+  }
+  const auto find = [&](int buf) {
+    if (tid >= kStreamRows) return;
+    const int t = min(at, last);
+    s_row[buf][tid] = {order ? order[t] : t, m};
+    at += step_at;
+    m += step_m;
+    if (m >= deg) {
+      m -= deg;
+      ++at;
+    }
+  };
+  const bool any = tile.group < a.n_groups && blk.n_src > 0;
+  const MixSource sc = any ? l.src[blk.src0] : MixSource{0, 0};
+  const int piece = tid % TPR, r0 = tid / TPR;
+  const bool in = piece * VEC < a.cin;
+  const T* x0 = static_cast<const T*>(a.x) + int64_t(sc.in_off) * a.cin + (in ? piece * VEC : 0);
+  u32x4 xv[NP];
+  const auto fetch = [&](int buf) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int2 r = s_row[buf][r0 + j * PASS];
+      xv[j] = *reinterpret_cast<const u32x4*>(x0 + (int64_t(r.x) * a.din + r.y) * a.cin);
+    }
+  };
+  find(0);
+  find(1);
+  __syncthreads();
+  if (any) fetch(0);
+
+  // this wavefront's columns of W: product i's row q of A
+  bf16x8 wf[2][NK][PARTS];
+  if (any) {
+    const T* W = static_cast<const T*>(a.W) +
+                 (int64_t(tile.group) * a.pairs + sc.pair) * a.cin * a.cout;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = std::is_same_v<T, float> ? i * 16 + q : 8 * (q >> 2) + 4 * i + (q & 3);
+      const int col = min(col0 + c, a.cout - 1);  // (columns past the end are not stored)
+#pragma unroll
+      for (int s = 0; s < NK; ++s) {
+        const int k = s * 32 + h * 8;
+        const bool have = k < a.cin;
+        const int k1 = have ? k : 0;
+        T v[8];
+        if constexpr (WT) {
+          const T* w = W + int64_t(col) * a.cin + k1;
+#pragma unroll
+          for (int e = 0; e < 8; e += VEC)
+            *reinterpret_cast<u32x4*>(v + e) = *reinterpret_cast<const u32x4*>(w + e);
+        } else {
+          const T* w = W + int64_t(k1) * a.cout + col;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = w[int64_t(e) * a.cout];
+        }
+        if constexpr (PARTS == 3) {
+          bf16x4 lo[3], hi[3];
+          split3(have ? f32x4{v[0], v[1], v[2], v[3]} : f32x4{}, lo);
+          split3(have ? f32x4{v[4], v[5], v[6], v[7]} : f32x4{}, hi);
+#pragma unroll
+          for (int t = 0; t < 3; ++t)
+            wf[i][s][t] = __builtin_shufflevector(lo[t], hi[t], 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            wf[i][s][0][e] = have ? __builtin_bit_cast(__bf16, v[e]) : __bf16(0.0f);
+        }
+      }
+    }
+  }
+
+  for (int t0 = 0, buf = 0; t0 < n; t0 += kStreamRows, buf = buf == 2 ? 0 : buf + 1) {
+    f32x4 acc[2][RT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{};
+    if (any) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int r = r0 + j * PASS;
+        const u32x4 v = in ? xv[j] : u32x4{};
+        if constexpr (PARTS == 3) {
+          bf16x4 p[3];
+          split3(__builtin_bit_cast(f32x4, v), p);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s_x[t][r][piece * VEC]) = p[t];
+        } else {
+          *reinterpret_cast<u32x4*>(&s_x[0][r][piece * VEC]) = v;
+        }
+      }
+    }
+    const int next = buf == 2 ? 0 : buf + 1, after = next == 2 ? 0 : next + 1;
+    find(after);
+    __syncthreads();
+    if (any) {
+      if (t0 + kStreamRows < n) fetch(next);
+#pragma unroll
+      for (int s = 0; s < NK; ++s)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          bf16x8 xf[PARTS];
+#pragma unroll
+          for (int t = 0; t < PARTS; ++t)
+            xf[t] = *reinterpret_cast<const bf16x8*>(
+                &s_x[t][(wm * RT + j) * 16 + q][s * 32 + h * 8]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[i][j] = product<PARTS>(wf[i][s], xf, acc[i][j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      const int r = (wm * RT + j) * 16 + q;
+      if (t0 + r >= n) continue;
+      const int2 to = s_row[buf][r];
+      T* y = static_cast<T*>(a.y) + (int64_t(to.x) * a.dout + blk.out_off + to.y) * a.cout;
+      if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (col0 + i * 16 + h * 4 < a.cout)
+            __builtin_nontemporal_store(acc[i][j],
+                                        reinterpret_cast<f32x4*>(y + col0 + i * 16 + h * 4));
+      } else {
+        bf16x8 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = __bf16(acc[0][j][e]);
+          v[4 + e] = __bf16(acc[1][j][e]);
+        }
+        if (col0 + h * 8 < a.cout)
+          __builtin_nontemporal_store(v, reinterpret_cast<bf16x8*>(y + col0 + h * 8));
+      }
+    }
+    __syncthreads();  // s_x and the rows' oldest buffer are written next
+  }
+}
+
+// Rows of a workgroup's walk: a few workgroups for every one that is resident
+// (two on a compute unit).
+int stream_chunk(int64_t rows) {
+  const int64_t n = (rows / 2048 + kStreamRows - 1) / kStreamRows * kStreamRows;
+  return int(std::min<int64_t>(1024, std::max<int64_t>(kStreamRows, n)));
+}
+
+template <class T, bool WT, int NK>
+hipError_t launch_stream(const MixArgs& a, MixList l, hipStream_t s) {
+  int64_t wgs = 0, comps = 0;
+  for (int i = 0; i < l.n_blocks; ++i) comps += l.blk[i].deg;
+  const int chunk = stream_chunk(a.n_rows * comps);
+  for (int i = 0; i < l.n_blocks; ++i) {
+    l.blk[i].wg0 = int(wgs);
+    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, chunk, a.index != nullptr);
+  }
+  const auto go = [&](auto cw) {
+    constexpr int CW = decltype(cw)::value;
+    hipLaunchKernelGGL((k_mix_stream<T, WT, NK, CW>),
+                       dim3(unsigned(wgs), unsigned((a.cout + 32 * CW - 1) / (32 * CW))),
+                       dim3(kThreads), 0, s, a, l, chunk);
+    return hipGetLastError();
+  };
+  if (a.cout > 64) return go(std::integral_constant<int, 4>{});
+  if (a.cout > 32) return go(std::integral_constant<int, 2>{});
+  return go(std::integral_constant<int, 1>{});
+}
+
+template <class T, bool WT>
+hipError_t launch_stream_k(const MixArgs& a, const MixList& l, hipStream_t s) {
+  if (a.cin <= 32) return launch_stream<T, WT, 1>(a, l, s);
+  if (a.cin <= 64) return launch_stream<T, WT, 2>(a, l, s);
+  if constexpr (sizeof(T) == 2)
+    if (a.cin > 128) return launch_stream<T, WT, 8>(a, l, s);
+  return launch_stream<T, WT, 4>(a, l, s);
+}
+
+template <class T>
+bool streams(const MixArgs& a, const MixList& l) {
+  for (int i = 0; i < l.n_blocks; ++i)
+    if (l.blk[i].n_src > 1) return false;
+  return a.cin <= (sizeof(T) == 2 ? 256 : 128);
+}
+
 template <class T>
 hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
+  if (streams<T>(a, l))
+    return a.w_trans ? launch_stream_k<T, true>(a, l, s) : launch_stream_k<T, false>(a, l, s);
   int64_t wgs = 0;
   for (int i = 0; i < l.n_blocks; ++i) {
     l.blk[i].wg0 = int(wgs);
