@@ -66,18 +66,18 @@ __device__ __forceinline__ void split3(const f32x4 v, bf16x4 (&p)[3]) {
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-// The products of split operands, smallest first.
-template <int PARTS>
-__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[PARTS], const bf16x8 (&b)[PARTS],
-                                         f32x4 c) {
-  if constexpr (PARTS == 3) {
-    c = mfma(a[2], b[0], c);
-    c = mfma(a[0], b[2], c);
-    c = mfma(a[1], b[1], c);
-    c = mfma(a[1], b[0], c);
-    c = mfma(a[0], b[1], c);
-  }
-  return mfma(a[0], b[0], c);
+// c[i][j] += a[i] b[j] of split operands, smallest products first; one product
+// of every pair in turn, so that none waits for the one before.
+template <int PARTS, int M, int N>
+__device__ __forceinline__ void products(const bf16x8 (&a)[M][PARTS], const bf16x8 (&b)[N][PARTS],
+                                         f32x4 (&c)[M][N]) {
+  constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+  for (int t = PARTS == 3 ? 0 : 5; t < 6; ++t)
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) c[i][j] = mfma(a[i][kA[t]], b[j][kB[t]], c[i][j]);
 }
 
 // ------------------------------------------------------------ the mixing
@@ -235,13 +235,12 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
               &s_x[t][wm * 64 + j * 16 + q][kk * 32 + h * 8]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        bf16x8 wf[PARTS];
+        bf16x8 wf[1][PARTS];
 #pragma unroll
         for (int t = 0; t < PARTS; ++t)
-          wf[t] = *reinterpret_cast<const bf16x8*>(
+          wf[0][t] = *reinterpret_cast<const bf16x8*>(
               &s_w[t][wn * 64 + i * 16 + q][kk * 32 + h * 8]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = product<PARTS>(wf, xf[j], acc[i][j]);
+        products<PARTS, 1, 4>(wf, xf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
       }
     }
   }
@@ -279,12 +278,16 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
 // 32 NK channels at most): a wavefront holds 32 columns of W in registers, in
 // parts, and a workgroup walks over its group's rows, 64 at a time.  Their x
 // passes through LDS once, split there; the next 64 rows are under way in
-// registers meanwhile, and where they lie is known two tiles ahead.  CW of the
-// 4 wavefronts share the tile's rows, 4 / CW its columns... as many as cover
-// the output channels.
+// registers meanwhile, and where they lie is known two tiles ahead.  CW
+// wavefronts share out the output channels, 4 / CW the tile's rows.
+//
+// Nothing in the walk is conditional: a wait for loads counts what was issued
+// after them, and with stores that may or may not have been issued it waits
+// for these as well.  Rows past the end of the walk are rows of the group all
+// the same, the last atom's; their results are written twice.
 constexpr int kStreamRows = 64;
 
-template <class T, bool WT, int NK, int CW>
+template <class T, bool WT, int NK, int CW, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, const MixList l,
                                                             int chunk) {
   constexpr int PARTS = Chunk<T>::PARTS, K = 32 * NK, LD = K + 8;
@@ -308,20 +311,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
   const int n = int(min(int64_t(chunk), tile.rows - tile.at));
   const int deg = blk.deg;
 
-  // where the rows are: thread r keeps to row r of the tiles
-  int at = 0, m = 0;
+  // where the rows are: thread r of the first wavefront keeps to row r of the
+  // tiles, and has the next one's place in `place`
   const int last = int((tile.at + n - 1) / deg), step_at = kStreamRows / deg,
             step_m = kStreamRows % deg;
-  if (tid < kStreamRows) {
-    const int64_t from = tile.at / deg;
-    const unsigned u = unsigned(tile.at - from * deg) + unsigned(tid), d = u / unsigned(deg);
-    at = int(from) + int(d);
-    m = int(u - d * unsigned(deg));
-  }
-  const auto find = [&](int buf) {
-    if (tid >= kStreamRows) return;
-    const int t = min(at, last);
-    s_row[buf][tid] = {order ? order[t] : t, m};
+  const int64_t from = tile.at / deg;
+  const unsigned u = unsigned(tile.at - from * deg) + unsigned(lane);
+  int at = int(from) + int(u / unsigned(deg)), m = int(u % unsigned(deg));
+  const int* source = order ? order : static_cast<const int*>(a.x);  // (read in any case)
+  const auto look = [&]() {
+    const int t = min(at, last), row = source[order ? t : 0];
+    return order ? row : t;
+  };
+  const auto put = [&](int buf, int place) {
+    if (wave == 0) s_row[buf][lane] = {place, m};
     at += step_at;
     m += step_m;
     if (m >= deg) {
@@ -329,8 +332,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
       ++at;
     }
   };
-  const bool any = tile.group < a.n_groups && blk.n_src > 0;
-  const MixSource sc = any ? l.src[blk.src0] : MixSource{0, 0};
+  int place = look();
+  if (tile.group >= a.n_groups || blk.n_src == 0) {  // zeros
+    for (int t0 = 0; t0 < n; t0 += kStreamRows) {
+      put(0, place);
+      place = look();
+      __syncthreads();
+      for (int e = tid; e < min(kStreamRows, n - t0) * 32 * CW; e += kThreads) {
+        const int2 to = s_row[0][e / (32 * CW)];
+        const int c = int(blockIdx.y) * (32 * CW) + e % (32 * CW);
+        if (c < a.cout)
+          static_cast<T*>(a.y)[(int64_t(to.x) * a.dout + blk.out_off + to.y) * a.cout + c] = T{};
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  put(0, place);
+  place = look();
+  put(1, place);
+  place = look();
+  __syncthreads();
+
+  const MixSource sc = l.src[blk.src0];
   const int piece = tid % TPR, r0 = tid / TPR;
   const bool in = piece * VEC < a.cin;
   const T* x0 = static_cast<const T*>(a.x) + int64_t(sc.in_off) * a.cin + (in ? piece * VEC : 0);
@@ -342,112 +366,106 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
       xv[j] = *reinterpret_cast<const u32x4*>(x0 + (int64_t(r.x) * a.din + r.y) * a.cin);
     }
   };
-  find(0);
-  find(1);
-  __syncthreads();
-  if (any) fetch(0);
+  fetch(0);
 
   // this wavefront's columns of W: product i's row q of A
-  bf16x8 wf[2][NK][PARTS];
-  if (any) {
-    const T* W = static_cast<const T*>(a.W) +
-                 (int64_t(tile.group) * a.pairs + sc.pair) * a.cin * a.cout;
+  bf16x8 wf[NK][2][PARTS];
+  const T* W = static_cast<const T*>(a.W) +
+               (int64_t(tile.group) * a.pairs + sc.pair) * a.cin * a.cout;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = std::is_same_v<T, float> ? i * 16 + q : 8 * (q >> 2) + 4 * i + (q & 3);
-      const int col = min(col0 + c, a.cout - 1);  // (columns past the end are not stored)
+  for (int i = 0; i < 2; ++i) {
+    const int c = std::is_same_v<T, float> ? i * 16 + q : 8 * (q >> 2) + 4 * i + (q & 3);
+    const int col = min(col0 + c, a.cout - 1);  // (columns past the end are not stored)
 #pragma unroll
-      for (int s = 0; s < NK; ++s) {
-        const int k = s * 32 + h * 8;
-        const bool have = k < a.cin;
-        const int k1 = have ? k : 0;
-        T v[8];
-        if constexpr (WT) {
-          const T* w = W + int64_t(col) * a.cin + k1;
+    for (int s = 0; s < NK; ++s) {
+      const int k = s * 32 + h * 8;
+      const bool have = k < a.cin;
+      const int k1 = have ? k : 0;
+      T v[8];
+      if constexpr (WT) {
+        const T* w = W + int64_t(col) * a.cin + k1;
 #pragma unroll
-          for (int e = 0; e < 8; e += VEC)
-            *reinterpret_cast<u32x4*>(v + e) = *reinterpret_cast<const u32x4*>(w + e);
-        } else {
-          const T* w = W + int64_t(k1) * a.cout + col;
+        for (int e = 0; e < 8; e += VEC)
+          *reinterpret_cast<u32x4*>(v + e) = *reinterpret_cast<const u32x4*>(w + e);
+      } else {
+        const T* w = W + int64_t(k1) * a.cout + col;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = w[int64_t(e) * a.cout];
-        }
-        if constexpr (PARTS == 3) {
-          bf16x4 lo[3], hi[3];
-          split3(have ? f32x4{v[0], v[1], v[2], v[3]} : f32x4{}, lo);
-          split3(have ? f32x4{v[4], v[5], v[6], v[7]} : f32x4{}, hi);
+        for (int e = 0; e < 8; ++e) v[e] = w[int64_t(e) * a.cout];
+      }
+      if constexpr (PARTS == 3) {
+        bf16x4 lo[3], hi[3];
+        split3(have ? f32x4{v[0], v[1], v[2], v[3]} : f32x4{}, lo);
+        split3(have ? f32x4{v[4], v[5], v[6], v[7]} : f32x4{}, hi);
 #pragma unroll
-          for (int t = 0; t < 3; ++t)
-            wf[i][s][t] = __builtin_shufflevector(lo[t], hi[t], 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
+        for (int t = 0; t < 3; ++t)
+          wf[s][i][t] = __builtin_shufflevector(lo[t], hi[t], 0, 1, 2, 3, 4, 5, 6, 7);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            wf[i][s][0][e] = have ? __builtin_bit_cast(__bf16, v[e]) : __bf16(0.0f);
-        }
+        for (int e = 0; e < 8; ++e)
+          wf[s][i][0][e] = have ? __builtin_bit_cast(__bf16, v[e]) : __bf16(0.0f);
       }
     }
   }
 
+  // everything asked for so far is here: at the walk's top only a turn's own
+  // loads and stores are left to count
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   for (int t0 = 0, buf = 0; t0 < n; t0 += kStreamRows, buf = buf == 2 ? 0 : buf + 1) {
-    f32x4 acc[2][RT];
+    constexpr int JB = RT < 2 ? RT : 2;  // row tiles whose products alternate
+    f32x4 acc[RT / JB][2][JB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = f32x4{};
-    if (any) {
+      for (int i = 0; i < 2; ++i) acc[j / JB][i][j % JB] = f32x4{};
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const int r = r0 + j * PASS;
-        const u32x4 v = in ? xv[j] : u32x4{};
-        if constexpr (PARTS == 3) {
-          bf16x4 p[3];
-          split3(__builtin_bit_cast(f32x4, v), p);
+    for (int j = 0; j < NP; ++j) {
+      const int r = r0 + j * PASS;
+      const u32x4 v = in ? xv[j] : u32x4{};
+      if constexpr (PARTS == 3) {
+        bf16x4 p[3];
+        split3(__builtin_bit_cast(f32x4, v), p);
 #pragma unroll
-          for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s_x[t][r][piece * VEC]) = p[t];
-        } else {
-          *reinterpret_cast<u32x4*>(&s_x[0][r][piece * VEC]) = v;
-        }
+        for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s_x[t][r][piece * VEC]) = p[t];
+      } else {
+        *reinterpret_cast<u32x4*>(&s_x[0][r][piece * VEC]) = v;
       }
     }
     const int next = buf == 2 ? 0 : buf + 1, after = next == 2 ? 0 : next + 1;
-    find(after);
+    put(after, place);
     __syncthreads();
-    if (any) {
-      if (t0 + kStreamRows < n) fetch(next);
+    place = look();
+    fetch(next);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
 #pragma unroll
-      for (int s = 0; s < NK; ++s)
+    for (int s = 0; s < NK; ++s)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          bf16x8 xf[PARTS];
+      for (int j = 0; j < RT / JB; ++j) {
+        bf16x8 xf[JB][PARTS];
+#pragma unroll
+        for (int b = 0; b < JB; ++b)
 #pragma unroll
           for (int t = 0; t < PARTS; ++t)
-            xf[t] = *reinterpret_cast<const bf16x8*>(
-                &s_x[t][(wm * RT + j) * 16 + q][s * 32 + h * 8]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) acc[i][j] = product<PARTS>(wf[i][s], xf, acc[i][j]);
-        }
-    }
+            xf[b][t] = *reinterpret_cast<const bf16x8*>(
+                &s_x[t][(wm * RT + j * JB + b) * 16 + q][s * 32 + h * 8]);
+        products<PARTS, 2, JB>(wf[s], xf, acc[j]);
+      }
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const int r = (wm * RT + j) * 16 + q;
-      if (t0 + r >= n) continue;
-      const int2 to = s_row[buf][r];
+      const int2 to = s_row[buf][(wm * RT + j) * 16 + q];
       T* y = static_cast<T*>(a.y) + (int64_t(to.x) * a.dout + blk.out_off + to.y) * a.cout;
       if constexpr (PARTS == 3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (col0 + i * 16 + h * 4 < a.cout)
-            __builtin_nontemporal_store(acc[i][j],
-                                        reinterpret_cast<f32x4*>(y + col0 + i * 16 + h * 4));
+          if (FULL || col0 + i * 16 + h * 4 < a.cout)
+            *reinterpret_cast<f32x4*>(y + col0 + i * 16 + h * 4) = acc[j / JB][i][j % JB];
       } else {
         bf16x8 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[e] = __bf16(acc[0][j][e]);
-          v[4 + e] = __bf16(acc[1][j][e]);
+          v[e] = __bf16(acc[j / JB][0][j % JB][e]);
+          v[4 + e] = __bf16(acc[j / JB][1][j % JB][e]);
         }
-        if (col0 + h * 8 < a.cout)
-          __builtin_nontemporal_store(v, reinterpret_cast<bf16x8*>(y + col0 + h * 8));
+        if (FULL || col0 + h * 8 < a.cout) *reinterpret_cast<bf16x8*>(y + col0 + h * 8) = v;
       }
     }
     __syncthreads();  // s_x and the rows' oldest buffer are written next
@@ -457,8 +475,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
 // Rows of a workgroup's walk: a few workgroups for every one that is resident
 // (two on a compute unit).
 int stream_chunk(int64_t rows) {
-  const int64_t n = (rows / 2048 + kStreamRows - 1) / kStreamRows * kStreamRows;
-  return int(std::min<int64_t>(1024, std::max<int64_t>(kStreamRows, n)));
+#ifndef V_WG
+#define V_WG 2048
+#define V_MAX 1024
+#endif
+  const int64_t n = (rows / V_WG + kStreamRows - 1) / kStreamRows * kStreamRows;
+  return int(std::min<int64_t>(V_MAX, std::max<int64_t>(kStreamRows, n)));
 }
 
 template <class T, bool WT, int NK>
@@ -472,9 +494,13 @@ hipError_t launch_stream(const MixArgs& a, MixList l, hipStream_t s) {
   }
   const auto go = [&](auto cw) {
     constexpr int CW = decltype(cw)::value;
-    hipLaunchKernelGGL((k_mix_stream<T, WT, NK, CW>),
-                       dim3(unsigned(wgs), unsigned((a.cout + 32 * CW - 1) / (32 * CW))),
-                       dim3(kThreads), 0, s, a, l, chunk);
+    const dim3 grid(unsigned(wgs), unsigned((a.cout + 32 * CW - 1) / (32 * CW)));
+    if (a.cout % (32 * CW) == 0)
+      hipLaunchKernelGGL((k_mix_stream<T, WT, NK, CW, true>), grid, dim3(kThreads), 0, s, a, l,
+                         chunk);
+    else
+      hipLaunchKernelGGL((k_mix_stream<T, WT, NK, CW, false>), grid, dim3(kThreads), 0, s, a, l,
+                         chunk);
     return hipGetLastError();
   };
   if (a.cout > 64) return go(std::integral_constant<int, 4>{});
@@ -663,10 +689,8 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
     stage(s_x, xv, in_x, n - k0);
     stage(s_y, yv, in_y, n - k0);
     __syncthreads();
-    if (k0 + BK < n) {
-      fetch();
-      find();
-    }
+    fetch();  // (past the end: the last rows again)
+    find();
 #pragma unroll
     for (int kk = 0; kk < BK / 32; ++kk) {
       bf16x8 yf[4][PARTS];
@@ -678,12 +702,11 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
               &s_y[t][slot_of(wn, j, q)][kk * 32 + h * 8]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        bf16x8 xf[PARTS];
+        bf16x8 xf[1][PARTS];
 #pragma unroll
         for (int t = 0; t < PARTS; ++t)
-          xf[t] = *reinterpret_cast<const bf16x8*>(&s_x[t][slot_of(wm, i, q)][kk * 32 + h * 8]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = product<PARTS>(xf, yf[j], acc[i][j]);
+          xf[0][t] = *reinterpret_cast<const bf16x8*>(&s_x[t][slot_of(wm, i, q)][kk * 32 + h * 8]);
+        products<PARTS, 1, 4>(xf, yf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
       }
     }
   }
