@@ -368,43 +368,51 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
   };
   fetch(0);
 
-  // this wavefront's columns of W: product i's row q of A
+  // this wavefront's columns of W: product i's row q of A.  All of them are
+  // asked for before the first is split (piece by piece the loads' delays add up).
   bf16x8 wf[NK][2][PARTS];
-  const T* W = static_cast<const T*>(a.W) +
-               (int64_t(tile.group) * a.pairs + sc.pair) * a.cin * a.cout;
+  {
+    const T* W = static_cast<const T*>(a.W) +
+                 (int64_t(tile.group) * a.pairs + sc.pair) * a.cin * a.cout;
+    T v[NK][2][8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int c = std::is_same_v<T, float> ? i * 16 + q : 8 * (q >> 2) + 4 * i + (q & 3);
-    const int col = min(col0 + c, a.cout - 1);  // (columns past the end are not stored)
+    for (int s = 0; s < NK; ++s)
 #pragma unroll
-    for (int s = 0; s < NK; ++s) {
-      const int k = s * 32 + h * 8;
-      const bool have = k < a.cin;
-      const int k1 = have ? k : 0;
-      T v[8];
-      if constexpr (WT) {
-        const T* w = W + int64_t(col) * a.cin + k1;
+      for (int i = 0; i < 2; ++i) {
+        const int c = std::is_same_v<T, float> ? i * 16 + q : 8 * (q >> 2) + 4 * i + (q & 3);
+        const int col = min(col0 + c, a.cout - 1);  // (columns past the end are not stored)
+        const int k = s * 32 + h * 8 < a.cin ? s * 32 + h * 8 : 0;
+        if constexpr (WT) {
+          const T* w = W + int64_t(col) * a.cin + k;
 #pragma unroll
-        for (int e = 0; e < 8; e += VEC)
-          *reinterpret_cast<u32x4*>(v + e) = *reinterpret_cast<const u32x4*>(w + e);
-      } else {
-        const T* w = W + int64_t(k1) * a.cout + col;
+          for (int e = 0; e < 8; e += VEC)
+            *reinterpret_cast<u32x4*>(&v[s][i][e]) = *reinterpret_cast<const u32x4*>(w + e);
+        } else {
+          const T* w = W + int64_t(k) * a.cout + col;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = w[int64_t(e) * a.cout];
+          for (int e = 0; e < 8; ++e) v[s][i][e] = w[int64_t(e) * a.cout];
+        }
       }
-      if constexpr (PARTS == 3) {
-        bf16x4 lo[3], hi[3];
-        split3(have ? f32x4{v[0], v[1], v[2], v[3]} : f32x4{}, lo);
-        split3(have ? f32x4{v[4], v[5], v[6], v[7]} : f32x4{}, hi);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < 3; ++t)
-          wf[s][i][t] = __builtin_shufflevector(lo[t], hi[t], 0, 1, 2, 3, 4, 5, 6, 7);
-      } else {
+    for (int s = 0; s < NK; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          wf[s][i][0][e] = have ? __builtin_bit_cast(__bf16, v[e]) : __bf16(0.0f);
+      for (int i = 0; i < 2; ++i) {
+        const bool have = s * 32 + h * 8 < a.cin;
+        if constexpr (PARTS == 3) {
+          const T* w = v[s][i];
+          bf16x4 lo[3], hi[3];
+          split3(have ? f32x4{w[0], w[1], w[2], w[3]} : f32x4{}, lo);
+          split3(have ? f32x4{w[4], w[5], w[6], w[7]} : f32x4{}, hi);
+#pragma unroll
+          for (int t = 0; t < 3; ++t)
+            wf[s][i][t] = __builtin_shufflevector(lo[t], hi[t], 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            wf[s][i][0][e] = have ? __builtin_bit_cast(__bf16, v[s][i][e]) : __bf16(0.0f);
+        }
       }
-    }
   }
 
   // everything asked for so far is here: at the walk's top only a turn's own
