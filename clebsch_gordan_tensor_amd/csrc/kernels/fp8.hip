@@ -27,6 +27,7 @@
 #include "fp8.h"
 #include "group_tiles.h"
 #include "registry.h"
+#include "tile128.h"
 
 namespace e3k {
 namespace {
@@ -155,20 +156,20 @@ __device__ __forceinline__ f32x4 product(const Values& a, const Values& b) {
   return c;
 }
 
-// Slot of column n of a tile: as the results are stored 16 bytes at once, for
+// Column of a tile in slot s: as the results are stored 16 bytes at once, for
 // bf16 two products' columns alternate by fours.
 template <class T>
-__device__ __forceinline__ int column_slot(int n) {
-  if constexpr (std::is_same_v<T, float>) return n;
-  else return (n & ~31) | ((n >> 2) & 1) << 4 | ((n >> 3) & 3) << 2 | (n & 3);
+__device__ __forceinline__ int column_in(int s) {
+  if constexpr (std::is_same_v<T, float>) return s;
+  else return (s & ~31) | ((s >> 2) & 3) << 3 | ((s >> 4) & 1) << 2 | (s & 3);
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const MixList l,
                                                       const Fp8Layout at) {
-  constexpr int LD = 128 + 16;
-  __shared__ __attribute__((aligned(16))) uint8_t s_x[kTile][LD];
-  __shared__ __attribute__((aligned(16))) uint8_t s_w[kTile][LD];
+  // two chunks of 128 k, one read while the other is on its way
+  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kTileBytes], s_w0[kTileBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x1[kTileBytes], s_w1[kTileBytes];
   if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
   const int* header = static_cast<const int*>(a.packed);
   if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
@@ -178,100 +179,95 @@ __global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const 
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
-  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
-                 int64_t(blockIdx.x) - blk.wg0, tile))
+  int col_tile;
+  if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
+                     blockIdx.x - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
+                     col_tile))
     return;
-  const int* order = a.index ? a.index + a.order + tile.first : nullptr;
+  const RowOrder order(a.index, a.order, tile, a.q);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
-  const int col0 = int(blockIdx.y) * kTile;
+  const int col0 = col_tile * kTile;
   const int n_rows = int(min(int64_t(kTile), tile.rows - tile.at));
-  const int64_t from = tile.at / blk.deg;
-  const unsigned m0 = unsigned(tile.at - from * blk.deg);
-  const auto row_of = [&](int r, int& m) {
-    const unsigned c = m0 + unsigned(r), d = c / unsigned(blk.deg);
-    m = int(c - d * unsigned(blk.deg));
-    const int64_t p = from + d;
-    return order ? int64_t(order[p]) : p;
-  };
+  const TileRows rows(tile.at, blk.deg);
   f32x4 acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
 
-  const int piece = tid % 8, r0 = tid / 8;  // 16 bytes of 4 rows
+  const TileLane tl;
   const int runs = at.in_blocks;
-  const uint8_t* xrow[4];
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
+  const int64_t kpad = int64_t(runs) * 128;
+  const uint8_t* packed = static_cast<const uint8_t*>(a.packed);
+  const int n_src = tile.group < a.n_groups ? blk.n_src : 0;
+  // rows past the end are the last one again, and so are columns
+  const uint8_t *xrow[4], *wrow[4];
+  // the rows this lane loads, and those it ends with
+  int load_row[4], load_m[4], row[4], comp[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int r = r0 + j * 32;
-    int m;
-    const int64_t row = row_of(min(r, n_rows - 1), m);
-    xrow[j] = r < n_rows ? static_cast<const uint8_t*>(a.q) + (row * a.din + m) * a.cin + piece * 16
-                         : nullptr;
+    load_row[j] = order(rows.place(min(tl.first + j * 32, n_rows - 1), load_m[j]));
+    row[j] = order(rows.place(min(wm * 64 + j * 16 + q, n_rows - 1), comp[j]));
   }
-  // the rows this lane ends with, and where their scales are
-  int64_t row[4];
-  int comp[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    xrow[j] = static_cast<const uint8_t*>(a.q) +
+              (int64_t(load_row[j]) * a.din + load_m[j]) * a.cin + tl.piece * 16;
+    const int n = min(col0 + column_in<T>(tl.first + j * 32), a.cout - 1);
+    wrow[j] = packed + at.codes + (int64_t(tile.group) * a.pairs * a.cout + n) * kpad +
+              tl.piece * 16;
+  }
   const float* srow[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    row[j] = row_of(min(wm * 64 + j * 16 + q, n_rows - 1), comp[j]);
-    srow[j] = a.scale + (row[j] * a.din + comp[j]) * runs;
-  }
-  const int n_src = tile.group < a.n_groups ? blk.n_src : 0;
-  const uint8_t* packed = static_cast<const uint8_t*>(a.packed);
-  const int64_t kpad = int64_t(runs) * 128;
+  for (int j = 0; j < 4; ++j)
+    srow[j] = a.scale + (int64_t(row[j]) * a.din + comp[j]) * runs;
 
-  u32x4 xv[4], wv[4];
-  float sx[4], sw;
-  const auto fetch = [&](int step) {
-    const int src = step / runs, b = step - src * runs;
-    const MixSource sc = l.src[blk.src0 + src];
-    const int64_t mat = int64_t(tile.group) * a.pairs + sc.pair;
-    const bool in = b * 128 + piece * 16 < a.cin;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      xv[j] = xrow[j] && in
-                  ? *reinterpret_cast<const u32x4*>(xrow[j] + int64_t(sc.in_off) * a.cin + b * 128)
-                  : u32x4{};
-      const int n = col0 + r0 + j * 32;
-      wv[j] = n < a.cout ? *reinterpret_cast<const u32x4*>(packed + at.codes +
-                                                           (mat * a.cout + n) * kpad + b * 128 +
-                                                           piece * 16)
-                         : u32x4{};
-      sx[j] = srow[j][sc.in_off * runs + b];
-    }
-    sw = reinterpret_cast<const float*>(packed + at.scales)[(mat * at.out_blocks + blockIdx.y) *
-                                                                runs + b];
-  };
   const int steps = n_src * runs;
-  if (steps > 0) fetch(0);
-  for (int step = 0; step < steps; ++step) {
-    __syncthreads();
+  int src = 0, b = 0;  // of the chunk asked for next
+  float sx[4], sw;
+  const auto fetch = [&](uint8_t* x, uint8_t* w) {
+    const MixSource sc = l.src[blk.src0 + src];
+    const bool in = b * 128 + tl.piece * 16 < a.cin;
+    const uint8_t *xp[4], *wp[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<u32x4*>(&s_x[r0 + j * 32][piece * 16]) = xv[j];
-      *reinterpret_cast<u32x4*>(&s_w[column_slot<T>(r0 + j * 32)][piece * 16]) = wv[j];
+      xp[j] = in ? xrow[j] + int64_t(sc.in_off) * a.cin + b * 128 : zeros;
+      wp[j] = wrow[j] + int64_t(sc.pair) * a.cout * kpad + b * 128;
     }
+    tile_load(xp, x);
+    tile_load(wp, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sx[j] = srow[j][sc.in_off * runs + b];
+    const int64_t mat = int64_t(tile.group) * a.pairs + sc.pair;
+    sw = reinterpret_cast<const float*>(packed + at.scales)[(mat * at.out_blocks + col_tile) *
+                                                                runs + b];
+    if (++b == runs) {
+      b = 0;
+      ++src;
+    }
+  };
+  const auto turn = [&](const uint8_t* x, const uint8_t* w, uint8_t* x_next, uint8_t* w_next,
+                        bool more) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this chunk is here
     float f[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = sx[j] * sw;
     __syncthreads();
-    if (step + 1 < steps) fetch(step + 1);
-    const auto operand = [&](const uint8_t (&s)[kTile][LD], int r) {
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(&s[r][h * 16]);
-      const u32x4 hi = *reinterpret_cast<const u32x4*>(&s[r][64 + h * 16]);
+    if (more) fetch(x_next, w_next);
+    const auto operand = [&](const uint8_t* s, int r) {
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(tile_at(s, r, h));
+      const u32x4 hi = *reinterpret_cast<const u32x4*>(tile_at(s, r, 4 + h));
       return Operand<T>::of(i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
                                   int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])});
     };
     typename Operand<T>::type xf[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) xf[j] = operand(s_x, wm * 64 + j * 16 + q);
+    for (int j = 0; j < 4; ++j) xf[j] = operand(x, wm * 64 + j * 16 + q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const auto wf = operand(s_w, wn * 64 + i * 16 + q);
+      const auto wf = operand(w, wn * 64 + i * 16 + q);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const f32x4 t = product(wf, xf[j]);
@@ -279,11 +275,16 @@ __global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const 
         for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[r], f[j], acc[i][j][r]);
       }
     }
+  };
+  if (steps > 0) fetch(s_x0, s_w0);
+  for (int step = 0; step < steps; step += 2) {
+    turn(s_x0, s_w0, s_x1, s_w1, step + 1 < steps);
+    if (step + 1 < steps) turn(s_x1, s_w1, s_x0, s_w0, step + 2 < steps);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (wm * 64 + j * 16 + q >= n_rows) continue;
-    T* y = static_cast<T*>(a.y) + (row[j] * a.dout + blk.out_off + comp[j]) * a.cout;
+    T* y = static_cast<T*>(a.y) + (int64_t(row[j]) * a.dout + blk.out_off + comp[j]) * a.cout;
     if constexpr (std::is_same_v<T, float>) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -349,11 +350,12 @@ hipError_t launch_fp8_mix(const Fp8MixArgs& a, const MixList& list, int bf16, hi
   int64_t wgs = 0;
   for (int i = 0; i < l.n_blocks; ++i) {
     l.blk[i].wg0 = int(wgs);
-    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTile, a.index != nullptr);
+    wgs += xcd_workgroups(most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTile,
+                                     a.index != nullptr), (a.cout + kTile - 1) / kTile);
   }
   if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
   const Fp8Layout at = fp8_layout(a.n_groups, a.pairs, a.cin, a.cout);
-  const dim3 grid(unsigned(wgs), unsigned((a.cout + kTile - 1) / kTile));
+  const dim3 grid{unsigned(wgs)};
   if (bf16) hipLaunchKernelGGL((k_fp8_mix<bf16_t>), grid, dim3(kThreads), 0, s, a, l, at);
   else hipLaunchKernelGGL((k_fp8_mix<float>), grid, dim3(kThreads), 0, s, a, l, at);
   return hipGetLastError();

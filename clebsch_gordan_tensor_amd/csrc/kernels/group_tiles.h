@@ -59,6 +59,73 @@ __device__ __forceinline__ bool find_tile(const int* offsets, int n_groups, int6
   return false;
 }
 
+// Tiles of all groups together.
+__device__ __forceinline__ int count_tiles(const int* offsets, int n_groups, int64_t n_rows,
+                                           int deg, int64_t size) {
+  if (!offsets) return int((n_rows * deg + size - 1) / size);
+  int total = 0;
+  for (int g0 = 0; g0 <= n_groups; g0 += 64) {
+    const int g = g0 + int(threadIdx.x & 63);
+    int n = 0;
+    if (g <= n_groups) {
+      const int64_t lo = offsets[g], hi = g < n_groups ? offsets[g + 1] : n_rows;
+      n = int(((hi - lo) * deg + size - 1) / size);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
+    total += n;
+  }
+  return __builtin_amdgcn_readfirstlane(total);
+}
+
+// The tile of workgroup `id` where `cols` column tiles share a tile's rows:
+// neighbouring workgroups run on different XCDs, and each XCD takes a stretch
+// of consecutive tiles, column by column, so that a tile's rows are read once
+// into its L2 and a group's weights by few of them.  The launch has
+// xcd_workgroups(most_tiles) workgroups.
+constexpr int kXcds = 8;
+__device__ __forceinline__ bool find_tile_xcd(const int* offsets, int n_groups, int64_t n_rows,
+                                              int deg, int64_t size, unsigned id, unsigned cols,
+                                              GroupTile& tile, int& col) {
+  const unsigned total = unsigned(count_tiles(offsets, n_groups, n_rows, deg, size));
+  const unsigned per = (total + kXcds - 1) / kXcds, slot = id / kXcds, t = slot / cols;
+  col = int(slot - t * cols);
+  const unsigned at = id % kXcds * per + t;
+  return t < per && at < total && find_tile(offsets, n_groups, n_rows, deg, size, at, tile);
+}
+inline int64_t xcd_workgroups(int64_t tiles, int64_t cols) {
+  return (tiles + kXcds - 1) / kXcds * kXcds * cols;
+}
+
+// Rows of a group by their place in it.  Without an index the rows are their
+// places; something is read all the same (`any`: memory of four bytes at
+// least), so that several rows can be asked for at once.
+struct RowOrder {
+  const int* at;
+  bool listed;
+  __device__ __forceinline__ RowOrder(const int* index, int order, const GroupTile& tile,
+                                      const void* any)
+      : at(index ? index + order + tile.first : static_cast<const int*>(any)), listed(index) {}
+  __device__ __forceinline__ int operator()(int place) const {
+    const int row = at[listed ? place : 0];
+    return listed ? row : place;
+  }
+};
+
+// Rows of a product's tile: row r is component m of the group's row `place`.
+struct TileRows {
+  int from;     // place of the tile's first row
+  unsigned m0;  // its component
+  unsigned deg;
+  __device__ __forceinline__ TileRows(int64_t first, int deg_)
+      : from(int(first / deg_)), m0(unsigned(first - int64_t(from) * deg_)), deg(unsigned(deg_)) {}
+  __device__ __forceinline__ int place(int r, int& m) const {
+    const unsigned c = m0 + unsigned(r), d = c / deg;
+    m = int(c - d * deg);
+    return from + int(d);
+  }
+};
+
 // Most tiles that n_rows rows in n_groups groups (and some without) can fill.
 inline int64_t most_tiles(int64_t n_rows, int n_groups, int deg, int64_t size, bool grouped) {
   return (n_rows * deg + size - 1) / size + (grouped ? n_groups : 0);

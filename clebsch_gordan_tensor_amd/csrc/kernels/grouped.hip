@@ -106,23 +106,17 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
-  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
-                 int64_t(blockIdx.x) - blk.wg0, tile))
+  int col_tile;
+  if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
+                     blockIdx.x - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
+                     col_tile))
     return;
-  const int* order = a.index ? a.index + a.order + tile.first : nullptr;
+  const RowOrder order(a.index, a.order, tile, a.x);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
-  const int col0 = int(blockIdx.y) * kTile;
+  const int col0 = col_tile * kTile;
   const int n_rows = int(min(int64_t(kTile), tile.rows - tile.at));
-  // row r of the tile: component m0 + r of the rows from `from` on
-  const int64_t from = tile.at / blk.deg;
-  const unsigned m0 = unsigned(tile.at - from * blk.deg);
-  const auto row_of = [&](int r, int& m) {
-    const unsigned c = m0 + unsigned(r), d = c / unsigned(blk.deg);
-    m = int(c - d * unsigned(blk.deg));
-    const int64_t p = from + d;
-    return order ? int64_t(order[p]) : p;
-  };
+  const TileRows rows(tile.at, blk.deg);
 
   f32x4 acc[4][4];  // [columns][rows] of 16
 #pragma unroll
@@ -130,17 +124,20 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
 
-  // the rows this thread stages, and its 16 bytes of them
+  // the rows this thread stages, and its 16 bytes of them; the rows this lane
+  // ends with
   const int piece = tid % TPR, r0 = tid / TPR;
   const T* xrow[NP];
+  int load_row[NP], load_m[NP], row[4], comp[4];
 #pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    const int r = r0 + j * PASS;
-    int m;
-    const int64_t row = row_of(min(r, n_rows - 1), m);
-    xrow[j] = r < n_rows ? static_cast<const T*>(a.x) + (row * a.din + m) * a.cin + piece * VEC
-                         : nullptr;
+  for (int j = 0; j < 4; ++j) {
+    load_row[j] = order(rows.place(min(r0 + j * PASS, n_rows - 1), load_m[j]));
+    row[j] = order(rows.place(min(wm * 64 + j * 16 + q, n_rows - 1), comp[j]));
   }
+#pragma unroll
+  for (int j = 0; j < NP; ++j)
+    xrow[j] = static_cast<const T*>(a.x) + (int64_t(load_row[j]) * a.din + load_m[j]) * a.cin +
+              piece * VEC;
   const int n_src = tile.group < a.n_groups ? blk.n_src : 0;
   const int chunks = (a.cin + BK - 1) / BK;
   const T* W0 = static_cast<const T*>(a.W) + int64_t(tile.group) * a.pairs * a.cin * a.cout;
@@ -153,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
     const bool in = k0 + piece * VEC < a.cin;
 #pragma unroll
     for (int j = 0; j < NP; ++j)
-      xv[j] = xrow[j] && in
+      xv[j] = in
                   ? *reinterpret_cast<const u32x4*>(xrow[j] + int64_t(sc.in_off) * a.cin + k0)
                   : u32x4{};
     if constexpr (WT) {  // rows of W are columns here, k along them
@@ -247,11 +244,8 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
 
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int r = wm * 64 + j * 16 + q;
-    if (r >= n_rows) continue;
-    int m;
-    const int64_t row = row_of(r, m);
-    T* y = static_cast<T*>(a.y) + (row * a.dout + blk.out_off + m) * a.cout;
+    if (wm * 64 + j * 16 + q >= n_rows) continue;
+    T* y = static_cast<T*>(a.y) + (int64_t(row[j]) * a.dout + blk.out_off + comp[j]) * a.cout;
     if constexpr (PARTS == 3) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -539,10 +533,11 @@ hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
   int64_t wgs = 0;
   for (int i = 0; i < l.n_blocks; ++i) {
     l.blk[i].wg0 = int(wgs);
-    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTile, a.index != nullptr);
+    wgs += xcd_workgroups(most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTile,
+                                     a.index != nullptr), (a.cout + kTile - 1) / kTile);
     if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
   }
-  const dim3 grid(unsigned(wgs), unsigned((a.cout + kTile - 1) / kTile));
+  const dim3 grid{unsigned(wgs)};
   if (a.w_trans) hipLaunchKernelGGL((k_mix<T, true>), grid, dim3(kThreads), 0, s, a, l);
   else hipLaunchKernelGGL((k_mix<T, false>), grid, dim3(kThreads), 0, s, a, l);
   return hipGetLastError();
