@@ -39,7 +39,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;
 
 // ------------------------------------------------------------ quantisation
 
@@ -164,12 +163,24 @@ __device__ __forceinline__ int column_in(int s) {
   else return (s & ~31) | ((s >> 2) & 3) << 3 | ((s >> 4) & 1) << 2 | (s & 3);
 }
 
+// Steps whose scales of the rows are in LDS at once.  Asked for step by step
+// they cost more of the L1 than the tiles (a line of memory for every row):
+// 16 experts of 2048 x 1024 channels took 96 us, 69 without any.
+constexpr int kScaleSteps = 16;
+
+// Tiles of 128 rows by 128 columns, one chunk of 128 k multiplied while the
+// next is on its way; two workgroups on a compute unit.  16,411 rows of 16
+// experts, 2048 to 1024 channels: 72 us (960 TFLOP/s); 256 columns a
+// workgroup, alone on its compute unit with two chunks on their way, 85 us,
+// three rounds of workgroups where 2.3 would do.
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const MixList l,
+__global__ void __launch_bounds__(kThreads, 2) k_fp8_mix(const Fp8MixArgs a, const MixList l,
                                                       const Fp8Layout at) {
-  // two chunks of 128 k, one read while the other is on its way
-  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kTileBytes], s_w0[kTileBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t s_x1[kTileBytes], s_w1[kTileBytes];
+  // a name for every stage: reads of one are then known not to wait for loads
+  // into the other
+  __shared__ __attribute__((aligned(128))) uint8_t s_x0[TileLoad::kBytes], s_w0[TileLoad::kBytes];
+  __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_w1[TileLoad::kBytes];
+  __shared__ float s_scale[kTileRows][kScaleSteps + 1];
   if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
   const int* header = static_cast<const int*>(a.packed);
   if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
@@ -180,15 +191,16 @@ __global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const 
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   int col_tile;
-  if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
-                     blockIdx.x - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
-                     col_tile))
+  if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg,
+                     kTileRows, blockIdx.x - unsigned(blk.wg0),
+                     unsigned((a.cout + 127) / 128), tile, col_tile))
     return;
   const RowOrder order(a.index, a.order, tile, a.q);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
-  const int col0 = col_tile * kTile;
-  const int n_rows = int(min(int64_t(kTile), tile.rows - tile.at));
+  const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
+  const TileLoad load;
+  const int wm = load.wave & 1, wn = load.wave >> 1;
+  const int col0 = col_tile * 128;
+  const int n_rows = int(min(int64_t(kTileRows), tile.rows - tile.at));
   const TileRows rows(tile.at, blk.deg);
   f32x4 acc[4][4];
 #pragma unroll
@@ -196,66 +208,84 @@ __global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const 
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
 
-  const TileLane tl;
+  // the rows this lane loads, and those it ends with; rows past the end are
+  // the last one again, and so are columns
   const int runs = at.in_blocks;
-  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
   const int64_t kpad = int64_t(runs) * 128;
   const uint8_t* packed = static_cast<const uint8_t*>(a.packed);
-  const int n_src = tile.group < a.n_groups ? blk.n_src : 0;
-  // rows past the end are the last one again, and so are columns
-  const uint8_t *xrow[4], *wrow[4];
-  // the rows this lane loads, and those it ends with
   int load_row[4], load_m[4], row[4], comp[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    load_row[j] = order(rows.place(min(tl.first + j * 32, n_rows - 1), load_m[j]));
+    load_row[j] = order(rows.place(min(load.row + j * 32, n_rows - 1), load_m[j]));
     row[j] = order(rows.place(min(wm * 64 + j * 16 + q, n_rows - 1), comp[j]));
   }
+  int scale_m;  // two threads share a row's scales
+  const int scale_of = order(rows.place(min(int(threadIdx.x) / 2, n_rows - 1), scale_m));
+  const float* scale_row = a.scale + (int64_t(scale_of) * a.din + scale_m) * runs;
+  const uint8_t *xrow[4], *wrow[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     xrow[j] = static_cast<const uint8_t*>(a.q) +
-              (int64_t(load_row[j]) * a.din + load_m[j]) * a.cin + tl.piece * 16;
-    const int n = min(col0 + column_in<T>(tl.first + j * 32), a.cout - 1);
+              (int64_t(load_row[j]) * a.din + load_m[j]) * a.cin + load.piece * 16;
+    const int n = min(col0 + column_in<T>(load.row + j * 32), a.cout - 1);
     wrow[j] = packed + at.codes + (int64_t(tile.group) * a.pairs * a.cout + n) * kpad +
-              tl.piece * 16;
+              load.piece * 16;
   }
-  const float* srow[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    srow[j] = a.scale + (int64_t(row[j]) * a.din + comp[j]) * runs;
 
-  const int steps = n_src * runs;
-  int src = 0, b = 0;  // of the chunk asked for next
-  float sx[4], sw;
-  const auto fetch = [&](uint8_t* x, uint8_t* w) {
-    const MixSource sc = l.src[blk.src0 + src];
-    const bool in = b * 128 + tl.piece * 16 < a.cin;
-    const uint8_t *xp[4], *wp[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      xp[j] = in ? xrow[j] + int64_t(sc.in_off) * a.cin + b * 128 : zeros;
-      wp[j] = wrow[j] + int64_t(sc.pair) * a.cout * kpad + b * 128;
-    }
-    tile_load(xp, x);
-    tile_load(wp, w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sx[j] = srow[j][sc.in_off * runs + b];
-    const int64_t mat = int64_t(tile.group) * a.pairs + sc.pair;
-    sw = reinterpret_cast<const float*>(packed + at.scales)[(mat * at.out_blocks + col_tile) *
-                                                                runs + b];
-    if (++b == runs) {
+  // step s is run s % runs of source s / runs
+  const int steps = tile.group < a.n_groups ? blk.n_src * runs : 0;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
+  int64_t xo = 0, wo = 0;  // of the chunk asked for next
+  int src = -1, b = runs - 1;
+  const auto advance = [&]() {  // past the last chunk it is asked for again
+    if (b + 1 < runs) {
+      ++b;
+      xo += 128;
+      wo += 128;
+    } else if (src + 1 < blk.n_src) {
+      const MixSource sc = l.src[blk.src0 + ++src];
       b = 0;
-      ++src;
+      xo = int64_t(sc.in_off) * a.cin;
+      wo = int64_t(sc.pair) * a.cout * kpad;
     }
   };
-  const auto turn = [&](const uint8_t* x, const uint8_t* w, uint8_t* x_next, uint8_t* w_next,
-                        bool more) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this chunk is here
+  const auto fetch = [&](uint8_t* x, uint8_t* w) {
+    advance();
+    const bool in = b * 128 + load.piece * 16 < a.cin;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load.ask(in ? xrow[j] + xo : zeros, x, j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load.ask(wrow[j] + wo, w, j);
+  };
+  // scales of the next kScaleSteps steps: the rows' into LDS, this wavefront's
+  // columns' into its lanes
+  float sw_lane = 0.0f;
+  constexpr int SS = kScaleSteps;
+  const auto scales = [&](int step0) {
+    float v[SS / 2];
+#pragma unroll
+    for (int i = 0; i < SS / 2; ++i) {
+      const int s = min(step0 + int(threadIdx.x) % 2 + i * 2, steps - 1), of = s / runs;
+      v[i] = scale_row[l.src[blk.src0 + of].in_off * runs + s - of * runs];
+    }
+#pragma unroll
+    for (int i = 0; i < SS / 2; ++i) s_scale[threadIdx.x / 2][threadIdx.x % 2 + i * 2] = v[i];
+    const int s = min(step0 + lane % SS, steps - 1), of = s / runs;
+    const int64_t mat = int64_t(tile.group) * a.pairs + l.src[blk.src0 + of].pair;
+    sw_lane = reinterpret_cast<const float*>(packed + at.scales)[
+        (mat * at.out_blocks + col_tile) * runs + s - of * runs];
+    asm volatile("" ::"v"(sw_lane));  // here, and not where it is used: the walk waits for no loads
+  };
+  const auto turn = [&](const uint8_t* x, const uint8_t* w, uint8_t* x_free, uint8_t* w_free,
+                        int step) {
+    tile_wait();
+    fetch(x_free, w_free);
+    if (step >= steps) return;
+    const int at_step = step % SS;
+    const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sw_lane), at_step));
     float f[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = sx[j] * sw;
-    __syncthreads();
-    if (more) fetch(x_next, w_next);
+    for (int j = 0; j < 4; ++j) f[j] = s_scale[wm * 64 + j * 16 + q][at_step] * sw;
     const auto operand = [&](const uint8_t* s, int r) {
       const u32x4 lo = *reinterpret_cast<const u32x4*>(tile_at(s, r, h));
       const u32x4 hi = *reinterpret_cast<const u32x4*>(tile_at(s, r, 4 + h));
@@ -268,19 +298,26 @@ __global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const auto wf = operand(w, wn * 64 + i * 16 + q);
+      f32x4 t[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x4 t = product(wf, xf[j]);
+      for (int j = 0; j < 4; ++j) t[j] = product(wf, xf[j]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[r], f[j], acc[i][j][r]);
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[j][r], f[j], acc[i][j][r]);
     }
   };
   if (steps > 0) fetch(s_x0, s_w0);
   for (int step = 0; step < steps; step += 2) {
-    turn(s_x0, s_w0, s_x1, s_w1, step + 1 < steps);
-    if (step + 1 < steps) turn(s_x1, s_w1, s_x0, s_w0, step + 2 < steps);
+    if (step % SS == 0) {
+      __syncthreads();
+      scales(step);
+      __syncthreads();
+    }
+    turn(s_x0, s_w0, s_x1, s_w1, step);
+    turn(s_x1, s_w1, s_x0, s_w0, step + 1);
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load writes to LDS after the end
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (wm * 64 + j * 16 + q >= n_rows) continue;
@@ -305,6 +342,168 @@ __global__ void __launch_bounds__(kThreads) k_fp8_mix(const Fp8MixArgs a, const 
       }
     }
   }
+}
+
+// Where every block has one source of at most 128 channels, that is one step:
+// a wavefront holds 128 columns of W in registers and walks over its group's
+// rows, 16 at a time, whose x goes from memory into the products' operand
+// without passing through LDS; no wavefront waits for another.  The next 16
+// rows' x and scales are under way meanwhile, and where the 16 after them lie.
+// Nothing in the walk is conditional (a wait for loads would have to wait for
+// stores that may not have been issued): rows past the end are the last atom's
+// again, written with the same values.
+constexpr int kStreamRows = 64;  // of a workgroup's wavefronts together
+
+template <class T, bool FULL>
+__global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, const MixList l,
+                                                            const Fp8Layout lay, int chunk) {
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const int* header = static_cast<const int*>(a.packed);
+  if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
+      header[3] != a.pairs || header[4] != a.n_groups)
+    return;
+  int bi = 0;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  const MixBlock blk = l.blk[bi];
+  GroupTile tile;
+  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, chunk,
+                 int64_t(blockIdx.x) - blk.wg0, tile))
+    return;
+  const RowOrder order(a.index, a.order, tile, a.q);
+  const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int col0 = int(blockIdx.y) * 128, deg = blk.deg;
+  const int n = int(min(int64_t(chunk), tile.rows - tile.at));
+  const int last = int((tile.at + n - 1) / deg);
+  const TileRows rows(tile.at, deg);
+  const int step_at = kStreamRows / deg, step_m = kStreamRows % deg;
+  int m, at = rows.place(wave * 16 + q, m);  // of the next row to look up
+  struct Row {
+    int row, m;
+  };
+  const auto look = [&]() {
+    const Row r{order(min(at, last)), m};
+    at += step_at;
+    m += step_m;
+    if (m >= deg) {
+      m -= deg;
+      ++at;
+    }
+    return r;
+  };
+  const bool zero = tile.group >= a.n_groups || blk.n_src == 0;
+  const MixSource sc = zero ? MixSource{0, 0} : l.src[blk.src0];
+  const uint8_t* x0 = static_cast<const uint8_t*>(a.q) + int64_t(sc.in_off) * a.cin;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
+  const bool in_lo = h * 16 < a.cin, in_hi = 64 + h * 16 < a.cin;
+  struct X {
+    u32x4 lo, hi;
+    float s;
+  };
+  const auto fetch = [&](const Row& r) {
+    const int64_t at_row = int64_t(r.row) * a.din + r.m;
+    const uint8_t* p = x0 + at_row * a.cin + h * 16;
+    return X{*reinterpret_cast<const u32x4*>(in_lo ? p : zeros),
+             *reinterpret_cast<const u32x4*>(in_hi ? p + 64 : zeros),
+             a.scale[at_row + sc.in_off]};
+  };
+  Row now = look(), next = look();
+  X x = fetch(now);
+
+  const int64_t mat = zero ? 0 : int64_t(tile.group) * a.pairs + sc.pair;
+  const uint8_t* packed = static_cast<const uint8_t*>(a.packed);
+  const float sw = zero ? 0.0f
+                        : reinterpret_cast<const float*>(packed + lay.scales)[mat * lay.out_blocks +
+                                                                              blockIdx.y];
+  const auto operand = [&](u32x4 lo, u32x4 hi) {
+    return Operand<T>::of(i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
+                                int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])});
+  };
+  typename Operand<T>::type wf[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = min(col0 + column_in<T>(i * 16 + q), a.cout - 1);
+    const uint8_t* w = packed + lay.codes + (mat * a.cout + c) * 128 + h * 16;
+    wf[i] = operand(*reinterpret_cast<const u32x4*>(w), *reinterpret_cast<const u32x4*>(w + 64));
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the walk counts its own loads alone
+  for (int t0 = wave * 16; t0 < n; t0 += kStreamRows) {
+    const X cur = x;
+    x = fetch(next);
+    const Row after = look();
+    __builtin_amdgcn_sched_barrier(0);
+    const auto xf = operand(cur.lo, cur.hi);
+    const float f = cur.s * sw;
+    T* y = static_cast<T*>(a.y) + (int64_t(now.row) * a.dout + blk.out_off + now.m) * a.cout + col0;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const f32x4 t0 = product(wf[i], xf), t1 = product(wf[i + 1], xf);
+      f32x4 u0, u1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        u0[r] = zero ? 0.0f : t0[r] * f;
+        u1[r] = zero ? 0.0f : t1[r] * f;
+      }
+      if constexpr (std::is_same_v<T, float>) {
+        if (FULL || col0 + i * 16 + h * 4 < a.cout)
+          *reinterpret_cast<f32x4*>(y + i * 16 + h * 4) = u0;
+        if (FULL || col0 + i * 16 + 16 + h * 4 < a.cout)
+          *reinterpret_cast<f32x4*>(y + i * 16 + 16 + h * 4) = u1;
+      } else {
+        bf16x8 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[r] = __bf16(u0[r]);
+          v[4 + r] = __bf16(u1[r]);
+        }
+        if (FULL || col0 + i * 16 + h * 8 < a.cout)
+          *reinterpret_cast<bf16x8*>(y + i * 16 + h * 8) = v;
+      }
+    }
+    now = next;
+    next = after;
+  }
+}
+
+// Rows of a workgroup's walk: some workgroups for every one that is resident.
+int stream_chunk(int64_t rows) {
+  const int64_t n = (rows / 4096 + kStreamRows - 1) / kStreamRows * kStreamRows;
+  return int(std::min<int64_t>(1024, std::max<int64_t>(kStreamRows, n)));
+}
+
+template <class T>
+hipError_t launch_fp8_stream(const Fp8MixArgs& a, MixList l, hipStream_t s) {
+  int64_t wgs = 0, comps = 0;
+  for (int i = 0; i < l.n_blocks; ++i) comps += l.blk[i].deg;
+  const int chunk = stream_chunk(a.n_rows * comps);
+  for (int i = 0; i < l.n_blocks; ++i) {
+    l.blk[i].wg0 = int(wgs);
+    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, chunk, a.index != nullptr);
+  }
+  const Fp8Layout at = fp8_layout(a.n_groups, a.pairs, a.cin, a.cout);
+  const dim3 grid(unsigned(wgs), unsigned((a.cout + 127) / 128));
+  if (a.cout % 128 == 0)
+    hipLaunchKernelGGL((k_fp8_stream<T, true>), grid, dim3(kThreads), 0, s, a, l, at, chunk);
+  else
+    hipLaunchKernelGGL((k_fp8_stream<T, false>), grid, dim3(kThreads), 0, s, a, l, at, chunk);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_fp8_mix_t(const Fp8MixArgs& a, MixList l, hipStream_t s) {
+  bool one = a.cin <= 128;
+  for (int i = 0; i < l.n_blocks; ++i) one &= l.blk[i].n_src <= 1;
+  if (one) return launch_fp8_stream<T>(a, l, s);
+  int64_t wgs = 0;
+  for (int i = 0; i < l.n_blocks; ++i) {
+    l.blk[i].wg0 = int(wgs);
+    wgs += xcd_workgroups(most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTileRows,
+                                     a.index != nullptr), (a.cout + 127) / 128);
+    if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
+  }
+  const Fp8Layout at = fp8_layout(a.n_groups, a.pairs, a.cin, a.cout);
+  hipLaunchKernelGGL((k_fp8_mix<T>), dim3(unsigned(wgs)), dim3(kThreads), 0, s, a, l, at);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -345,20 +544,8 @@ hipError_t launch_fp8_quantize(int64_t n_rows, int C, const void* x, int bf16, v
   return bf16 ? go(bf16_t{}) : go(float{});
 }
 
-hipError_t launch_fp8_mix(const Fp8MixArgs& a, const MixList& list, int bf16, hipStream_t s) {
-  MixList l = list;
-  int64_t wgs = 0;
-  for (int i = 0; i < l.n_blocks; ++i) {
-    l.blk[i].wg0 = int(wgs);
-    wgs += xcd_workgroups(most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, kTile,
-                                     a.index != nullptr), (a.cout + kTile - 1) / kTile);
-  }
-  if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
-  const Fp8Layout at = fp8_layout(a.n_groups, a.pairs, a.cin, a.cout);
-  const dim3 grid{unsigned(wgs)};
-  if (bf16) hipLaunchKernelGGL((k_fp8_mix<bf16_t>), grid, dim3(kThreads), 0, s, a, l, at);
-  else hipLaunchKernelGGL((k_fp8_mix<float>), grid, dim3(kThreads), 0, s, a, l, at);
-  return hipGetLastError();
+hipError_t launch_fp8_mix(const Fp8MixArgs& a, const MixList& l, int bf16, hipStream_t s) {
+  return bf16 ? launch_fp8_mix_t<bf16_t>(a, l, s) : launch_fp8_mix_t<float>(a, l, s);
 }
 
 }  // namespace e3k
