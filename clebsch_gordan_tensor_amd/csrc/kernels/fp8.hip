@@ -27,12 +27,14 @@
 #include "fp8.h"
 #include "group_tiles.h"
 #include "registry.h"
+#include "row_halves.h"
 #include "tile128.h"
 
 namespace e3k {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -391,8 +393,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, 
     }
     return r;
   };
-  const bool zero = tile.group >= a.n_groups || blk.n_src == 0;
-  const MixSource sc = zero ? MixSource{0, 0} : l.src[blk.src0];
+  if (tile.group >= a.n_groups || blk.n_src == 0) {  // zeros
+    for (int t0 = wave * 16; t0 < n; t0 += kStreamRows) {
+      const Row r = look();
+      T* y = static_cast<T*>(a.y) + (int64_t(r.row) * a.dout + blk.out_off + r.m) * a.cout;
+      for (int c = col0 + h; c < min(col0 + 128, a.cout); c += 4) y[c] = T{};
+    }
+    return;
+  }
+  const MixSource sc = l.src[blk.src0];
+  const RowHalves halves;
   const uint8_t* x0 = static_cast<const uint8_t*>(a.q) + int64_t(sc.in_off) * a.cin;
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
   const bool in_lo = h * 16 < a.cin, in_hi = 64 + h * 16 < a.cin;
@@ -410,11 +420,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, 
   Row now = look(), next = look();
   X x = fetch(now);
 
-  const int64_t mat = zero ? 0 : int64_t(tile.group) * a.pairs + sc.pair;
+  const int64_t mat = int64_t(tile.group) * a.pairs + sc.pair;
   const uint8_t* packed = static_cast<const uint8_t*>(a.packed);
-  const float sw = zero ? 0.0f
-                        : reinterpret_cast<const float*>(packed + lay.scales)[mat * lay.out_blocks +
-                                                                              blockIdx.y];
+  const float sw =
+      reinterpret_cast<const float*>(packed + lay.scales)[mat * lay.out_blocks + blockIdx.y];
   const auto operand = [&](u32x4 lo, u32x4 hi) {
     return Operand<T>::of(i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
                                 int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])});
@@ -434,30 +443,45 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, 
     __builtin_amdgcn_sched_barrier(0);
     const auto xf = operand(cur.lo, cur.hi);
     const float f = cur.s * sw;
-    T* y = static_cast<T*>(a.y) + (int64_t(now.row) * a.dout + blk.out_off + now.m) * a.cout + col0;
+    Row r0, r1;
+    halves.rows(now.row, r0.row, r1.row);
+    halves.rows(now.m, r0.m, r1.m);
+    const auto start = [&](const Row& r) {
+      return reinterpret_cast<uint8_t*>(static_cast<T*>(a.y) +
+                                        (int64_t(r.row) * a.dout + blk.out_off + r.m) * a.cout +
+                                        col0) + halves.column;
+    };
+    uint8_t *y0 = start(r0), *y1 = start(r1);
+    constexpr int LINE = 128 / sizeof(T), PER = LINE / 16;  // columns, products of a line
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const f32x4 t0 = product(wf[i], xf), t1 = product(wf[i + 1], xf);
-      f32x4 u0, u1;
+    for (int c = 0; c < 128 / LINE; ++c) {
+      f32x4 u[PER];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        u0[r] = zero ? 0.0f : t0[r] * f;
-        u1[r] = zero ? 0.0f : t1[r] * f;
+      for (int i = 0; i < PER; ++i) {
+        const f32x4 t = product(wf[c * PER + i], xf);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[i][r] = t[r] * f;
       }
+      u32x4 v[2];
       if constexpr (std::is_same_v<T, float>) {
-        if (FULL || col0 + i * 16 + h * 4 < a.cout)
-          *reinterpret_cast<f32x4*>(y + i * 16 + h * 4) = u0;
-        if (FULL || col0 + i * 16 + 16 + h * 4 < a.cout)
-          *reinterpret_cast<f32x4*>(y + i * 16 + 16 + h * 4) = u1;
+        v[0] = __builtin_bit_cast(u32x4, u[0]);
+        v[1] = __builtin_bit_cast(u32x4, u[1]);
       } else {
-        bf16x8 v;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          v[r] = __bf16(u0[r]);
-          v[4 + r] = __bf16(u1[r]);
+        for (int i = 0; i < 2; ++i) {
+          bf16x8 b;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            b[r] = __bf16(u[2 * i][r]);
+            b[4 + r] = __bf16(u[2 * i + 1][r]);
+          }
+          v[i] = __builtin_bit_cast(u32x4, b);
         }
-        if (FULL || col0 + i * 16 + h * 8 < a.cout)
-          *reinterpret_cast<bf16x8*>(y + i * 16 + h * 8) = v;
+      }
+      halves.trade(v[0], v[1]);
+      if (FULL || col0 + c * LINE + halves.column / int(sizeof(T)) < a.cout) {
+        __builtin_nontemporal_store(v[0], reinterpret_cast<u32x4*>(y0 + c * 128));
+        __builtin_nontemporal_store(v[1], reinterpret_cast<u32x4*>(y1 + c * 128));
       }
     }
     now = next;
@@ -467,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, 
 
 // Rows of a workgroup's walk: some workgroups for every one that is resident.
 int stream_chunk(int64_t rows) {
-  const int64_t n = (rows / 4096 + kStreamRows - 1) / kStreamRows * kStreamRows;
-  return int(std::min<int64_t>(1024, std::max<int64_t>(kStreamRows, n)));
+  const int64_t n = (rows / 1024 + kStreamRows - 1) / kStreamRows * kStreamRows;
+  return int(std::min<int64_t>(4096, std::max<int64_t>(kStreamRows, n)));
 }
 
 template <class T>
@@ -489,8 +513,95 @@ hipError_t launch_fp8_stream(const Fp8MixArgs& a, MixList l, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Few rows of a group: what counts is that the weights are asked for at once.
+// A wavefront takes 16 rows and 16 columns and asks for 8 steps (float32: 4)
+// before it multiplies the first; the steps' sums are added in the other
+// kernels' order, so that a row's result stays the same.
+template <class T>
+__global__ void __launch_bounds__(64) k_fp8_few(const Fp8MixArgs a, const MixList l,
+                                                const Fp8Layout lay) {
+  constexpr int N = std::is_same_v<T, float> ? 4 : 8;
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const int* header = static_cast<const int*>(a.packed);
+  if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
+      header[3] != a.pairs || header[4] != a.n_groups)
+    return;
+  int bi = 0;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  const MixBlock blk = l.blk[bi];
+  GroupTile tile;
+  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, 16,
+                 int64_t(blockIdx.x) - blk.wg0, tile))
+    return;
+  const RowOrder order(a.index, a.order, tile, a.q);
+  const int lane = threadIdx.x, q = lane & 15, h = lane >> 4;
+  const int n_rows = int(min(int64_t(16), tile.rows - tile.at)), col0 = int(blockIdx.y) * 16;
+  const TileRows rows(tile.at, blk.deg);
+  int m;
+  const int row = order(rows.place(min(q, n_rows - 1), m));
+  const int64_t at_row = int64_t(row) * a.din + m;
+  const int runs = lay.in_blocks;
+  const int steps = tile.group < a.n_groups ? blk.n_src * runs : 0;
+  const uint8_t* x = static_cast<const uint8_t*>(a.q) + at_row * a.cin + h * 16;
+  const float* sx = a.scale + at_row * runs;
+  const uint8_t* packed = static_cast<const uint8_t*>(a.packed);
+  const float* sw = reinterpret_cast<const float*>(packed + lay.scales);
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
+  const auto operand = [&](u32x4 lo, u32x4 hi) {
+    return Operand<T>::of(i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
+                                int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])});
+  };
+  f32x4 acc{};
+  for (int s0 = 0; s0 < steps; s0 += N) {
+    u32x4 xv[N][2], wv[N][2];
+    float fx[N], fw[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {  // past the last step it is asked for again
+      const int s = min(s0 + i, steps - 1), of = s / runs, b = s - of * runs;
+      const MixSource sc = l.src[blk.src0 + of];
+      const int64_t mat = int64_t(tile.group) * a.pairs + sc.pair;
+      const uint8_t* xp = x + int64_t(sc.in_off) * a.cin + b * 128;
+      const uint8_t* wp = packed + lay.codes + ((mat * a.cout + col0 + q) * runs + b) * 128 + h * 16;
+      xv[i][0] = *reinterpret_cast<const u32x4*>(b * 128 + h * 16 < a.cin ? xp : zeros);
+      xv[i][1] = *reinterpret_cast<const u32x4*>(b * 128 + 64 + h * 16 < a.cin ? xp + 64 : zeros);
+      wv[i][0] = *reinterpret_cast<const u32x4*>(wp);
+      wv[i][1] = *reinterpret_cast<const u32x4*>(wp + 64);
+      fx[i] = sx[sc.in_off * runs + b];
+      fw[i] = sw[(mat * lay.out_blocks + col0 / 128) * runs + b];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (s0 + i < steps) {
+        const f32x4 t = product(operand(wv[i][0], wv[i][1]), operand(xv[i][0], xv[i][1]));
+        const float f = fx[i] * fw[i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(t[r], f, acc[r]);
+      }
+  }
+  if (q >= n_rows) return;
+  T* y = static_cast<T*>(a.y) + (int64_t(row) * a.dout + blk.out_off + m) * a.cout + col0 + h * 4;
+  if constexpr (std::is_same_v<T, float>)
+    *reinterpret_cast<f32x4*>(y) = acc;
+  else
+    *reinterpret_cast<bf16x4*>(y) = __builtin_convertvector(acc, bf16x4);
+}
+
+template <class T>
+hipError_t launch_fp8_few(const Fp8MixArgs& a, MixList l, hipStream_t s) {
+  int64_t wgs = 0;
+  for (int i = 0; i < l.n_blocks; ++i) {
+    l.blk[i].wg0 = int(wgs);
+    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, 16, a.index != nullptr);
+  }
+  hipLaunchKernelGGL((k_fp8_few<T>), dim3(unsigned(wgs), unsigned(a.cout / 16)), dim3(64), 0, s,
+                     a, l, fp8_layout(a.n_groups, a.pairs, a.cin, a.cout));
+  return hipGetLastError();
+}
+
 template <class T>
 hipError_t launch_fp8_mix_t(const Fp8MixArgs& a, MixList l, hipStream_t s) {
+  if (few_rows(a.n_rows, a.n_groups, l)) return launch_fp8_few<T>(a, l, s);
   bool one = a.cin <= 128;
   for (int i = 0; i < l.n_blocks; ++i) one &= l.blk[i].n_src <= 1;
   if (one) return launch_fp8_stream<T>(a, l, s);

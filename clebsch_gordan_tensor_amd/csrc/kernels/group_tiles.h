@@ -126,6 +126,17 @@ struct TileRows {
   }
 };
 
+// Whether the groups have so few rows that kernels of small tiles answer
+// sooner.  One group, 1024 to 1024 channels in bf16, us by rows, small tiles and
+// large: 1 10.4 and 25.8, 128 10.8 and 26.8, 256 14.1 and 27.1, 512 20.3 and
+// 27.1; ten groups: 64 15.8 and 27.0, 128 18.5 and 26.9, 256 27.8 and 27.1; in 8
+// bits they part between 256 and 512 rows, one group or ten.
+inline bool few_rows(int64_t n_rows, int n_groups, const MixList& l) {
+  int deg = 1;
+  for (int i = 0; i < l.n_blocks; ++i) deg = l.blk[i].deg > deg ? l.blk[i].deg : deg;
+  return n_rows * deg <= 16 * int64_t(n_groups) + 112;
+}
+
 // Most tiles that n_rows rows in n_groups groups (and some without) can fill.
 inline int64_t most_tiles(int64_t n_rows, int n_groups, int deg, int64_t size, bool grouped) {
   return (n_rows * deg + size - 1) / size + (grouped ? n_groups : 0);

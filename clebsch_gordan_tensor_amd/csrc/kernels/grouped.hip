@@ -26,6 +26,7 @@
 #include "common.h"
 #include "group_tiles.h"
 #include "registry.h"
+#include "row_halves.h"
 
 namespace e3k {
 namespace {
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
   place = look();
   __syncthreads();
 
+  const RowHalves halves;
   const MixSource sc = l.src[blk.src0];
   const int piece = tid % TPR, r0 = tid / TPR;
   const bool in = piece * VEC < a.cin;
@@ -453,14 +455,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
       }
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const int2 to = s_row[buf][(wm * RT + j) * 16 + q];
-      T* y = static_cast<T*>(a.y) + (int64_t(to.x) * a.dout + blk.out_off + to.y) * a.cout;
-      if constexpr (PARTS == 3) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (FULL || col0 + i * 16 + h * 4 < a.cout)
-            *reinterpret_cast<f32x4*>(y + col0 + i * 16 + h * 4) = acc[j / JB][i][j % JB];
+      if constexpr (PARTS == 3) {  // 32 columns are a line
+        f32x4 v0 = acc[j / JB][0][j % JB], v1 = acc[j / JB][1][j % JB];
+        halves.trade(v0, v1);
+        const int c = col0 + halves.column / 4, r = (wm * RT + j) * 16 + (q & 7);
+        const int2 r0 = s_row[buf][r], r1 = s_row[buf][r + 8];
+        T* y = static_cast<T*>(a.y) + int64_t(blk.out_off) * a.cout + c;
+        if (FULL || c < a.cout) {
+          __builtin_nontemporal_store(
+              v0, reinterpret_cast<f32x4*>(y + (int64_t(r0.x) * a.dout + r0.y) * a.cout));
+          __builtin_nontemporal_store(
+              v1, reinterpret_cast<f32x4*>(y + (int64_t(r1.x) * a.dout + r1.y) * a.cout));
+        }
       } else {
+        const int2 to = s_row[buf][(wm * RT + j) * 16 + q];
+        T* y = static_cast<T*>(a.y) + (int64_t(to.x) * a.dout + blk.out_off + to.y) * a.cout;
         bf16x8 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -477,12 +486,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
 // Rows of a workgroup's walk: a few workgroups for every one that is resident
 // (two on a compute unit).
 int stream_chunk(int64_t rows) {
-#ifndef V_WG
-#define V_WG 2048
-#define V_MAX 1024
-#endif
-  const int64_t n = (rows / V_WG + kStreamRows - 1) / kStreamRows * kStreamRows;
-  return int(std::min<int64_t>(V_MAX, std::max<int64_t>(kStreamRows, n)));
+  const int64_t n = (rows / 2048 + kStreamRows - 1) / kStreamRows * kStreamRows;
+  return int(std::min<int64_t>(1024, std::max<int64_t>(kStreamRows, n)));
 }
 
 template <class T, bool WT, int NK>
@@ -526,8 +531,105 @@ bool streams(const MixArgs& a, const MixList& l) {
   return a.cin <= (sizeof(T) == 2 ? 256 : 128);
 }
 
+// Few rows of a group: what counts is that the weights are asked for at once.
+// A wavefront takes 16 rows and 16 columns, straight from memory into the
+// products' operands, and asks for 4 (bf16: 8) times 32 k before it multiplies
+// the first; the products are added in the other kernels' order, so that a
+// row's result stays the same.
+template <class T, bool WT>
+__global__ void __launch_bounds__(64) k_mix_few(const MixArgs a, const MixList l) {
+  constexpr int PARTS = Chunk<T>::PARTS, VEC = 16 / sizeof(T), N = PARTS == 3 ? 4 : 8;
+  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  int bi = 0;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  const MixBlock blk = l.blk[bi];
+  GroupTile tile;
+  if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, 16,
+                 int64_t(blockIdx.x) - blk.wg0, tile))
+    return;
+  const RowOrder order(a.index, a.order, tile, a.x);
+  const int lane = threadIdx.x, q = lane & 15, h = lane >> 4;
+  const int n_rows = int(min(int64_t(16), tile.rows - tile.at)), col0 = int(blockIdx.y) * 16;
+  const TileRows rows(tile.at, blk.deg);
+  int m;
+  const int row = order(rows.place(min(q, n_rows - 1), m));
+  const int chunks = (a.cin + 31) / 32;
+  const int steps = tile.group < a.n_groups ? blk.n_src * chunks : 0;
+  const T* x = static_cast<const T*>(a.x) + (int64_t(row) * a.din + m) * a.cin;
+  const int col = min(col0 + q, a.cout - 1);  // (columns past the end are not stored)
+  const T* W = static_cast<const T*>(a.W) + int64_t(tile.group) * a.pairs * a.cin * a.cout +
+               (WT ? int64_t(col) * a.cin : col);
+  f32x4 acc[1][1] = {};
+  for (int s0 = 0; s0 < steps; s0 += N) {
+    T xv[N][8], wv[N][8];
+    bool have[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {  // past the last step it is asked for again
+      const int s = min(s0 + i, steps - 1), of = s / chunks;
+      int k = (s - of * chunks) * 32 + h * 8;
+      have[i] = k < a.cin;
+      k = have[i] ? k : 0;
+      const MixSource sc = l.src[blk.src0 + of];
+      const T* xp = x + int64_t(sc.in_off) * a.cin + k;
+      const T* w = W + int64_t(sc.pair) * a.cin * a.cout + (WT ? k : int64_t(k) * a.cout);
+#pragma unroll
+      for (int e = 0; e < 8; e += VEC)
+        *reinterpret_cast<u32x4*>(&xv[i][e]) = *reinterpret_cast<const u32x4*>(xp + e);
+      if constexpr (WT) {
+#pragma unroll
+        for (int e = 0; e < 8; e += VEC)
+          *reinterpret_cast<u32x4*>(&wv[i][e]) = *reinterpret_cast<const u32x4*>(w + e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wv[i][e] = w[int64_t(e) * a.cout];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const auto operand = [&](const T (&v)[8], bool have, bf16x8 (&out)[PARTS]) {
+      if constexpr (PARTS == 3) {
+        bf16x4 lo[3], hi[3];
+        split3(have ? f32x4{v[0], v[1], v[2], v[3]} : f32x4{}, lo);
+        split3(have ? f32x4{v[4], v[5], v[6], v[7]} : f32x4{}, hi);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          out[t] = __builtin_shufflevector(lo[t], hi[t], 0, 1, 2, 3, 4, 5, 6, 7);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          out[0][e] = have ? __builtin_bit_cast(__bf16, v[e]) : __bf16(0.0f);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (s0 + i < steps) {
+        bf16x8 xf[1][PARTS], wf[1][PARTS];
+        operand(xv[i], have[i], xf[0]);
+        operand(wv[i], have[i], wf[0]);
+        products<PARTS, 1, 1>(wf, xf, acc);
+      }
+  }
+  if (q >= n_rows || col0 + h * 4 >= a.cout) return;
+  T* y = static_cast<T*>(a.y) + (int64_t(row) * a.dout + blk.out_off + m) * a.cout + col0 + h * 4;
+  if constexpr (PARTS == 3) *reinterpret_cast<f32x4*>(y) = acc[0][0];
+  else *reinterpret_cast<bf16x4*>(y) = __builtin_convertvector(acc[0][0], bf16x4);
+}
+
+template <class T>
+hipError_t launch_few(const MixArgs& a, MixList l, hipStream_t s) {
+  int64_t wgs = 0;
+  for (int i = 0; i < l.n_blocks; ++i) {
+    l.blk[i].wg0 = int(wgs);
+    wgs += most_tiles(a.n_rows, a.n_groups, l.blk[i].deg, 16, a.index != nullptr);
+  }
+  const dim3 grid(unsigned(wgs), unsigned((a.cout + 15) / 16));
+  if (a.w_trans) hipLaunchKernelGGL((k_mix_few<T, true>), grid, dim3(64), 0, s, a, l);
+  else hipLaunchKernelGGL((k_mix_few<T, false>), grid, dim3(64), 0, s, a, l);
+  return hipGetLastError();
+}
+
 template <class T>
 hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
+  if (few_rows(a.n_rows, a.n_groups, l)) return launch_few<T>(a, l, s);
   if (streams<T>(a, l))
     return a.w_trans ? launch_stream_k<T, true>(a, l, s) : launch_stream_k<T, false>(a, l, s);
   int64_t wgs = 0;
