@@ -183,11 +183,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_mix(const Fp8MixArgs a, con
   __shared__ __attribute__((aligned(128))) uint8_t s_x0[TileLoad::kBytes], s_w0[TileLoad::kBytes];
   __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_w1[TileLoad::kBytes];
   __shared__ float s_scale[kTileRows][kScaleSteps + 1];
-  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   const int* header = static_cast<const int*>(a.packed);
-  if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
-      header[3] != a.pairs || header[4] != a.n_groups)
-    return;  // packed for another call
+  valid &= (header[0] == kFp8Magic) & (header[1] == a.cin) & (header[2] == a.cout) &
+           (header[3] == a.pairs) & (header[4] == a.n_groups);  // packed for this call
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_mix(const Fp8MixArgs a, con
   int col_tile;
   if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg,
                      kTileRows, blockIdx.x - unsigned(blk.wg0),
-                     unsigned((a.cout + 127) / 128), tile, col_tile))
+                     unsigned((a.cout + 127) / 128), tile, col_tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.q);
   const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
@@ -359,17 +358,16 @@ constexpr int kStreamRows = 64;  // of a workgroup's wavefronts together
 template <class T, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, const MixList l,
                                                             const Fp8Layout lay, int chunk) {
-  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   const int* header = static_cast<const int*>(a.packed);
-  if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
-      header[3] != a.pairs || header[4] != a.n_groups)
-    return;
+  valid &= (header[0] == kFp8Magic) & (header[1] == a.cin) & (header[2] == a.cout) &
+           (header[3] == a.pairs) & (header[4] == a.n_groups);  // packed for this call
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, chunk,
-                 int64_t(blockIdx.x) - blk.wg0, tile))
+                 int64_t(blockIdx.x) - blk.wg0, tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.q);
   const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
@@ -521,17 +519,16 @@ template <class T>
 __global__ void __launch_bounds__(64) k_fp8_few(const Fp8MixArgs a, const MixList l,
                                                 const Fp8Layout lay) {
   constexpr int N = std::is_same_v<T, float> ? 4 : 8;
-  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   const int* header = static_cast<const int*>(a.packed);
-  if (header[0] != kFp8Magic || header[1] != a.cin || header[2] != a.cout ||
-      header[3] != a.pairs || header[4] != a.n_groups)
-    return;
+  valid &= (header[0] == kFp8Magic) & (header[1] == a.cin) & (header[2] == a.cout) &
+           (header[3] == a.pairs) & (header[4] == a.n_groups);  // packed for this call
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, 16,
-                 int64_t(blockIdx.x) - blk.wg0, tile))
+                 int64_t(blockIdx.x) - blk.wg0, tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.q);
   const int lane = threadIdx.x, q = lane & 15, h = lane >> 4;

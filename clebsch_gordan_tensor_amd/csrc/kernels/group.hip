@@ -21,6 +21,7 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kPerLane = 8;                         // rows of a lane
 constexpr int kChunk = kThreads * kPerLane;         // rows of a workgroup
+constexpr int kFewCounts = 8192;                    // (groups + 1) x chunks
 
 __device__ __forceinline__ int key_of(const int* group, int64_t r, int n_groups) {
   const int g = group[r];
@@ -37,19 +38,24 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits, bool active) {
   return m;
 }
 
-// Adds the wavefront's lanes to count[key]; returns the count before this lane.
-__device__ __forceinline__ int place(int* count, int key, int bits, bool active) {
-  const uint64_t same = same_key(key, bits, active);
+// Adds the wavefront's lanes to count[key], `same` being those of this lane's
+// key: the first of them adds for all.
+__device__ __forceinline__ void count_same(int* count, int key, uint64_t same) {
   const int lane = threadIdx.x & 63;
-  const int first = active ? __ffsll((unsigned long long)same) - 1 : lane;
+  if (same && lane == __ffsll((unsigned long long)same) - 1) atomicAdd(count + key, __popcll(same));
+}
+// The same; returns the count before this lane.
+__device__ __forceinline__ int place_same(int* count, int key, uint64_t same) {
+  const int lane = threadIdx.x & 63;
+  const int first = same ? __ffsll((unsigned long long)same) - 1 : lane;
   int old = 0;
-  if (active && lane == first) old = atomicAdd(count + key, __popcll(same));
+  if (same && lane == first) old = atomicAdd(count + key, __popcll(same));
   old = __shfl(old, first);
   return old + __popcll(same & ((uint64_t(1) << lane) - 1));
 }
 
 // Exclusive prefix sums of v[0..n) in LDS by the whole workgroup, n <= 1025;
-// `part` holds a value for each thread.
+// `part` holds a value for each wavefront.
 __device__ __forceinline__ void prefix(int* v, int n, int* part) {
   const int tid = threadIdx.x, threads = blockDim.x;
   const int per = (n + threads - 1) / threads;
@@ -58,21 +64,22 @@ __device__ __forceinline__ void prefix(int* v, int n, int* part) {
     const int i = tid * per + j;
     if (i < n) s += v[i];
   }
-  part[tid] = s;
-  __syncthreads();
-  for (int o = 1; o < threads; o <<= 1) {
-    const int t = tid >= o ? part[tid - o] : 0;
-    __syncthreads();
-    part[tid] += t;
-    __syncthreads();
+  int t = s;  // inclusive over the wavefront
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(t, o);
+    if ((tid & 63) >= o) t += u;
   }
-  s = part[tid] - s;
+  if ((tid & 63) == 63) part[tid >> 6] = t;
+  __syncthreads();
+  s = t - s;
+  for (int j = 0; j < (tid >> 6); ++j) s += part[j];
   for (int j = 0; j < per; ++j) {
     const int i = tid * per + j;
     if (i < n) {
-      const int t = v[i];
+      const int c = v[i];
       v[i] = s;
-      s += t;
+      s += c;
     }
   }
   __syncthreads();
@@ -131,32 +138,52 @@ __global__ void __launch_bounds__(kThreads) k_group_scan(const GroupArgs a) {
   if (tid == 0) a.total[blockIdx.x] = before;
 }
 
+// FEW: few enough counts for every workgroup to add them up for itself, which
+// saves a launch.
+template <bool FEW>
 __global__ void __launch_bounds__(kThreads) k_group_place(const GroupArgs a) {
   __shared__ int s_at[kWaves][kMaxGroups + 1];  // next place of each group in each wavefront
   __shared__ int s_start[kMaxGroups + 1];
+  __shared__ int s_before[FEW ? kMaxGroups + 1 : 1];
   __shared__ int s_part[kThreads];
   const int G = a.n_groups, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  for (int g = tid; g <= G; g += kThreads) {
-    s_start[g] = a.total[g];
-    for (int j = 0; j < kWaves; ++j) s_at[j][g] = 0;
-  }
-  __syncthreads();
-  prefix(s_start, G + 1, s_part);
-  if (blockIdx.x == 0) {
-    for (int g = tid; g <= G; g += kThreads) a.offsets[g] = s_start[g];
-    write_header(a);
-  }
   const int64_t r0 = int64_t(blockIdx.x) * kChunk + w * 64 * kPerLane + lane;
   int key[kPerLane];
 #pragma unroll
   for (int j = 0; j < kPerLane; ++j) {
     const int64_t r = r0 + j * 64;
     key[j] = r < a.n_rows ? key_of(a.group, r, G) : -1;
-    if (key[j] >= 0) atomicAdd(&s_at[w][key[j]], 1);
+  }
+  for (int g = tid; g <= G; g += kThreads) {
+    s_start[g] = FEW ? 0 : a.total[g];
+    if (FEW) s_before[g] = 0;
+    for (int j = 0; j < kWaves; ++j) s_at[j][g] = 0;
   }
   __syncthreads();
+  uint64_t same[kPerLane];
+#pragma unroll
+  for (int j = 0; j < kPerLane; ++j) {
+    same[j] = same_key(max(key[j], 0), a.bits, key[j] >= 0);
+    count_same(s_at[w], key[j], same[j]);
+  }
+  if constexpr (FEW) {
+    const int n = (G + 1) * a.n_chunks;
+    for (int i = tid; i < n; i += kThreads) {
+      const int g = i / a.n_chunks, v = a.hist[i];
+      if (v) {
+        atomicAdd(s_start + g, v);
+        if (i - g * a.n_chunks < int(blockIdx.x)) atomicAdd(s_before + g, v);
+      }
+    }
+    __syncthreads();
+  }
+  prefix(s_start, G + 1, s_part);
+  if (blockIdx.x == 0) {
+    for (int g = tid; g <= G; g += kThreads) a.offsets[g] = s_start[g];
+    write_header(a);
+  }
   for (int g = tid; g <= G; g += kThreads) {
-    int at = s_start[g] + a.hist[int64_t(g) * a.n_chunks + blockIdx.x];
+    int at = s_start[g] + (FEW ? s_before[g] : a.hist[int64_t(g) * a.n_chunks + blockIdx.x]);
     for (int j = 0; j < kWaves; ++j) {
       const int n = s_at[j][g];
       s_at[j][g] = at;
@@ -166,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) k_group_place(const GroupArgs a) {
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kPerLane; ++j) {
-    const int p = place(s_at[w], max(key[j], 0), a.bits, key[j] >= 0);
+    const int p = place_same(s_at[w], key[j], same[j]);
     if (key[j] >= 0) a.order[p] = int(r0 + j * 64);
   }
 }
@@ -211,7 +238,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_group_small(const GroupArgs a
     const int r = r0 + j * 64;
     const bool in = r < a.n_rows;
     const int key = in ? key_of(a.group, r, G) : 0;
-    const int p = place(s_at[w], key, a.bits, in);
+    const int p = place_same(s_at[w], key, same_key(key, a.bits, in));
     if (in) a.order[p] = r;
   }
 }
@@ -251,9 +278,13 @@ hipError_t launch_group_index(int n_rows, int n_groups, const int* group, int* i
   hipLaunchKernelGGL(k_group_count, dim3(unsigned(a.n_chunks)), dim3(kThreads), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (int64_t(a.n_chunks) * (n_groups + 1) <= kFewCounts) {
+    hipLaunchKernelGGL((k_group_place<true>), dim3(unsigned(a.n_chunks)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_group_scan, dim3(unsigned(n_groups + 1)), dim3(kThreads), 0, s, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(k_group_place, dim3(unsigned(a.n_chunks)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_group_place<false>), dim3(unsigned(a.n_chunks)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

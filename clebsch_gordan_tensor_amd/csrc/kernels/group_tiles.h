@@ -18,8 +18,11 @@ struct GroupTile {
 };
 
 // An index of other sizes than the call's is not used (its launches do nothing).
+// Asked before find_tile and looked at after it, its words come with the offsets.
 __device__ __forceinline__ bool index_matches(const int* index, int64_t n_rows, int n_groups) {
-  return !index || (index[0] == kGroupMagic && index[1] == n_rows && index[2] == n_groups);
+  if (!index) return true;
+  const int magic = index[0], rows = index[1], groups = index[2];
+  return (magic == kGroupMagic) & (rows == n_rows) & (groups == n_groups);
 }
 
 // Tile t when every group's rows x deg go into tiles of `size`; false past the

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
   static_assert(TPR == 8 && NP == 4);
   __shared__ __bf16 s_x[PARTS][kTile][LD];
   __shared__ __bf16 s_w[PARTS][kTile][LD];
-  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
   int col_tile;
   if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
                      blockIdx.x - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
-                     col_tile))
+                     col_tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.x);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -291,13 +291,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
   static_assert(NP >= 1);
   __shared__ __bf16 s_x[PARTS][kStreamRows][LD];
   __shared__ int2 s_row[3][kStreamRows];  // row and component
-  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, chunk,
-                 int64_t(blockIdx.x) - blk.wg0, tile))
+                 int64_t(blockIdx.x) - blk.wg0, tile) || !valid)
     return;
   const int* order = a.index ? a.index + a.order + tile.first : nullptr;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -539,13 +539,13 @@ bool streams(const MixArgs& a, const MixList& l) {
 template <class T, bool WT>
 __global__ void __launch_bounds__(64) k_mix_few(const MixArgs a, const MixList l) {
   constexpr int PARTS = Chunk<T>::PARTS, VEC = 16 / sizeof(T), N = PARTS == 3 ? 4 : 8;
-  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   if (!find_tile(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, 16,
-                 int64_t(blockIdx.x) - blk.wg0, tile))
+                 int64_t(blockIdx.x) - blk.wg0, tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.x);
   const int lane = threadIdx.x, q = lane & 15, h = lane >> 4;
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
   static_assert(kThreads / CT * NP == BK);
   __shared__ __bf16 s_x[PARTS][kTile][LD];
   __shared__ __bf16 s_y[PARTS][kTile][LD];
-  if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   const int* offsets = a.index ? a.index + a.offsets : nullptr;
   const int pi = int(blockIdx.y);
   const MixPair p = l.p[pi];
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
   int64_t n;  // rows of this workgroup
   if (part_rows > 0) {
     if (!find_tile(offsets, a.n_groups, a.n_rows, p.deg, part_rows, slot, tile) ||
-        tile.group >= a.n_groups)
+        tile.group >= a.n_groups || !valid)
       return;
     n = min(part_rows, tile.rows - tile.at);
   } else {
@@ -697,6 +697,7 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
     const int64_t lo = offsets ? offsets[g] : 0, hi = offsets ? offsets[g + 1] : a.n_rows;
     tile = {g, lo, (hi - lo) * p.deg, 0};
     n = tile.rows;
+    if (!valid) return;
   }
   const int* order = a.index ? a.index + a.order + tile.first : nullptr;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
