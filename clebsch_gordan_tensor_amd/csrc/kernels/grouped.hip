@@ -27,6 +27,7 @@
 #include "group_tiles.h"
 #include "registry.h"
 #include "row_halves.h"
+#include "tile128.h"
 
 namespace e3k {
 namespace {
@@ -265,6 +266,122 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
         }
         if (n < a.cout) *reinterpret_cast<bf16x8*>(y + n) = v;
       }
+    }
+  }
+}
+
+// bf16 with W transposed, where both operands lie along k in memory: chunks of
+// 64 k go straight to LDS, one is multiplied while the next is on its way; two
+// workgroups on a compute unit.
+__global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, const MixList l) {
+  // a name for every stage: reads of one are then known not to wait for loads
+  // into the other
+  __shared__ __attribute__((aligned(128))) uint8_t s_x0[TileLoad::kBytes], s_w0[TileLoad::kBytes];
+  __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_w1[TileLoad::kBytes];
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
+  int bi = 0;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  const MixBlock blk = l.blk[bi];
+  GroupTile tile;
+  int col_tile;
+  if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
+                     blockIdx.x - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
+                     col_tile) || !valid)
+    return;
+  const RowOrder order(a.index, a.order, tile, a.x);
+  const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
+  const TileLoad load;
+  const int wm = load.wave & 1, wn = load.wave >> 1, col0 = col_tile * kTile;
+  const int n_rows = int(min(int64_t(kTile), tile.rows - tile.at));
+  const TileRows rows(tile.at, blk.deg);
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+  // the rows this lane loads, and those it ends with; rows past the end are
+  // the last one again, and so are columns
+  int load_row[4], load_m[4], row[4], comp[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    load_row[j] = order(rows.place(min(load.row + j * 32, n_rows - 1), load_m[j]));
+    row[j] = order(rows.place(min(wm * 64 + j * 16 + q, n_rows - 1), comp[j]));
+  }
+  const uint8_t *xrow[4], *wrow[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    xrow[j] = static_cast<const uint8_t*>(a.x) +
+              ((int64_t(load_row[j]) * a.din + load_m[j]) * a.cin + load.piece * 8) * 2;
+    // slot s of the columns holds column 8 (s >> 2 & 3) + 4 (s >> 4 & 1) + (s & 3) of its 32
+    const int s = load.row + j * 32;
+    const int n = min(col0 + ((s & ~31) | ((s >> 2) & 3) << 3 | ((s >> 4) & 1) << 2 | (s & 3)),
+                      a.cout - 1);
+    wrow[j] = static_cast<const uint8_t*>(a.W) +
+              ((int64_t(tile.group) * a.pairs * a.cout + n) * a.cin + load.piece * 8) * 2;
+  }
+  const int chunks = (a.cin + 63) / 64;
+  const int steps = tile.group < a.n_groups ? blk.n_src * chunks : 0;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
+  int64_t xo = 0, wo = 0;  // bytes to the chunk asked for next
+  int src = -1, b = chunks - 1;
+  const auto fetch = [&](uint8_t* x, uint8_t* w) {
+    if (b + 1 < chunks) {  // past the last chunk it is asked for again
+      ++b;
+      xo += 128;
+      wo += 128;
+    } else if (src + 1 < blk.n_src) {
+      const MixSource sc = l.src[blk.src0 + ++src];
+      b = 0;
+      xo = int64_t(sc.in_off) * a.cin * 2;
+      wo = int64_t(sc.pair) * a.cout * a.cin * 2;
+    }
+    const bool in = b * 64 + load.piece * 8 < a.cin;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load.ask(in ? xrow[j] + xo : zeros, x, j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load.ask(in ? wrow[j] + wo : zeros, w, j);
+  };
+  const auto turn = [&](const uint8_t* x, const uint8_t* w, uint8_t* x_free, uint8_t* w_free,
+                        int step) {
+    tile_wait();
+    fetch(x_free, w_free);
+    if (step >= steps) return;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 xf[4][1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        xf[j][0] = *reinterpret_cast<const bf16x8*>(tile_at(x, wm * 64 + j * 16 + q, kk * 4 + h));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8 wf[1][1] = {
+            {*reinterpret_cast<const bf16x8*>(tile_at(w, wn * 64 + i * 16 + q, kk * 4 + h))}};
+        products<1, 1, 4>(wf, xf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
+      }
+    }
+  };
+  if (steps > 0) fetch(s_x0, s_w0);
+  for (int step = 0; step < steps; step += 2) {
+    turn(s_x0, s_w0, s_x1, s_w1, step);
+    turn(s_x1, s_w1, s_x0, s_w0, step + 1);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load writes to LDS after the end
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (wm * 64 + j * 16 + q >= n_rows) continue;
+    bf16_t* y = static_cast<bf16_t*>(a.y) +
+                (int64_t(row[j]) * a.dout + blk.out_off + comp[j]) * a.cout;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const int n = col0 + wn * 64 + i * 16 + h * 8;
+      bf16x8 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = __bf16(acc[i][j][e]);
+        v[4 + e] = __bf16(acc[i + 1][j][e]);
+      }
+      if (n < a.cout) *reinterpret_cast<bf16x8*>(y + n) = v;
     }
   }
 }
@@ -640,8 +757,13 @@ hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
     if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
   }
   const dim3 grid{unsigned(wgs)};
-  if (a.w_trans) hipLaunchKernelGGL((k_mix<T, true>), grid, dim3(kThreads), 0, s, a, l);
-  else hipLaunchKernelGGL((k_mix<T, false>), grid, dim3(kThreads), 0, s, a, l);
+  if constexpr (sizeof(T) == 2) {
+    if (a.w_trans) hipLaunchKernelGGL(k_mix_along, grid, dim3(kThreads), 0, s, a, l);
+    else hipLaunchKernelGGL((k_mix<T, false>), grid, dim3(kThreads), 0, s, a, l);
+  } else {
+    if (a.w_trans) hipLaunchKernelGGL((k_mix<T, true>), grid, dim3(kThreads), 0, s, a, l);
+    else hipLaunchKernelGGL((k_mix<T, false>), grid, dim3(kThreads), 0, s, a, l);
+  }
   return hipGetLastError();
 }
 
