@@ -42,19 +42,26 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256;   // 4 wavefronts, 64 x 64 of the tile each
 constexpr int kTile = 128;      // rows and columns of a workgroup's tile
 
-// Chunk of the contraction in LDS, parts of an operand; rows are padded by 16
-// bytes, so that the 16-byte reads of 16 lanes in consecutive rows meet every
-// bank once.
+// Chunk of the contraction in LDS, parts of an operand.
 template <class T>
 struct Chunk;
 template <>
 struct Chunk<float> {
-  static constexpr int K = 32, PARTS = 3, LD = 40;
+  static constexpr int K = 32, PARTS = 3;
 };
 template <>
 struct Chunk<bf16_t> {
-  static constexpr int K = 64, PARTS = 1, LD = 72;
+  static constexpr int K = 64, PARTS = 1;
 };
+
+// Where 16 bytes (8 values) `piece` of row r of K values lie in LDS, in values:
+// the pieces of 8 consecutive rows (K = 32: of 8 rows, two a 128-byte line) are
+// exchanged so that reads of one piece of 16 rows meet every bank alike.
+// (Padded rows left half of the LDS cycles to conflicts.)
+template <int K>
+__device__ __forceinline__ int lds_at(int r, int piece) {
+  return r * K + ((piece ^ (K >= 64 ? r & 7 : (r >> 1) & 3)) << 3);
+}
 
 // Parts of 4 consecutive values.
 __device__ __forceinline__ void split3(const f32x4 v, bf16x4 (&p)[3]) {
@@ -95,14 +102,13 @@ __device__ __forceinline__ int column_slot(int n) {
 
 template <class T, bool WT>
 __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList l) {
-  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS, LD = Chunk<T>::LD;
+  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS;
   constexpr int VEC = 16 / sizeof(T);     // elements of a 16-byte load
   constexpr int TPR = BK / VEC;           // threads of a row of a chunk: 8
   constexpr int PASS = kThreads / TPR;    // rows of a pass: 32
   constexpr int NP = kTile / PASS;        // passes: 4
   static_assert(TPR == 8 && NP == 4);
-  __shared__ __bf16 s_x[PARTS][kTile][LD];
-  __shared__ __bf16 s_w[PARTS][kTile][LD];
+  __shared__ __attribute__((aligned(16))) __bf16 s_x[PARTS][kTile * BK], s_w[PARTS][kTile * BK];
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
@@ -173,14 +179,15 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
     }
   };
   // 16 bytes along k into row r of an operand in LDS
-  const auto stage_row = [&](__bf16 (&s)[PARTS][kTile][LD], int r, u32x4 v) {
+  const auto stage_row = [&](__bf16 (&s)[PARTS][kTile * BK], int r, u32x4 v) {
+    const int at = lds_at<BK>(r, piece * VEC / 8) + piece * VEC % 8;
     if constexpr (PARTS == 3) {
       bf16x4 p[3];
       split3(__builtin_bit_cast(f32x4, v), p);
 #pragma unroll
-      for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s[t][r][piece * VEC]) = p[t];
+      for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s[t][at]) = p[t];
     } else {
-      *reinterpret_cast<u32x4*>(&s[0][r][piece * VEC]) = v;
+      *reinterpret_cast<u32x4*>(&s[0][at]) = v;
     }
   };
   const auto stage = [&]() {
@@ -202,7 +209,8 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
           split3(v, p);
 #pragma unroll
           for (int t = 0; t < 3; ++t)
-            *reinterpret_cast<bf16x4*>(&s_w[t][column_slot<T>(n + e)][k]) = p[t];
+            *reinterpret_cast<bf16x4*>(
+                &s_w[t][lds_at<BK>(column_slot<T>(n + e), k / 8) + k % 8]) = p[t];
         }
       } else {
 #pragma unroll
@@ -210,7 +218,8 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
           bf16x4 v;
 #pragma unroll
           for (int j = 0; j < NP; ++j) v[j] = __builtin_bit_cast(bf16x8, wv[j])[e];
-          *reinterpret_cast<bf16x4*>(&s_w[0][column_slot<T>(n + e)][k]) = v;
+          *reinterpret_cast<bf16x4*>(
+              &s_w[0][lds_at<BK>(column_slot<T>(n + e), k / 8) + k % 8]) = v;
         }
       }
     }
@@ -231,14 +240,14 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
 #pragma unroll
         for (int t = 0; t < PARTS; ++t)
           xf[j][t] = *reinterpret_cast<const bf16x8*>(
-              &s_x[t][wm * 64 + j * 16 + q][kk * 32 + h * 8]);
+              &s_x[t][lds_at<BK>(wm * 64 + j * 16 + q, kk * 4 + h)]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         bf16x8 wf[1][PARTS];
 #pragma unroll
         for (int t = 0; t < PARTS; ++t)
           wf[0][t] = *reinterpret_cast<const bf16x8*>(
-              &s_w[t][wn * 64 + i * 16 + q][kk * 32 + h * 8]);
+              &s_w[t][lds_at<BK>(wn * 64 + i * 16 + q, kk * 4 + h)]);
         products<PARTS, 1, 4>(wf, xf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
       }
     }
@@ -402,11 +411,11 @@ constexpr int kStreamRows = 64;
 template <class T, bool WT, int NK, int CW, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, const MixList l,
                                                             int chunk) {
-  constexpr int PARTS = Chunk<T>::PARTS, K = 32 * NK, LD = K + 8;
+  constexpr int PARTS = Chunk<T>::PARTS, K = 32 * NK;
   constexpr int VEC = 16 / sizeof(T), TPR = K / VEC, PASS = kThreads / TPR;
   constexpr int NP = kStreamRows / PASS, RT = CW;  // row tiles of a wavefront
   static_assert(NP >= 1);
-  __shared__ __bf16 s_x[PARTS][kStreamRows][LD];
+  __shared__ __attribute__((aligned(16))) __bf16 s_x[PARTS][kStreamRows * K];
   __shared__ int2 s_row[3][kStreamRows];  // row and component
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   int bi = 0;
@@ -542,13 +551,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
     for (int j = 0; j < NP; ++j) {
       const int r = r0 + j * PASS;
       const u32x4 v = in ? xv[j] : u32x4{};
+      const int to = lds_at<K>(r, piece * VEC / 8) + piece * VEC % 8;
       if constexpr (PARTS == 3) {
         bf16x4 p[3];
         split3(__builtin_bit_cast(f32x4, v), p);
 #pragma unroll
-        for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s_x[t][r][piece * VEC]) = p[t];
+        for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s_x[t][to]) = p[t];
       } else {
-        *reinterpret_cast<u32x4*>(&s_x[0][r][piece * VEC]) = v;
+        *reinterpret_cast<u32x4*>(&s_x[0][to]) = v;
       }
     }
     const int next = buf == 2 ? 0 : buf + 1, after = next == 2 ? 0 : next + 1;
@@ -567,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
 #pragma unroll
           for (int t = 0; t < PARTS; ++t)
             xf[b][t] = *reinterpret_cast<const bf16x8*>(
-                &s_x[t][(wm * RT + j * JB + b) * 16 + q][s * 32 + h * 8]);
+                &s_x[t][lds_at<K>((wm * RT + j * JB + b) * 16 + q, s * 4 + h)]);
         products<PARTS, 2, JB>(wf[s], xf, acc[j]);
       }
 #pragma unroll
@@ -792,11 +802,10 @@ int64_t dw_rows(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* 
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const MixDwList l,
                                                      int64_t part_rows, int slots) {
-  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS, LD = Chunk<T>::LD;
+  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS;
   constexpr int VEC = 16 / sizeof(T), CT = kTile / VEC, NP = 4;
   static_assert(kThreads / CT * NP == BK);
-  __shared__ __bf16 s_x[PARTS][kTile][LD];
-  __shared__ __bf16 s_y[PARTS][kTile][LD];
+  __shared__ __attribute__((aligned(16))) __bf16 s_x[PARTS][kTile * BK], s_y[PARTS][kTile * BK];
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   const int* offsets = a.index ? a.index + a.offsets : nullptr;
   const int pi = int(blockIdx.y);
@@ -874,7 +883,7 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
       }
     }
   };
-  const auto stage = [&](__bf16 (&s)[PARTS][kTile][LD], u32x4 (&v)[NP], bool in, int64_t left) {
+  const auto stage = [&](__bf16 (&s)[PARTS][kTile * BK], u32x4 (&v)[NP], bool in, int64_t left) {
 #pragma unroll
     for (int j = 0; j < NP; ++j)
       if (!in || k + j >= left) v[j] = u32x4{};
@@ -887,12 +896,13 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
         bf16x4 part[3];
         split3(t, part);
 #pragma unroll
-        for (int u = 0; u < 3; ++u) *reinterpret_cast<bf16x4*>(&s[u][e * CT + c][k]) = part[u];
+        for (int u = 0; u < 3; ++u)
+          *reinterpret_cast<bf16x4*>(&s[u][lds_at<BK>(e * CT + c, k / 8) + k % 8]) = part[u];
       } else {
         bf16x4 t;
 #pragma unroll
         for (int j = 0; j < NP; ++j) t[j] = __builtin_bit_cast(bf16x8, v[j])[e];
-        *reinterpret_cast<bf16x4*>(&s[0][e * CT + c][k]) = t;
+        *reinterpret_cast<bf16x4*>(&s[0][lds_at<BK>(e * CT + c, k / 8) + k % 8]) = t;
       }
     }
   };
@@ -927,13 +937,14 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
 #pragma unroll
         for (int t = 0; t < PARTS; ++t)
           yf[j][t] = *reinterpret_cast<const bf16x8*>(
-              &s_y[t][slot_of(wn, j, q)][kk * 32 + h * 8]);
+              &s_y[t][lds_at<BK>(slot_of(wn, j, q), kk * 4 + h)]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         bf16x8 xf[1][PARTS];
 #pragma unroll
         for (int t = 0; t < PARTS; ++t)
-          xf[0][t] = *reinterpret_cast<const bf16x8*>(&s_x[t][slot_of(wm, i, q)][kk * 32 + h * 8]);
+          xf[0][t] = *reinterpret_cast<const bf16x8*>(
+              &s_x[t][lds_at<BK>(slot_of(wm, i, q), kk * 4 + h)]);
         products<PARTS, 1, 4>(xf, yf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
       }
     }
