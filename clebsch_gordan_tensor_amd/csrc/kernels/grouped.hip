@@ -800,7 +800,7 @@ int64_t dw_rows(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* 
 // Channel of slot (e, c) of a tile: VEC c + e; slot = e (128 / VEC) + c, so
 // that neighbouring threads write neighbouring rows of LDS.
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const MixDwList l,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) k_mix_dw(const MixDwArgs a, const MixDwList l,
                                                      int64_t part_rows, int slots) {
   constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS;
   constexpr int VEC = 16 / sizeof(T), CT = kTile / VEC, NP = 4;
@@ -883,10 +883,13 @@ __global__ void __launch_bounds__(kThreads) k_mix_dw(const MixDwArgs a, const Mi
       }
     }
   };
+  const bool whole = a0 + kTile <= a.cin && b0 + kTile <= a.cout;
   const auto stage = [&](__bf16 (&s)[PARTS][kTile * BK], u32x4 (&v)[NP], bool in, int64_t left) {
+    if (!whole || left < BK) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
-      if (!in || k + j >= left) v[j] = u32x4{};
+      for (int j = 0; j < NP; ++j)
+        if (!in || k + j >= left) v[j] = u32x4{};
+    }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       if constexpr (PARTS == 3) {
