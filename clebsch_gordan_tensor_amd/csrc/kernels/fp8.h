@@ -19,27 +19,25 @@ __host__ __device__ constexpr int fp8_runs(int channels) {
   return (channels + kFp8Run - 1) / kFp8Run;
 }
 
-// The larger one; NaN where either is (fmaxf would drop it).
+// Largest |v|, as the largest of their bits: an infinity is above every finite
+// value there, and NaN above that.
 __device__ __forceinline__ float fp8_max(float a, float b) {
-  return fmaf(a, 0.0f, fmaf(b, 0.0f, fmaxf(a, b)));
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
 template <int V>
 __device__ __forceinline__ float fp8_top(const float (&v)[V]) {
-  float t = fabsf(v[0]), any = v[0];
+  uint32_t t = 0;
 #pragma unroll
-  for (int i = 1; i < V; ++i) {
-    t = fmaxf(t, fabsf(v[i]));
-    any = fmaf(v[i], 0.0f, any);
-  }
-  return fmaf(any, 0.0f, t);  // NaN where one of them is not finite
+  for (int i = 0; i < V; ++i) t = max(t, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return __uint_as_float(t);
 }
 
 struct Fp8Scale {
   float scale, inv;
-  // top: the run's largest |v|, NaN where one of its values is not finite
+  // top: the run's largest |v|
   __device__ __forceinline__ explicit Fp8Scale(float top) {
-    scale = top * kFp8Part;
-    if (scale < kFp8Least) scale = kFp8Least;  // (false for NaN)
+    scale = fmaxf(top * kFp8Part, kFp8Least);
+    if (!(top < __builtin_inff())) scale = __builtin_nanf("");
     inv = 1.0f / scale;
   }
   // v / scale rounded once: the product with the reciprocal, corrected by what
