@@ -2676,9 +2676,9 @@ std::vector<e3k::MixPair> mix_pairs(const Mix& m) {
   return p;
 }
 
-size_t mix_workspace(int64_t n_rows, int32_t n_groups, const Mix& m) {
+size_t mix_workspace(int64_t n_rows, const Mix& m) {
   const auto p = mix_pairs(m);
-  return 4 * e3k::mix_dw_part_floats(n_rows, n_groups, m.cin, m.cout, p.data(), int(p.size()));
+  return 4 * e3k::mix_dw_part_floats(n_rows, m.cin, m.cout, p.data(), int(p.size()));
 }
 
 }  // namespace
@@ -2692,7 +2692,7 @@ e3_status e3_linear_grouped_workspace_size(const e3_irreps* in, const e3_irreps*
         (s = parse_mix(in, out, n_rows, 8, m)) != E3_OK)
       return s;
     if (!bytes) return fail(E3_ERR_INVALID_ARG, "bytes is null");
-    *bytes = mix_workspace(n_rows, n_groups, m);
+    *bytes = mix_workspace(n_rows, m);
     return ok();
   });
 }
@@ -2712,7 +2712,7 @@ e3_status e3_linear_grouped_backward(const e3_irreps* in, const e3_irreps* out, 
     const bool pairs = !m.pairs.empty();
     if (n_rows > 0 && (!x || !dy || (dx && pairs && !W)))
       return fail(E3_ERR_INVALID_ARG, "null pointer");
-    const size_t need = dW ? mix_workspace(n_rows, n_groups, m) : 0;
+    const size_t need = dW ? mix_workspace(n_rows, m) : 0;
     if (need > 0 && (!workspace || ws_bytes < need))
       return fail(E3_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
     if (!aligned16(x) || !aligned16(W) || !aligned16(dy) || !aligned16(dx) || !aligned16(dW) ||

@@ -25,13 +25,14 @@ __device__ __forceinline__ bool index_matches(const int* index, int64_t n_rows, 
   return (magic == kGroupMagic) & (rows == n_rows) & (groups == n_groups);
 }
 
-// Tile t when every group's rows x deg go into tiles of `size`; false past the
-// last one.  A lane per group counts, the tile's group is found by a ballot.
+// Tile t when every group's rows x deg go into tiles of `size`, at least
+// `least` of them; false past the last one.  A lane per group counts, the
+// tile's group is found by a ballot.
 __device__ __forceinline__ bool find_tile(const int* offsets, int n_groups, int64_t n_rows, int deg,
-                                          int64_t size, int64_t t, GroupTile& tile) {
+                                          int64_t size, int64_t t, GroupTile& tile, int least = 0) {
   if (!offsets) {
     tile = {0, 0, n_rows * deg, t * size};
-    return tile.at < tile.rows;
+    return tile.at < tile.rows || t < least;
   }
   const int lane = threadIdx.x & 63;
   for (int g0 = 0; g0 <= n_groups; g0 += 64) {
@@ -41,7 +42,7 @@ __device__ __forceinline__ bool find_tile(const int* offsets, int n_groups, int6
       lo = offsets[g];
       hi = g < n_groups ? offsets[g + 1] : n_rows;
     }
-    const int n = int(((hi - lo) * deg + size - 1) / size);
+    const int n = g <= n_groups ? max(least, int(((hi - lo) * deg + size - 1) / size)) : 0;
     int s = n;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {

@@ -784,24 +784,47 @@ struct MixDwList {
   MixPair p[kMixSources];
 };
 
-// Rows of a workgroup's part of the sum, 0 for all of a group's at once (then
-// there are no partials): enough workgroups to fill the chip.
+// Rows of a workgroup's part of a group's sum.  Parts of a group that has
+// several are written to the workspace and added afterwards: enough of them to
+// fill the chip, but of so many rows that the parts are a quarter of what x and
+// dy are at most; the only part of a group goes straight to dW.  Where one
+// group's tiles fill the chip by themselves there are no parts.
 constexpr int kDwTarget = 1024;
-int64_t dw_rows(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* p, int n_pairs) {
+int64_t dw_rows(int64_t n_rows, int cin, int cout, const MixPair* p, int n_pairs, int esize) {
   const int64_t tiles = int64_t((cin + kTile - 1) / kTile) * ((cout + kTile - 1) / kTile);
+  if (tiles >= 256) return int64_t(1) << 40;
   int64_t comps = 0;
   for (int i = 0; i < n_pairs; ++i) comps += p[i].deg;
-  const int64_t want = kDwTarget / tiles;  // parts of the sums, all pairs together
-  const int64_t rows = n_rows * comps;     // rows of all pairs
-  if (want <= int64_t(n_groups) * n_pairs || rows <= 512 * int64_t(n_groups) * n_pairs) return 0;
-  return std::max<int64_t>(256, (rows / want + 63) / 64 * 64);
+  const int64_t least = int64_t(32) * cin * cout / (int64_t(cin + cout) * esize);
+  const int64_t rows = std::max(n_rows * comps * tiles / kDwTarget, std::max<int64_t>(256, least));
+  return (rows + 63) / 64 * 64;
+}
+// Most parts that groups with several can have together: each holds half of
+// `rows` at least on average.
+__host__ __device__ inline int64_t dw_parts(int64_t n_rows, int deg, int64_t rows) {
+  const int64_t n = n_rows * deg;
+  return n > rows ? 2 * n / rows : 0;
+}
+// Parts of the groups before group g that have several.
+__device__ __forceinline__ int parts_before(const int* offsets, int g, int deg, int64_t rows) {
+  int total = 0;
+  for (int g0 = 0; g0 < g; g0 += 64) {
+    const int i = g0 + int(threadIdx.x & 63);
+    int n = 0;
+    if (i < g) n = int((int64_t(offsets[i + 1] - offsets[i]) * deg + rows - 1) / rows);
+    n = n > 1 ? n : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
+    total += n;
+  }
+  return total;
 }
 
 // Channel of slot (e, c) of a tile: VEC c + e; slot = e (128 / VEC) + c, so
 // that neighbouring threads write neighbouring rows of LDS.
 template <class T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) k_mix_dw(const MixDwArgs a, const MixDwList l,
-                                                     int64_t part_rows, int slots) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    k_mix_dw(const MixDwArgs a, const MixDwList l, int64_t part_rows) {
   constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS;
   constexpr int VEC = 16 / sizeof(T), CT = kTile / VEC, NP = 4;
   static_assert(kThreads / CT * NP == BK);
@@ -817,19 +840,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) k_mix_dw(con
   if (tiles % 8 == 0) tile_of = tile_of % 8 * (tiles / 8) + tile_of / 8;
   const int slot = int(blockIdx.x) / tiles;
   GroupTile tile;
-  int64_t n;  // rows of this workgroup
-  if (part_rows > 0) {
-    if (!find_tile(offsets, a.n_groups, a.n_rows, p.deg, part_rows, slot, tile) ||
-        tile.group >= a.n_groups || !valid)
-      return;
-    n = min(part_rows, tile.rows - tile.at);
-  } else {
-    const int g = slot;
-    const int64_t lo = offsets ? offsets[g] : 0, hi = offsets ? offsets[g + 1] : a.n_rows;
-    tile = {g, lo, (hi - lo) * p.deg, 0};
-    n = tile.rows;
-    if (!valid) return;
-  }
+  if (!find_tile(offsets, a.n_groups, a.n_rows, p.deg, part_rows, slot, tile, 1) ||
+      tile.group >= a.n_groups || !valid)
+    return;
+  const int64_t n = min(part_rows, tile.rows - tile.at);  // rows of this workgroup
   const int* order = a.index ? a.index + a.order + tile.first : nullptr;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
@@ -954,9 +968,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) k_mix_dw(con
   }
 
   const int64_t size = int64_t(a.cin) * a.cout;
-  float* out = part_rows > 0
-                   ? a.part + (int64_t(pi) * slots + slot) * size
-                   : a.dW + (int64_t(tile.group) * a.pairs + pi) * size;
+  float* out = a.dW + (int64_t(tile.group) * a.pairs + pi) * size;
+  if (tile.rows > part_rows) {
+    int64_t at = tile.at / part_rows;
+    for (int i = 0; i < pi; ++i) at += dw_parts(a.n_rows, l.p[i].deg, part_rows);
+    if (offsets) at += parts_before(offsets, tile.group, p.deg, part_rows);
+    out = a.part + at * size;
+  }
   const int col = b0 + channel_of(wn, q);
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -971,62 +989,54 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) k_mix_dw(con
   }
 }
 
-// dW from the partials of every group, in their order: a workgroup per 1024
-// elements of a (group, pair).
+// dW of the groups with several parts, added in their order, 1024 elements of a
+// (group, pair) at a time; most groups may have nothing here, so that the
+// launch is of kSumTarget workgroups rather than of one for every 1024 elements
+// (16 groups of 1024 x 2048 without parts: 18 us and 4).
+constexpr int kSumTarget = 4096;
 __global__ void __launch_bounds__(256) k_mix_dw_sum(const MixDwArgs a, const MixDwList l,
-                                                    int64_t part_rows, int slots) {
+                                                    int64_t part_rows) {
   if (!index_matches(a.index, a.n_rows, a.n_groups)) return;
   const int g = int(blockIdx.y), pi = int(blockIdx.z), deg = l.p[pi].deg;
   const int64_t size = int64_t(a.cin) * a.cout;
-  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  // the group's first slot: tiles of the groups before it
-  __shared__ int s_first;
-  if (threadIdx.x == 0) s_first = 0;
-  __syncthreads();
-  const auto tiles = [&](int i) {
-    if (!a.index) return int((a.n_rows * deg + part_rows - 1) / part_rows);
-    const int* offsets = a.index + a.offsets;
-    return int((int64_t(offsets[i + 1] - offsets[i]) * deg + part_rows - 1) / part_rows);
-  };
-  int mine = 0;
-  for (int i = threadIdx.x; i < g; i += 256) mine += tiles(i);
-  if (mine) atomicAdd(&s_first, mine);
-  __syncthreads();
-  const int first = s_first, n = tiles(g);
-  if (e >= size) return;
-  const float* part = a.part + (int64_t(pi) * slots + first) * size + e;
-  f32x4 s{};
+  const int* offsets = a.index ? a.index + a.offsets : nullptr;
+  const int64_t rows = (offsets ? offsets[g + 1] - offsets[g] : a.n_rows) * deg;
+  const int n = int((rows + part_rows - 1) / part_rows);
+  if (n < 2) return;
+  int64_t at = offsets ? parts_before(offsets, g, deg, part_rows) : 0;
+  for (int i = 0; i < pi; ++i) at += dw_parts(a.n_rows, l.p[i].deg, part_rows);
+  const float* part = a.part + at * size;
+  float* dW = a.dW + (int64_t(g) * a.pairs + pi) * size;
+  const int64_t step = int64_t(gridDim.x) * 1024;
+  for (int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; e < size; e += step) {
+    f32x4 s{};
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) s += *reinterpret_cast<const f32x4*>(part + i * size);
-  *reinterpret_cast<f32x4*>(a.dW + (int64_t(g) * a.pairs + pi) * size + e) = s;
-}
-
-int dw_slots(int64_t n_rows, int n_groups, int64_t rows, const MixPair* p, int n_pairs,
-             bool grouped) {
-  int64_t most = 0;
-  for (int i = 0; i < n_pairs; ++i)
-    most = std::max(most, most_tiles(n_rows, n_groups, p[i].deg, rows, grouped));
-  return int(most);
+    for (int i = 0; i < n; ++i) s += *reinterpret_cast<const f32x4*>(part + i * size + e);
+    *reinterpret_cast<f32x4*>(dW + e) = s;
+  }
 }
 
 template <class T>
 hipError_t launch_mix_dw_t(const MixDwArgs& a, const MixPair* p, hipStream_t s) {
   MixDwList l;
   l.n_pairs = a.pairs;
-  for (int i = 0; i < a.pairs; ++i) l.p[i] = p[i];
-  const int64_t rows = dw_rows(a.n_rows, a.n_groups, a.cin, a.cout, p, a.pairs);
-  const int slots = rows > 0 ? dw_slots(a.n_rows, a.n_groups, rows, p, a.pairs, a.index != nullptr)
-                             : a.n_groups;
-  const unsigned tiles = unsigned((a.cin + kTile - 1) / kTile) *
-                         unsigned((a.cout + kTile - 1) / kTile);
-  hipLaunchKernelGGL((k_mix_dw<T>), dim3(unsigned(slots) * tiles, unsigned(a.pairs)),
-                     dim3(kThreads), 0, s, a, l, rows, slots);
+  int deg = 1;
+  for (int i = 0; i < a.pairs; ++i) {
+    l.p[i] = p[i];
+    deg = std::max(deg, p[i].deg);
+  }
+  const int64_t rows = dw_rows(a.n_rows, a.cin, a.cout, p, a.pairs, sizeof(T));
+  const int64_t slots = most_tiles(a.n_rows, a.n_groups, deg, rows, true) + 1;
+  const int64_t tiles = int64_t((a.cin + kTile - 1) / kTile) * ((a.cout + kTile - 1) / kTile);
+  hipLaunchKernelGGL((k_mix_dw<T>), dim3(unsigned(slots * tiles), unsigned(a.pairs)),
+                     dim3(kThreads), 0, s, a, l, rows);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || rows == 0) return e;
+  if (e != hipSuccess || a.n_rows * deg <= rows) return e;
+  const int64_t runs = std::min((int64_t(a.cin) * a.cout + 1023) / 1024,
+                                kSumTarget / (int64_t(a.n_groups) * a.pairs) + 1);
   hipLaunchKernelGGL(k_mix_dw_sum,
-                     dim3(unsigned((int64_t(a.cin) * a.cout + 1023) / 1024),
-                          unsigned(a.n_groups), unsigned(a.pairs)),
-                     dim3(256), 0, s, a, l, rows, slots);
+                     dim3(unsigned(runs), unsigned(a.n_groups), unsigned(a.pairs)), dim3(256), 0, s,
+                     a, l, rows);
   return hipGetLastError();
 }
 
@@ -1036,11 +1046,15 @@ hipError_t launch_mix(const MixArgs& a, const MixList& l, int bf16, hipStream_t 
   return bf16 ? launch_mix_t<bf16_t>(a, l, s) : launch_mix_t<float>(a, l, s);
 }
 
-size_t mix_dw_part_floats(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* p,
-                          int n_pairs) {
-  const int64_t rows = dw_rows(n_rows, n_groups, cin, cout, p, n_pairs);
-  if (rows == 0) return 0;
-  return size_t(dw_slots(n_rows, n_groups, rows, p, n_pairs, true)) * n_pairs * cin * cout;
+size_t mix_dw_part_floats(int64_t n_rows, int cin, int cout, const MixPair* p, int n_pairs) {
+  int64_t most = 0;  // for either storage type
+  for (int esize : {2, 4}) {
+    const int64_t rows = dw_rows(n_rows, cin, cout, p, n_pairs, esize);
+    int64_t parts = 0;
+    for (int i = 0; i < n_pairs; ++i) parts += dw_parts(n_rows, p[i].deg, rows);
+    most = std::max(most, parts);
+  }
+  return size_t(most) * cin * cout;
 }
 
 hipError_t launch_mix_dw(const MixDwArgs& a, const MixPair* p, int bf16, hipStream_t s) {

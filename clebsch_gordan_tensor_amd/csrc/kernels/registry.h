@@ -518,8 +518,7 @@ struct MixDwArgs {
 struct MixPair {
   int in_off, out_off, deg;
 };
-size_t mix_dw_part_floats(int64_t n_rows, int n_groups, int cin, int cout, const MixPair* p,
-                          int n_pairs);
+size_t mix_dw_part_floats(int64_t n_rows, int cin, int cout, const MixPair* p, int n_pairs);
 hipError_t launch_mix_dw(const MixDwArgs& a, const MixPair* p, int bf16, hipStream_t s);
 
 // 8-bit features and weights (fp8.hip).  Packed weights: a header of 64 bytes

@@ -1,0 +1,173 @@
+"""The channel mixing by group where its work is split another way: one group
+with most of the rows, more groups than a wavefront has lanes, wide and ragged
+channels, sums over many blocks, and the operators run together, against their
+64-bit forms (tests/grouped_reference.py)."""
+import numpy as np
+import pytest
+
+from clebsch_gordan_tensor_amd import synth as S
+from tests import grouped_reference as R
+from tests import norm_reference as N
+from tests.gpu_util import dev, host
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible to torch")
+    from clebsch_gordan_tensor_amd import api
+    api.lib()
+    return api
+
+
+def _ir(s):
+    return S.parse_irreps(s)[1]
+
+
+def _case(into, out, group, groups, cin, cout, dtype="f32", seed=0):
+    rng = np.random.default_rng(len(group) + 13 * groups + cin + cout + seed)
+    x = rng.standard_normal((len(group), S.dim(into), cin)).astype(np.float32)
+    W = (rng.standard_normal((groups, len(R.pairs(into, out)), cin, cout)) /
+         np.sqrt(cin)).astype(np.float32)
+    dy = rng.standard_normal((len(group), S.dim(out), cout)).astype(np.float32)
+    return [S.round_bf16(t) if dtype == "bf16" else t for t in (x, W, dy)]
+
+
+def _skewed(rows, groups, share, seed=0):
+    """A share of the rows in one group, the rest evenly; the last group has
+    none and a few rows are in no group."""
+    rng = np.random.default_rng(rows + groups + seed)
+    g = rng.integers(0, max(groups - 1, 1), rows).astype(np.int32)
+    g[rng.random(rows) < share] = groups // 2 if groups > 2 else 0
+    g[rng.random(rows) < 0.02] = -1
+    return g
+
+
+def _check(gpu, into, out, group, x, W, dy, dtype):
+    groups, bf16 = W.shape[0], dtype == "bf16"
+    index = gpu.group_rows(dev(group), groups)
+    X, Wd, D = dev(x, dtype), dev(W, dtype), dev(dy, dtype)
+    y = gpu.linear_grouped(into, out, index, X, Wd)
+    R.check(host(y), R.mix(into, out, group, x, W), "y", bf16)
+    dx, dW = gpu.linear_grouped_backward(into, out, index, X, Wd, D, dW=torch.full(
+        W.shape, np.nan, device="cuda"))
+    rx, rW = R.mix_backward(into, out, group, x, W, dy)
+    R.check(host(dx), rx, "dx", bf16)
+    R.check(host(dW), rW, "dW")
+
+
+# a group alone in parts; all of them; none; a part's rows and one more or less
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("xs,os_,rows,groups,share,cin,cout", [
+    ("0e+1o+2e+3o", "0e+1o", 6000, 41, 0.3, 40, 16), ("0e+1o", "0e+1o", 9000, 3, 0.9, 16, 24),
+    ("0e+0e", "0e", 5000, 70, 0.5, 8, 136), ("0e", "0e", 257, 2, 1.0, 16, 16),
+    ("0e", "0e", 256, 1, 1.0, 16, 16), ("1o", "1o", 2000, 200, 0.2, 24, 16),
+    ("0e", "0e", 4000, 4, 0.8, 264, 392), ("2e+0e", "0e+2e", 1300, 2, 0.6, 128, 128),
+    ("0e", "0e", 700, 5, 0.7, 1992, 2040)])
+def test_groups_of_other_lengths(gpu, xs, os_, rows, groups, share, cin, cout, dtype):
+    into, out = _ir(xs), _ir(os_)
+    group = _skewed(rows, groups, share)
+    _check(gpu, into, out, group, *_case(into, out, group, groups, cin, cout, dtype), dtype)
+
+
+# tiled products with more groups than the lanes that look for a tile
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("xs,os_,rows,groups,cin,cout", [
+    ("0e", "0e", 3000, 65, 264, 136), ("0e+1o+0e", "1o+0e", 2500, 130, 72, 40),
+    ("0e", "0e", 2300, 64, 512, 384), ("0e+0e+0e", "0e", 1500, 20, 328, 520),
+    ("0e+1o", "0e+1o", 5000, 200, 128, 128)])
+def test_many_groups(gpu, xs, os_, rows, groups, cin, cout, dtype):
+    into, out = _ir(xs), _ir(os_)
+    group = _skewed(rows, groups, 0.1)
+    _check(gpu, into, out, group, *_case(into, out, group, groups, cin, cout, dtype), dtype)
+
+
+# both sides of the rows at which the tiles of few rows give way to the large
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [127, 128, 129, 143, 144, 145])
+def test_around_few_rows(gpu, rows, dtype):
+    into = out = _ir("0e")
+    for groups in (1, 2):
+        group = _skewed(rows, groups, 0.5)
+        _check(gpu, into, out, group, *_case(into, out, group, groups, 200, 264, dtype), dtype)
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("xs,os_,rows,groups,cin,cout", [
+    ("0e", "0e", 200, 1, 4096, 144), ("0e", "0e", 300, 3, 2064, 160), ("0e", "0e", 5, 1, 8192, 48),
+    ("0e+0e+0e", "0e", 400, 2, 912, 128), ("0e+1o+0e", "1o+0e", 900, 130, 80, 48),
+    ("0e", "0e", 2500, 70, 272, 400), ("0e+1o", "0e+1o", 2000, 100, 128, 128)])
+def test_mixing_in_8_bits(gpu, xs, os_, rows, groups, cin, cout, out_dtype):
+    into, out = _ir(xs), _ir(os_)
+    group = _skewed(rows, groups, 0.2) if groups > 1 else np.zeros(rows, np.int32)
+    x, W, _ = _case(into, out, group, groups, cin, cout)
+    index = gpu.group_rows(dev(group), groups) if groups > 1 else None
+    q, scale = gpu.quantize_fp8(dev(x))
+    y = gpu.linear_fp8(into, out, q, scale, gpu.linear_fp8_pack(into, out, dev(W)), index=index,
+                       dtype=torch.float32 if out_dtype == "f32" else None)
+    xv = R.values(host(q.float()).astype(np.float64), host(scale))
+    ref = R.mix(into, out, group, xv, R.weight_values(*R.quantize_weights(W)))
+    bf16 = out_dtype == "bf16"
+    R.check(host(y), ref, "y", bf16, adds=1, drops=R.EIGHTS if bf16 else 0.0)
+
+
+def _train(gpu, ir, groups, X, Rd, Wn, B, W, Gd, dY, dH, stream=None):
+    """A layer's pass: h = x + r normalised and mixed by element, then back."""
+    index = gpu.group_rows(Gd, groups, stream=stream)
+    n, h = gpu.layer_norm_residual(ir, X, Rd, Wn, B, stream=stream)
+    y = gpu.linear_grouped(ir, ir, index, n, W, stream=stream)
+    dn, dW = gpu.linear_grouped_backward(ir, ir, index, n, W, dY, stream=stream)
+    dx, dw, db = gpu.layer_norm_residual_backward(ir, h, Wn, dn, dH, stream=stream)
+    return y, h, n, dn, dW, dx, dw, db
+
+
+def _layer(rows, groups, C, seed=0):
+    ir = _ir("0e+1o+2e")
+    group = _skewed(rows, groups, 0.4, seed)
+    x, W, dy = _case(ir, ir, group, groups, C, C, seed=seed)
+    rng = np.random.default_rng(seed + 5)
+    r, dh = rng.standard_normal((2, *x.shape)).astype(np.float32)
+    wn = (1 + 0.2 * rng.standard_normal((3, C))).astype(np.float32)
+    b = rng.standard_normal((1, C)).astype(np.float32)
+    return ir, group, x, W, dy, r, dh, wn, b
+
+
+def test_a_layer_and_its_gradients(gpu):
+    ir, group, x, W, dy, r, dh, wn, b = _layer(1500, 4, 64)
+    got = _train(gpu, ir, 4, *map(dev, (x, r, wn, b, W, group, dy, dh)))
+    y, h, n, dn, dW, dx, dw, db = map(host, got)
+    # every step against its plain form on what the step before gave
+    assert np.array_equal(h, x + r)
+    ref, tol = N.norm_forward(ir, h, wn, b, 1e-5)
+    assert np.all(np.abs(n - ref) <= tol)
+    R.check(y, R.mix(ir, ir, group, n, W), "y")
+    rx, rW = R.mix_backward(ir, ir, group, n, W, dy)
+    R.check(dn, rx, "dn")
+    R.check(dW, rW, "dW")
+    (gx, gw, gb), (tx, tw, tb) = N.norm_backward(ir, h, wn, dn, 1e-5)
+    assert np.all(np.abs(dx - (gx + dh)) <= tx + R.U * np.abs(gx + dh))
+    assert np.all(np.abs(dw - gw) <= tw) and np.all(np.abs(db - gb) <= tb)
+
+
+def test_layers_on_two_streams(gpu):
+    # two passes at once, each with its own memory: what each gives alone
+    cases = [_layer(n, 5, 64, seed) for n, seed in ((3000, 1), (4100, 2))]
+    args = [(ir, 5, *map(dev, (x, r, wn, b, W, group, dy, dh)))
+            for ir, group, x, W, dy, r, dh, wn, b in cases]
+    alone = [_train(gpu, *a) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        both = []
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                both.append(_train(gpu, *a, stream=s))
+        torch.cuda.synchronize()
+        for one, two in zip(alone, both):
+            for p, q in zip(one, two):
+                assert torch.equal(p, q)
