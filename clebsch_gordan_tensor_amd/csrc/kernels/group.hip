@@ -170,8 +170,7 @@ __global__ void __launch_bounds__(kThreads) k_group_place(const GroupArgs a) {
     key[j] = r < a.n_rows ? key_of(a.group, r, G) : -1;
   }
   for (int g = tid; g <= G; g += kThreads) {
-    s_start[g] = FEW ? 0 : a.total[g];
-    if (FEW) s_before[g] = 0;
+    if (!FEW) s_start[g] = a.total[g];
     for (int j = 0; j < kWaves; ++j) s_at[j][g] = 0;
   }
   __syncthreads();
@@ -182,12 +181,25 @@ __global__ void __launch_bounds__(kThreads) k_group_place(const GroupArgs a) {
     count_same(s_at[w], key[j], same[j]);
   }
   if constexpr (FEW) {
-    const int n = (G + 1) * a.n_chunks;
-    for (int i = tid; i < n; i += kThreads) {
-      const int g = i / a.n_chunks, v = a.hist[i];
-      if (v) {
-        atomicAdd(s_start + g, v);
-        if (i - g * a.n_chunks < int(blockIdx.x)) atomicAdd(s_before + g, v);
+    // a power of two of lanes for a group
+    int log = 0;
+    while (log < 6 && (1 << log) < a.n_chunks) ++log;
+    const int lanes = 1 << log, mine = tid & (lanes - 1);
+    for (int g = tid >> log; g <= G; g += kThreads >> log) {
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int c = mine; c < a.n_chunks; c += lanes) {
+        const int v = a.hist[int64_t(g) * a.n_chunks + c];
+        all += v;
+        before += c < int(blockIdx.x) ? v : 0;
+      }
+      for (int o = lanes >> 1; o; o >>= 1) {
+        all += __shfl_xor(all, o);
+        before += __shfl_xor(before, o);
+      }
+      if (mine == 0) {
+        s_start[g] = all;
+        s_before[g] = before;
       }
     }
     __syncthreads();
