@@ -34,25 +34,14 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;   // 4 wavefronts, 64 x 64 of the tile each
 constexpr int kTile = 128;      // rows and columns of a workgroup's tile
 
-// Chunk of the contraction in LDS, parts of an operand.
 template <class T>
-struct Chunk;
-template <>
-struct Chunk<float> {
-  static constexpr int K = 32, PARTS = 3;
-};
-template <>
-struct Chunk<bf16_t> {
-  static constexpr int K = 64, PARTS = 1;
-};
+constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of an operand
 
 // Where 16 bytes (8 values) `piece` of row r of K values lie in LDS, in values:
 // the pieces of 8 consecutive rows (K = 32: of 8 rows, two a 128-byte line) are
@@ -91,24 +80,15 @@ __device__ __forceinline__ void products(const bf16x8 (&a)[M][PARTS], const bf16
 
 // ------------------------------------------------------------ the mixing
 
-// Where column n of a tile lies in LDS: for bf16 results the columns of two
-// 16-column products alternate by fours, so that a lane's 4 + 4 results are 8
-// consecutive columns (16 bytes).
-template <class T>
-__device__ __forceinline__ int column_slot(int n) {
-  if constexpr (std::is_same_v<T, float>) return n;
-  else return (n & ~31) | ((n >> 2) & 1) << 4 | ((n >> 3) & 3) << 2 | (n & 3);
-}
-
-template <class T, bool WT>
+// float32: chunks of 32 k pass through registers, where they are split, to LDS;
+// the next chunk is on its way meanwhile.
+template <bool WT>
 __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList l) {
-  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS;
-  constexpr int VEC = 16 / sizeof(T);     // elements of a 16-byte load
-  constexpr int TPR = BK / VEC;           // threads of a row of a chunk: 8
+  constexpr int BK = 32;
+  constexpr int TPR = BK / 4;             // threads of a row of a chunk, 4 values each
   constexpr int PASS = kThreads / TPR;    // rows of a pass: 32
-  constexpr int NP = kTile / PASS;        // passes: 4
-  static_assert(TPR == 8 && NP == 4);
-  __shared__ __attribute__((aligned(16))) __bf16 s_x[PARTS][kTile * BK], s_w[PARTS][kTile * BK];
+  constexpr int CT = kTile / 4;           // threads of a row of W
+  __shared__ __attribute__((aligned(16))) __bf16 s_x[3][kTile * BK], s_w[3][kTile * BK];
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
@@ -132,96 +112,69 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
 
-  // the rows this thread stages, and its 16 bytes of them; the rows this lane
+  // the rows this thread stages, and its 4 values of them; the rows this lane
   // ends with
   const int piece = tid % TPR, r0 = tid / TPR;
-  const T* xrow[NP];
-  int load_row[NP], load_m[NP], row[4], comp[4];
+  const float* xrow[4];
+  int load_row[4], load_m[4], row[4], comp[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     load_row[j] = order(rows.place(min(r0 + j * PASS, n_rows - 1), load_m[j]));
     row[j] = order(rows.place(min(wm * 64 + j * 16 + q, n_rows - 1), comp[j]));
   }
 #pragma unroll
-  for (int j = 0; j < NP; ++j)
-    xrow[j] = static_cast<const T*>(a.x) + (int64_t(load_row[j]) * a.din + load_m[j]) * a.cin +
-              piece * VEC;
+  for (int j = 0; j < 4; ++j)
+    xrow[j] = static_cast<const float*>(a.x) +
+              (int64_t(load_row[j]) * a.din + load_m[j]) * a.cin + piece * 4;
   const int n_src = tile.group < a.n_groups ? blk.n_src : 0;
   const int chunks = (a.cin + BK - 1) / BK;
-  const T* W0 = static_cast<const T*>(a.W) + int64_t(tile.group) * a.pairs * a.cin * a.cout;
+  const float* W0 = static_cast<const float*>(a.W) + int64_t(tile.group) * a.pairs * a.cin * a.cout;
 
-  u32x4 xv[NP], wv[NP];
+  f32x4 xv[4], wv[4];
   const auto fetch = [&](int step) {
     const int src = step / chunks, k0 = (step - src * chunks) * BK;
     const MixSource sc = l.src[blk.src0 + src];
-    const T* W = W0 + int64_t(sc.pair) * a.cin * a.cout;
-    const bool in = k0 + piece * VEC < a.cin;
+    const float* W = W0 + int64_t(sc.pair) * a.cin * a.cout;
+    const bool in = k0 + piece * 4 < a.cin;
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
-      xv[j] = in
-                  ? *reinterpret_cast<const u32x4*>(xrow[j] + int64_t(sc.in_off) * a.cin + k0)
-                  : u32x4{};
+    for (int j = 0; j < 4; ++j)
+      xv[j] = in ? *reinterpret_cast<const f32x4*>(xrow[j] + int64_t(sc.in_off) * a.cin + k0)
+                 : f32x4{};
     if constexpr (WT) {  // rows of W are columns here, k along them
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int n = col0 + r0 + j * PASS;
-        wv[j] = n < a.cout && in ? *reinterpret_cast<const u32x4*>(W + int64_t(n) * a.cin + k0 + piece * VEC)
-                                 : u32x4{};
+        wv[j] = n < a.cout && in
+                    ? *reinterpret_cast<const f32x4*>(W + int64_t(n) * a.cin + k0 + piece * 4)
+                    : f32x4{};
       }
-    } else {  // VEC columns of NP consecutive k
-      constexpr int CT = kTile / VEC;  // threads of a row of W
-      const int n = col0 + tid % CT * VEC, k = k0 + tid / CT * NP;
+    } else {  // 4 columns of 4 consecutive k
+      const int n = col0 + tid % CT * 4, k = k0 + tid / CT * 4;
 #pragma unroll
-      for (int j = 0; j < NP; ++j)
+      for (int j = 0; j < 4; ++j)
         wv[j] = n < a.cout && k + j < a.cin
-                    ? *reinterpret_cast<const u32x4*>(W + int64_t(k + j) * a.cout + n)
-                    : u32x4{};
+                    ? *reinterpret_cast<const f32x4*>(W + int64_t(k + j) * a.cout + n)
+                    : f32x4{};
     }
   };
-  // 16 bytes along k into row r of an operand in LDS
-  const auto stage_row = [&](__bf16 (&s)[PARTS][kTile * BK], int r, u32x4 v) {
-    const int at = lds_at<BK>(r, piece * VEC / 8) + piece * VEC % 8;
-    if constexpr (PARTS == 3) {
-      bf16x4 p[3];
-      split3(__builtin_bit_cast(f32x4, v), p);
+  // parts of 4 values along k into row r of an operand in LDS
+  const auto put = [&](__bf16 (&s)[3][kTile * BK], int r, int k, f32x4 v) {
+    bf16x4 p[3];
+    split3(v, p);
 #pragma unroll
-      for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x4*>(&s[t][at]) = p[t];
-    } else {
-      *reinterpret_cast<u32x4*>(&s[0][at]) = v;
-    }
+    for (int t = 0; t < 3; ++t)
+      *reinterpret_cast<bf16x4*>(&s[t][lds_at<BK>(r, k / 8) + k % 8]) = p[t];
   };
   const auto stage = [&]() {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) stage_row(s_x, r0 + j * PASS, xv[j]);
+    for (int j = 0; j < 4; ++j) put(s_x, r0 + j * PASS, piece * 4, xv[j]);
     if constexpr (WT) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) stage_row(s_w, column_slot<T>(r0 + j * PASS), wv[j]);
+      for (int j = 0; j < 4; ++j) put(s_w, r0 + j * PASS, piece * 4, wv[j]);
     } else {
-      constexpr int CT = kTile / VEC;
-      const int n = tid % CT * VEC, k = tid / CT * NP;
-      if constexpr (PARTS == 3) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          f32x4 v;
-#pragma unroll
-          for (int j = 0; j < NP; ++j) v[j] = __builtin_bit_cast(f32x4, wv[j])[e];
-          bf16x4 p[3];
-          split3(v, p);
-#pragma unroll
-          for (int t = 0; t < 3; ++t)
-            *reinterpret_cast<bf16x4*>(
-                &s_w[t][lds_at<BK>(column_slot<T>(n + e), k / 8) + k % 8]) = p[t];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          bf16x4 v;
-#pragma unroll
-          for (int j = 0; j < NP; ++j) v[j] = __builtin_bit_cast(bf16x8, wv[j])[e];
-          *reinterpret_cast<bf16x4*>(
-              &s_w[0][lds_at<BK>(column_slot<T>(n + e), k / 8) + k % 8]) = v;
-        }
-      }
+      for (int e = 0; e < 4; ++e)
+        put(s_w, tid % CT * 4 + e, tid / CT * 4, f32x4{wv[0][e], wv[1][e], wv[2][e], wv[3][e]});
     }
   };
 
@@ -232,56 +185,41 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
     stage();
     __syncthreads();
     if (step + 1 < steps) fetch(step + 1);
+    bf16x8 xf[4][3];
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; ++kk) {
-      bf16x8 xf[4][PARTS];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int t = 0; t < 3; ++t)
+        xf[j][t] = *reinterpret_cast<const bf16x8*>(
+            &s_x[t][lds_at<BK>(wm * 64 + j * 16 + q, h)]);
 #pragma unroll
-        for (int t = 0; t < PARTS; ++t)
-          xf[j][t] = *reinterpret_cast<const bf16x8*>(
-              &s_x[t][lds_at<BK>(wm * 64 + j * 16 + q, kk * 4 + h)]);
+    for (int i = 0; i < 4; ++i) {
+      bf16x8 wf[1][3];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bf16x8 wf[1][PARTS];
-#pragma unroll
-        for (int t = 0; t < PARTS; ++t)
-          wf[0][t] = *reinterpret_cast<const bf16x8*>(
-              &s_w[t][lds_at<BK>(wn * 64 + i * 16 + q, kk * 4 + h)]);
-        products<PARTS, 1, 4>(wf, xf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
-      }
+      for (int t = 0; t < 3; ++t)
+        wf[0][t] = *reinterpret_cast<const bf16x8*>(
+            &s_w[t][lds_at<BK>(wn * 64 + i * 16 + q, h)]);
+      products<3, 1, 4>(wf, xf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
     }
   }
 
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (wm * 64 + j * 16 + q >= n_rows) continue;
-    T* y = static_cast<T*>(a.y) + (int64_t(row[j]) * a.dout + blk.out_off + comp[j]) * a.cout;
-    if constexpr (PARTS == 3) {
+    float* y = static_cast<float*>(a.y) +
+               (int64_t(row[j]) * a.dout + blk.out_off + comp[j]) * a.cout;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = col0 + wn * 64 + i * 16 + h * 4;
-        if (n < a.cout) *reinterpret_cast<f32x4*>(y + n) = acc[i][j];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const int n = col0 + wn * 64 + i * 16 + h * 8;
-        bf16x8 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = __bf16(acc[i][j][e]);
-          v[4 + e] = __bf16(acc[i + 1][j][e]);
-        }
-        if (n < a.cout) *reinterpret_cast<bf16x8*>(y + n) = v;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int n = col0 + wn * 64 + i * 16 + h * 4;
+      if (n < a.cout) *reinterpret_cast<f32x4*>(y + n) = acc[i][j];
     }
   }
 }
 
-// bf16 with W transposed, where both operands lie along k in memory: chunks of
-// 64 k go straight to LDS, one is multiplied while the next is on its way; two
-// workgroups on a compute unit.
+// bf16: chunks of 64 k go straight to LDS, one is multiplied while the next is
+// on its way; two workgroups on a compute unit.  W lies along k when it is
+// transposed, and along its columns when not: then it is read across.
+template <bool WT>
 __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, const MixList l) {
   // a name for every stage: reads of one are then known not to wait for loads
   // into the other
@@ -300,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, cons
   const RowOrder order(a.index, a.order, tile, a.x);
   const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
   const TileLoad load;
+  const AcrossLoad<4> across;
   const int wm = load.wave & 1, wn = load.wave >> 1, col0 = col_tile * kTile;
   const int n_rows = int(min(int64_t(kTile), tile.rows - tile.at));
   const TileRows rows(tile.at, blk.deg);
@@ -325,9 +264,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, cons
     const int s = load.row + j * 32;
     const int n = min(col0 + ((s & ~31) | ((s >> 2) & 3) << 3 | ((s >> 4) & 1) << 2 | (s & 3)),
                       a.cout - 1);
+    const int64_t W0 = int64_t(tile.group) * a.pairs * a.cin * a.cout;
     wrow[j] = static_cast<const uint8_t*>(a.W) +
-              ((int64_t(tile.group) * a.pairs * a.cout + n) * a.cin + load.piece * 8) * 2;
+              (W0 + (WT ? int64_t(n) * a.cin + load.piece * 8
+                        : int64_t(across.row + j * 16) * a.cout + col0 + across.piece * 8)) * 2;
   }
+  const bool in_col = col0 + across.piece * 8 < a.cout;
   const int chunks = (a.cin + 63) / 64;
   const int steps = tile.group < a.n_groups ? blk.n_src * chunks : 0;
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
@@ -337,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, cons
     if (b + 1 < chunks) {  // past the last chunk it is asked for again
       ++b;
       xo += 128;
-      wo += 128;
+      wo += WT ? 128 : int64_t(a.cout) * 128;
     } else if (src + 1 < blk.n_src) {
       const MixSource sc = l.src[blk.src0 + ++src];
       b = 0;
@@ -348,7 +290,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, cons
 #pragma unroll
     for (int j = 0; j < 4; ++j) load.ask(in ? xrow[j] + xo : zeros, x, j);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load.ask(in ? wrow[j] + wo : zeros, w, j);
+    for (int j = 0; j < 4; ++j) {
+      const bool have = WT ? in : in_col && b * 64 + across.row + j * 16 < a.cin;
+      load.ask(have ? wrow[j] + wo : zeros, w, j);
+    }
   };
   const auto turn = [&](const uint8_t* x, const uint8_t* w, uint8_t* x_free, uint8_t* w_free,
                         int step) {
@@ -364,8 +309,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, cons
         xf[j][0] = *reinterpret_cast<const bf16x8*>(tile_at(x, wm * 64 + j * 16 + q, kk * 4 + h));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bf16x8 wf[1][1] = {
-            {*reinterpret_cast<const bf16x8*>(tile_at(w, wn * 64 + i * 16 + q, kk * 4 + h))}};
+        bf16x8 wf[1][1];
+        if constexpr (WT)
+          wf[0][0] = *reinterpret_cast<const bf16x8*>(tile_at(w, wn * 64 + i * 16 + q, kk * 4 + h));
+        else wf[0][0] = across.read(w, kk, wn * 8 + (i >> 1) * 4 + (lane & 3), i & 1);
         products<1, 1, 4>(wf, xf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
       }
     }
@@ -411,7 +358,7 @@ constexpr int kStreamRows = 64;
 template <class T, bool WT, int NK, int CW, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, const MixList l,
                                                             int chunk) {
-  constexpr int PARTS = Chunk<T>::PARTS, K = 32 * NK;
+  constexpr int PARTS = kParts<T>, K = 32 * NK;
   constexpr int VEC = 16 / sizeof(T), TPR = K / VEC, PASS = kThreads / TPR;
   constexpr int NP = kStreamRows / PASS, RT = CW;  // row tiles of a wavefront
   static_assert(NP >= 1);
@@ -665,7 +612,7 @@ bool streams(const MixArgs& a, const MixList& l) {
 // row's result stays the same.
 template <class T, bool WT>
 __global__ void __launch_bounds__(64) k_mix_few(const MixArgs a, const MixList l) {
-  constexpr int PARTS = Chunk<T>::PARTS, VEC = 16 / sizeof(T), N = PARTS == 3 ? 4 : 8;
+  constexpr int PARTS = kParts<T>, VEC = 16 / sizeof(T), N = PARTS == 3 ? 4 : 8;
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
@@ -768,11 +715,11 @@ hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
   }
   const dim3 grid{unsigned(wgs)};
   if constexpr (sizeof(T) == 2) {
-    if (a.w_trans) hipLaunchKernelGGL(k_mix_along, grid, dim3(kThreads), 0, s, a, l);
-    else hipLaunchKernelGGL((k_mix<T, false>), grid, dim3(kThreads), 0, s, a, l);
+    if (a.w_trans) hipLaunchKernelGGL((k_mix_along<true>), grid, dim3(kThreads), 0, s, a, l);
+    else hipLaunchKernelGGL((k_mix_along<false>), grid, dim3(kThreads), 0, s, a, l);
   } else {
-    if (a.w_trans) hipLaunchKernelGGL((k_mix<T, true>), grid, dim3(kThreads), 0, s, a, l);
-    else hipLaunchKernelGGL((k_mix<T, false>), grid, dim3(kThreads), 0, s, a, l);
+    if (a.w_trans) hipLaunchKernelGGL((k_mix<true>), grid, dim3(kThreads), 0, s, a, l);
+    else hipLaunchKernelGGL((k_mix<false>), grid, dim3(kThreads), 0, s, a, l);
   }
   return hipGetLastError();
 }
@@ -820,35 +767,98 @@ __device__ __forceinline__ int parts_before(const int* offsets, int g, int deg, 
   return total;
 }
 
-// Channel of slot (e, c) of a tile: VEC c + e; slot = e (128 / VEC) + c, so
-// that neighbouring threads write neighbouring rows of LDS.
-template <class T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
-    k_mix_dw(const MixDwArgs a, const MixDwList l, int64_t part_rows) {
-  constexpr int BK = Chunk<T>::K, PARTS = Chunk<T>::PARTS;
-  constexpr int VEC = 16 / sizeof(T), CT = kTile / VEC, NP = 4;
-  static_assert(kThreads / CT * NP == BK);
-  __shared__ __attribute__((aligned(16))) __bf16 s_x[PARTS][kTile * BK], s_y[PARTS][kTile * BK];
-  const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
-  const int* offsets = a.index ? a.index + a.offsets : nullptr;
-  const int pi = int(blockIdx.y);
-  const MixPair p = l.p[pi];
-  // tiles of dW: neighbouring workgroups are on different XCDs, each of which
-  // takes neighbouring tiles, whose rows of x and dy meet in its L2
-  const int tiles = ((a.cin + kTile - 1) / kTile) * ((a.cout + kTile - 1) / kTile);
-  int tile_of = int(blockIdx.x) % tiles;
-  if (tiles % 8 == 0) tile_of = tile_of % 8 * (tiles / 8) + tile_of / 8;
-  const int slot = int(blockIdx.x) / tiles;
+// What a workgroup adds up: rows of a group for 128 x 128 elements of a pair.
+struct DwTile {
   GroupTile tile;
-  if (!find_tile(offsets, a.n_groups, a.n_rows, p.deg, part_rows, slot, tile, 1) ||
-      tile.group >= a.n_groups || !valid)
-    return;
-  const int64_t n = min(part_rows, tile.rows - tile.at);  // rows of this workgroup
-  const int* order = a.index ? a.index + a.order + tile.first : nullptr;
+  int pair, a0, b0;  // first channels
+  int64_t n;         // rows
+  int last;          // last of the group's rows that has one
+  const int* order;
+  __device__ __forceinline__ bool find(const MixDwArgs& a, const MixDwList& l, int64_t part_rows) {
+    const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
+    const int* offsets = a.index ? a.index + a.offsets : nullptr;
+    pair = int(blockIdx.y);
+    const int deg = l.p[pair].deg;
+    // neighbouring workgroups are on different XCDs, each of which takes
+    // neighbouring tiles, whose rows of x and dy meet in its L2
+    const int row_tiles = (a.cin + kTile - 1) / kTile;
+    const int tiles = row_tiles * ((a.cout + kTile - 1) / kTile);
+    int of = int(blockIdx.x) % tiles;
+    if (tiles % 8 == 0) of = of % 8 * (tiles / 8) + of / 8;
+    a0 = of % row_tiles * kTile;
+    b0 = of / row_tiles * kTile;
+    if (!find_tile(offsets, a.n_groups, a.n_rows, deg, part_rows, int(blockIdx.x) / tiles, tile,
+                   1) || tile.group >= a.n_groups || !valid)
+      return false;
+    n = min(part_rows, tile.rows - tile.at);
+    order = a.index ? a.index + a.order + tile.first : nullptr;
+    last = int((tile.at + n - 1) / deg);
+    return true;
+  }
+  // Where the sums go.
+  __device__ __forceinline__ float* out(const MixDwArgs& a, const MixDwList& l,
+                                        int64_t part_rows) const {
+    const int64_t size = int64_t(a.cin) * a.cout;
+    if (tile.rows <= part_rows) return a.dW + (int64_t(tile.group) * a.pairs + pair) * size;
+    int64_t at = tile.at / part_rows;
+    for (int i = 0; i < pair; ++i) at += dw_parts(a.n_rows, l.p[i].deg, part_rows);
+    if (a.index)
+      at += parts_before(a.index + a.offsets, tile.group, l.p[pair].deg, part_rows);
+    return a.part + at * size;
+  }
+};
+
+// Rows that a lane loads: k, k + STRIDE, k + 2 STRIDE, k + 3 STRIDE of a chunk of
+// BK, in memory (row, component).  A chunk's rows are asked for a chunk ahead of
+// their channels; past the end they are the last row again.
+template <int STRIDE, int BK>
+struct DwRows {
+  int at[4], m[4], row[4], deg, last, step_at, step_m;
+  const int* order;
+  __device__ __forceinline__ DwRows(const DwTile& d, int deg_, int k)
+      : deg(deg_), last(d.last), step_at(BK / deg_), step_m(BK % deg_), order(d.order) {
+    const int64_t from = d.tile.at / deg;
+    const unsigned m0 = unsigned(d.tile.at - from * deg);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned u = m0 + unsigned(k + j * STRIDE), e = u / unsigned(deg);
+      at[j] = int(from) + int(e);
+      m[j] = int(u - e * unsigned(deg));
+    }
+  }
+  __device__ __forceinline__ void find() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = min(at[j], last);
+      row[j] = order ? order[t] : t;
+    }
+  }
+  __device__ __forceinline__ void next() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      at[j] += step_at;
+      m[j] += step_m;
+      if (m[j] >= deg) {
+        m[j] -= deg;
+        ++at[j];
+      }
+    }
+  }
+};
+
+// float32: rows pass through registers, where they are split and turned, to
+// LDS.  Channel 4 c + e of a tile lies in LDS row 32 e + c, so that neighbouring
+// threads write neighbouring rows.
+__global__ void __launch_bounds__(kThreads, 2)
+    k_mix_dw(const MixDwArgs a, const MixDwList l, int64_t part_rows) {
+  constexpr int BK = 32, CT = kTile / 4;
+  static_assert(kThreads / CT * 4 == BK);
+  __shared__ __attribute__((aligned(16))) __bf16 s_x[3][kTile * BK], s_y[3][kTile * BK];
+  DwTile d;
+  if (!d.find(a, l, part_rows)) return;
+  const MixPair p = l.p[d.pair];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave & 1, wn = wave >> 1, q = lane & 15, h = lane >> 4;
-  const int row_tiles = (a.cin + kTile - 1) / kTile;
-  const int a0 = tile_of % row_tiles * kTile, b0 = tile_of / row_tiles * kTile;
 
   f32x4 acc[4][4];  // [input channels][output channels]
 #pragma unroll
@@ -856,135 +866,164 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
 
-  // this thread's VEC channels of NP consecutive rows of a chunk.  Channels
-  // and rows past the end are read at the last ones' place and then cleared.
-  const int c = tid % CT, k = tid / CT * NP;
-  const bool in_x = a0 + c * VEC < a.cin, in_y = b0 + c * VEC < a.cout;
-  const T* x0 = static_cast<const T*>(a.x) + int64_t(p.in_off) * a.cin + (in_x ? a0 + c * VEC : 0);
-  const T* y0 = static_cast<const T*>(a.dy) + int64_t(p.out_off) * a.cout + (in_y ? b0 + c * VEC : 0);
-  const int last = int((tile.at + n - 1) / p.deg);  // last of the group's rows
-  const int step_at = BK / p.deg, step_m = BK % p.deg;
-  int at[NP], m[NP], row[NP];  // of the chunk whose rows are asked for next
-  if (n > 0) {
-    const int64_t from = tile.at / p.deg;
-    const unsigned m0 = unsigned(tile.at - from * p.deg);
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const unsigned u = m0 + unsigned(k + j), d = u / unsigned(p.deg);
-      at[j] = int(from) + int(d);
-      m[j] = int(u - d * unsigned(p.deg));
-    }
-  }
-  // a chunk's rows in memory are asked for a chunk ahead of their channels
-  const auto find = [&]() {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const int t = min(at[j], last);
-      row[j] = order ? order[t] : t;
-    }
-  };
-  u32x4 xv[NP], yv[NP];
+  // this thread's 4 channels of 4 consecutive rows of a chunk.  Channels and
+  // rows past the end are read at the last ones' place and then cleared.
+  const int c = tid % CT, k = tid / CT * 4;
+  const bool in_x = d.a0 + c * 4 < a.cin, in_y = d.b0 + c * 4 < a.cout;
+  const float* x0 = static_cast<const float*>(a.x) + int64_t(p.in_off) * a.cin +
+                    (in_x ? d.a0 + c * 4 : 0);
+  const float* y0 = static_cast<const float*>(a.dy) + int64_t(p.out_off) * a.cout +
+                    (in_y ? d.b0 + c * 4 : 0);
+  DwRows<1, BK> rows(d, p.deg, k);
+  f32x4 xv[4], yv[4];
   const auto fetch = [&]() {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      xv[j] = *reinterpret_cast<const u32x4*>(x0 + (int64_t(row[j]) * a.din + m[j]) * a.cin);
-      yv[j] = *reinterpret_cast<const u32x4*>(y0 + (int64_t(row[j]) * a.dout + m[j]) * a.cout);
-      at[j] += step_at;
-      m[j] += step_m;
-      if (m[j] >= p.deg) {
-        m[j] -= p.deg;
-        ++at[j];
-      }
+    for (int j = 0; j < 4; ++j) {
+      xv[j] = *reinterpret_cast<const f32x4*>(x0 + (int64_t(rows.row[j]) * a.din + rows.m[j]) * a.cin);
+      yv[j] = *reinterpret_cast<const f32x4*>(y0 + (int64_t(rows.row[j]) * a.dout + rows.m[j]) * a.cout);
     }
+    rows.next();
   };
-  const bool whole = a0 + kTile <= a.cin && b0 + kTile <= a.cout;
-  const auto stage = [&](__bf16 (&s)[PARTS][kTile * BK], u32x4 (&v)[NP], bool in, int64_t left) {
+  const bool whole = d.a0 + kTile <= a.cin && d.b0 + kTile <= a.cout;
+  const auto stage = [&](__bf16 (&s)[3][kTile * BK], f32x4 (&v)[4], bool in, int64_t left) {
     if (!whole || left < BK) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j)
-        if (!in || k + j >= left) v[j] = u32x4{};
+      for (int j = 0; j < 4; ++j)
+        if (!in || k + j >= left) v[j] = f32x4{};
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if constexpr (PARTS == 3) {
-        f32x4 t;
+    for (int e = 0; e < 4; ++e) {
+      bf16x4 part[3];
+      split3(f32x4{v[0][e], v[1][e], v[2][e], v[3][e]}, part);
 #pragma unroll
-        for (int j = 0; j < NP; ++j) t[j] = __builtin_bit_cast(f32x4, v[j])[e];
-        bf16x4 part[3];
-        split3(t, part);
-#pragma unroll
-        for (int u = 0; u < 3; ++u)
-          *reinterpret_cast<bf16x4*>(&s[u][lds_at<BK>(e * CT + c, k / 8) + k % 8]) = part[u];
-      } else {
-        bf16x4 t;
-#pragma unroll
-        for (int j = 0; j < NP; ++j) t[j] = __builtin_bit_cast(bf16x8, v[j])[e];
-        *reinterpret_cast<bf16x4*>(&s[0][lds_at<BK>(e * CT + c, k / 8) + k % 8]) = t;
-      }
+      for (int u = 0; u < 3; ++u)
+        *reinterpret_cast<bf16x4*>(&s[u][lds_at<BK>(e * CT + c, k / 8) + k % 8]) = part[u];
     }
-  };
-  // LDS row of lane q of product i of this wavefront's 64 channels, and the
-  // channel: a lane's four products are four consecutive channels
-  const auto slot_of = [&](int w, int i, int lane16) {
-    if constexpr (PARTS == 3) return i * CT + w * 16 + lane16;
-    else return (i + 4 * (lane16 >> 3)) * CT + w * 8 + (lane16 & 7);
-  };
-  const auto channel_of = [&](int w, int lane16) {  // of product 0
-    if constexpr (PARTS == 3) return (w * 16 + lane16) * 4;
-    else return (w * 8 + (lane16 & 7)) * 8 + 4 * (lane16 >> 3);
   };
 
-  if (n > 0) {
-    find();
+  if (d.n > 0) {
+    rows.find();
     fetch();
-    find();
+    rows.find();
   }
-  for (int64_t k0 = 0; k0 < n; k0 += BK) {
+  for (int64_t k0 = 0; k0 < d.n; k0 += BK) {
     __syncthreads();
-    stage(s_x, xv, in_x, n - k0);
-    stage(s_y, yv, in_y, n - k0);
+    stage(s_x, xv, in_x, d.n - k0);
+    stage(s_y, yv, in_y, d.n - k0);
     __syncthreads();
     fetch();  // (past the end: the last rows again)
-    find();
+    rows.find();
+    bf16x8 yf[4][3];
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; ++kk) {
-      bf16x8 yf[4][PARTS];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int t = 0; t < 3; ++t)
+        yf[j][t] = *reinterpret_cast<const bf16x8*>(&s_y[t][lds_at<BK>(j * CT + wn * 16 + q, h)]);
 #pragma unroll
-        for (int t = 0; t < PARTS; ++t)
-          yf[j][t] = *reinterpret_cast<const bf16x8*>(
-              &s_y[t][lds_at<BK>(slot_of(wn, j, q), kk * 4 + h)]);
+    for (int i = 0; i < 4; ++i) {
+      bf16x8 xf[1][3];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bf16x8 xf[1][PARTS];
-#pragma unroll
-        for (int t = 0; t < PARTS; ++t)
-          xf[0][t] = *reinterpret_cast<const bf16x8*>(
-              &s_x[t][lds_at<BK>(slot_of(wm, i, q), kk * 4 + h)]);
-        products<PARTS, 1, 4>(xf, yf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
-      }
+      for (int t = 0; t < 3; ++t)
+        xf[0][t] = *reinterpret_cast<const bf16x8*>(&s_x[t][lds_at<BK>(i * CT + wm * 16 + q, h)]);
+      products<3, 1, 4>(xf, yf, reinterpret_cast<f32x4(&)[1][4]>(acc[i]));
     }
   }
 
-  const int64_t size = int64_t(a.cin) * a.cout;
-  float* out = a.dW + (int64_t(tile.group) * a.pairs + pi) * size;
-  if (tile.rows > part_rows) {
-    int64_t at = tile.at / part_rows;
-    for (int i = 0; i < pi; ++i) at += dw_parts(a.n_rows, l.p[i].deg, part_rows);
-    if (offsets) at += parts_before(offsets, tile.group, p.deg, part_rows);
-    out = a.part + at * size;
-  }
-  const int col = b0 + channel_of(wn, q);
+  float* out = d.out(a, l, part_rows);
+  const int col = d.b0 + (wn * 16 + q) * 4;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = a0 + channel_of(wm, 4 * h + r) + i;
+      const int row = d.a0 + (wm * 16 + 4 * h + r) * 4 + i;
       f32x4 v;
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = acc[i][j][r];
-      if (row < a.cin && col < a.cout) *reinterpret_cast<f32x4*>(out + int64_t(row) * a.cout + col) = v;
+      if (row < a.cin && col < a.cout)
+        *reinterpret_cast<f32x4*>(out + int64_t(row) * a.cout + col) = v;
+    }
+  }
+}
+
+// The same in bf16: rows of x and dy go straight to LDS as they lie in memory
+// and are read across them; one chunk of 64 rows is multiplied while the next is
+// on its way.  Rows past the end are zeros.
+__global__ void __launch_bounds__(kThreads, 2)
+    k_mix_dw_across(const MixDwArgs a, const MixDwList l, int64_t part_rows) {
+  __shared__ __attribute__((aligned(128))) uint8_t s_x0[TileLoad::kBytes], s_y0[TileLoad::kBytes];
+  __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_y1[TileLoad::kBytes];
+  DwTile d;
+  if (!d.find(a, l, part_rows)) return;
+  const MixPair p = l.p[d.pair];
+  const TileLoad load;
+  const AcrossLoad<2> across;
+  const int lane = threadIdx.x & 63, q = lane & 15, h = lane >> 4;
+  const int wm = load.wave & 1, wn = load.wave >> 1;
+  f32x4 acc[4][4];  // [input channels][output channels]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+  const int ca = d.a0 + across.piece * 8, cb = d.b0 + across.piece * 8;
+  const bool in_x = ca < a.cin, in_y = cb < a.cout;
+  const uint8_t* x0 = static_cast<const uint8_t*>(a.x) + (int64_t(p.in_off) * a.cin + ca) * 2;
+  const uint8_t* y0 = static_cast<const uint8_t*>(a.dy) + (int64_t(p.out_off) * a.cout + cb) * 2;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
+  DwRows<16, 64> rows(d, p.deg, across.row);
+  int64_t left = d.n - across.row;
+  const auto fetch = [&](uint8_t* x, uint8_t* y) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = j * 16 < left;
+      const int64_t xo = (int64_t(rows.row[j]) * a.din + rows.m[j]) * a.cin * 2;
+      const int64_t yo = (int64_t(rows.row[j]) * a.dout + rows.m[j]) * a.cout * 2;
+      load.ask(in && in_x ? x0 + xo : zeros, x, j);
+      load.ask(in && in_y ? y0 + yo : zeros, y, j);
+    }
+    left -= 64;
+    rows.next();
+    rows.find();
+  };
+  const int64_t steps = (d.n + 63) / 64;
+  const auto turn = [&](const uint8_t* x, const uint8_t* y, uint8_t* x_free, uint8_t* y_free,
+                        int64_t step) {
+    tile_wait();
+    fetch(x_free, y_free);
+    if (step >= steps) return;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 yf[4][1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        yf[j][0] = across.read(y, kk, wn * 8 + j * 2 + ((lane & 3) >> 1), lane & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8 xf[1][1] = {
+            {across.read(x, kk, wm * 8 + i * 2 + ((lane & 3) >> 1), lane & 1)}};
+        // rows of the products: output channels
+        products<1, 4, 1>(yf, xf, reinterpret_cast<f32x4(&)[4][1]>(acc[i]));
+      }
+    }
+  };
+  if (steps > 0) {
+    rows.find();
+    fetch(s_x0, s_y0);
+  }
+  for (int64_t step = 0; step < steps; step += 2) {
+    turn(s_x0, s_y0, s_x1, s_y1, step);
+    turn(s_x1, s_y1, s_x0, s_y0, step + 1);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load writes to LDS after the end
+  float* out = d.out(a, l, part_rows);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int ch = d.a0 + wm * 64 + i * 16 + q;
+    if (ch >= a.cin) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = d.b0 + wn * 64 + j * 16 + h * 4;
+      if (col < a.cout) *reinterpret_cast<f32x4*>(out + int64_t(ch) * a.cout + col) = acc[i][j];
     }
   }
 }
@@ -1028,8 +1067,10 @@ hipError_t launch_mix_dw_t(const MixDwArgs& a, const MixPair* p, hipStream_t s) 
   const int64_t rows = dw_rows(a.n_rows, a.cin, a.cout, p, a.pairs, sizeof(T));
   const int64_t slots = most_tiles(a.n_rows, a.n_groups, deg, rows, true) + 1;
   const int64_t tiles = int64_t((a.cin + kTile - 1) / kTile) * ((a.cout + kTile - 1) / kTile);
-  hipLaunchKernelGGL((k_mix_dw<T>), dim3(unsigned(slots * tiles), unsigned(a.pairs)),
-                     dim3(kThreads), 0, s, a, l, rows);
+  const dim3 grid(unsigned(slots * tiles), unsigned(a.pairs));
+  if constexpr (sizeof(T) == 2)
+    hipLaunchKernelGGL(k_mix_dw_across, grid, dim3(kThreads), 0, s, a, l, rows);
+  else hipLaunchKernelGGL(k_mix_dw, grid, dim3(kThreads), 0, s, a, l, rows);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_rows * deg <= rows) return e;
   const int64_t runs = std::min((int64_t(a.cin) * a.cout + 1023) / 1024,

@@ -14,6 +14,9 @@
 
 namespace e3k {
 
+using s16x4_t = short __attribute__((ext_vector_type(4)));
+using bf16x8_t = __bf16 __attribute__((ext_vector_type(8)));
+
 constexpr int kTileRows = 128;
 
 // What is read where a row has ended.
@@ -38,6 +41,32 @@ struct TileLoad {
 __device__ __forceinline__ const uint8_t* tile_at(const uint8_t* lds, int r, int piece) {
   return lds + r * 128 + ((piece ^ (r & 7)) << 4);
 }
+
+// Tiles of 64 k of 128 bf16 channels that lie along the channels in memory: 16
+// pieces a k, which a transposing read turns to the order of the products.  A
+// lane's pieces are of rows row, row + 16, row + 32 and row + 48; FLIP: the bit
+// of the piece at which the rows of 16 lanes part, 4 for reads of 4 channels
+// out of every 8, 2 for 16 channels in a row (then 32 lanes meet no bank twice).
+template <int FLIP>
+struct AcrossLoad {
+  int row, piece;
+  __device__ __forceinline__ AcrossLoad()
+      : row(int(threadIdx.x >> 4)), piece((int(threadIdx.x) & 15) ^ flip(row)) {}
+  static __device__ __forceinline__ int flip(int k) {
+    return FLIP == 4 ? (k & 3) << 2 : (k & 3) << 1 | (k & 8);
+  }
+  // 8 values along k, from 8 (lane / 16) on, of channel lane % 16 of those
+  // whose fourths the lanes name: lane 4 r + c of 16 names fourth c
+  static __device__ __forceinline__ bf16x8_t read(const uint8_t* lds, int kk, int piece, int half) {
+    const int lane = int(threadIdx.x) & 63;
+    const int k = kk * 32 + (lane >> 4) * 8 + ((lane >> 2) & 3);
+    const uint8_t* at = lds + k * 256 + ((piece ^ flip(k)) << 4) + half * 8;
+    using Lds = __attribute__((address_space(3))) s16x4_t;
+    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)at);
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(at + 4 * 256));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
 
 // Waits for this wavefront's loads, then for the other wavefronts.
 __device__ __forceinline__ void tile_wait() {
