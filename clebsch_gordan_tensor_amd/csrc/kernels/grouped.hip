@@ -732,18 +732,22 @@ struct MixDwList {
 };
 
 // Rows of a workgroup's part of a group's sum.  Parts of a group that has
-// several are written to the workspace and added afterwards: enough of them to
-// fill the chip, but of so many rows that the parts are a quarter of what x and
-// dy are at most; the only part of a group goes straight to dW.  Where one
-// group's tiles fill the chip by themselves there are no parts.
-constexpr int kDwTarget = 1024;
+// several are written to the workspace and added afterwards; the only part of a
+// group goes straight to dW.  Parts are short enough to fill the chip, in bf16
+// once (two workgroups on a compute unit at a time: 20,000 x 16 rows of 128
+// channels with dx 80 us in 350 parts, 91 in 550), in float32, whose rows take
+// longest, twice; but not so short that a part's beginning and end outweigh its
+// rows, or that all of them are more than half of what x and dy are (3,051 rows
+// in 9 groups, 744 x 256 channels in float32 with dx: 57 us, 89 with parts of an
+// eighth).  Where one group's tiles fill the chip there are no parts.
 int64_t dw_rows(int64_t n_rows, int cin, int cout, const MixPair* p, int n_pairs, int esize) {
   const int64_t tiles = int64_t((cin + kTile - 1) / kTile) * ((cout + kTile - 1) / kTile);
   if (tiles >= 256) return int64_t(1) << 40;
   int64_t comps = 0;
   for (int i = 0; i < n_pairs; ++i) comps += p[i].deg;
-  const int64_t least = int64_t(32) * cin * cout / (int64_t(cin + cout) * esize);
-  const int64_t rows = std::max(n_rows * comps * tiles / kDwTarget, std::max<int64_t>(256, least));
+  const int64_t least = std::max(int64_t(8) * cin * cout / (int64_t(cin + cout) * esize),
+                                 int64_t(esize == 4 ? 128 : 512));
+  const int64_t rows = std::max(n_rows * comps * tiles / (esize == 4 ? 1024 : 384), least);
   return (rows + 63) / 64 * 64;
 }
 // Most parts that groups with several can have together: each holds half of
