@@ -593,16 +593,16 @@ template <class T, bool WT>
 hipError_t launch_stream_k(const MixArgs& a, const MixList& l, hipStream_t s) {
   if (a.cin <= 32) return launch_stream<T, WT, 1>(a, l, s);
   if (a.cin <= 64) return launch_stream<T, WT, 2>(a, l, s);
-  if constexpr (sizeof(T) == 2)
-    if (a.cin > 128) return launch_stream<T, WT, 8>(a, l, s);
   return launch_stream<T, WT, 4>(a, l, s);
 }
 
-template <class T>
+// Whether W's columns fit into registers.  (20,000 x 4 rows in 10 groups, bf16,
+// 256 to 256 channels: 43 us so, 28 through tiles; 20,000 x 16 rows of 128: 32
+// and 39; of 64: 17 and 31.)
 bool streams(const MixArgs& a, const MixList& l) {
   for (int i = 0; i < l.n_blocks; ++i)
     if (l.blk[i].n_src > 1) return false;
-  return a.cin <= (sizeof(T) == 2 ? 256 : 128);
+  return a.cin <= 128;
 }
 
 // Few rows of a group: what counts is that the weights are asked for at once.
@@ -704,7 +704,7 @@ hipError_t launch_few(const MixArgs& a, MixList l, hipStream_t s) {
 template <class T>
 hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
   if (few_rows(a.n_rows, a.n_groups, l)) return launch_few<T>(a, l, s);
-  if (streams<T>(a, l))
+  if (streams(a, l))
     return a.w_trans ? launch_stream_k<T, true>(a, l, s) : launch_stream_k<T, false>(a, l, s);
   int64_t wgs = 0;
   for (int i = 0; i < l.n_blocks; ++i) {
