@@ -602,9 +602,15 @@ hipError_t launch_fp8_few(const Fp8MixArgs& a, MixList l, hipStream_t s) {
 
 template <class T>
 hipError_t launch_fp8_mix_t(const Fp8MixArgs& a, MixList l, hipStream_t s) {
-  if (few_rows(a.n_rows, a.n_groups, l)) return launch_fp8_few<T>(a, l, s);
   bool one = a.cin <= 128;
   for (int i = 0; i < l.n_blocks; ++i) one &= l.blk[i].n_src <= 1;
+  // us by small tiles and by large, 1024 to 1024 channels: float32, one group,
+  // 512 rows 12.5 and 17.5, 1024 21.7 and 17.6; 16 groups, 512 17.1 and 19.1;
+  // bf16, one group, 256 rows 10.3 and 11.7, 512 12.2 and 11.7; 16 groups of
+  // 2048 to 512, 512 rows 17.0 and 19.3, 1024 26.2 and 21.1
+  if (one ? few_rows(a.n_rows, a.n_groups, l)
+          : small_tiles(a.n_rows, a.n_groups, l, a.cout) <= (sizeof(T) == 4 ? 3000 : 1600))
+    return launch_fp8_few<T>(a, l, s);
   if (one) return launch_fp8_stream<T>(a, l, s);
   int64_t wgs = 0;
   for (int i = 0; i < l.n_blocks; ++i) {

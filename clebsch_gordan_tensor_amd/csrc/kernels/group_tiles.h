@@ -130,15 +130,27 @@ struct TileRows {
   }
 };
 
-// Whether the groups have so few rows that kernels of small tiles answer
-// sooner.  One group, 1024 to 1024 channels in bf16, us by rows, small tiles and
-// large: 1 10.4 and 25.8, 128 10.8 and 26.8, 256 14.1 and 27.1, 512 20.3 and
-// 27.1; ten groups: 64 15.8 and 27.0, 128 18.5 and 26.9, 256 27.8 and 27.1; in 8
-// bits they part between 256 and 512 rows, one group or ten.
+// Whether the groups have so few rows that kernels of tiles of 16 rows and
+// columns answer sooner than those that keep W's columns in registers, which
+// first have to fetch all of them.
 inline bool few_rows(int64_t n_rows, int n_groups, const MixList& l) {
   int deg = 1;
   for (int i = 0; i < l.n_blocks; ++i) deg = l.blk[i].deg > deg ? l.blk[i].deg : deg;
   return n_rows * deg <= 16 * int64_t(n_groups) + 112;
+}
+
+// Tiles of 16 rows and columns of all blocks.  Kernels of such tiles fetch W for
+// each, and yet they answer sooner than large tiles as long as the chip isn't
+// full of them.  us by small tiles and by large, 1024 to 1024 channels: float32,
+// one group, 512 rows 32 and 78, 1024 52 and 79, 2048 93 and 79; 16 groups,
+// 1024 67 and 81, 2048 113 and 82; bf16, one group, 256 rows 11.5 and 14.8, 512
+// 15.8 and 14.7; 16 groups, 128 15.5 and 15.7, 256 18.6 and 15.6; the same of
+// 2048 to 512: 4,100 to 4,600 tiles 100 and 152 to 128 and 154 in float32, 1,020
+// tiles 21 and 26 and 1,540 28 and 26 in bf16.
+inline int64_t small_tiles(int64_t n_rows, int n_groups, const MixList& l, int cout) {
+  int64_t n = 0;
+  for (int i = 0; i < l.n_blocks; ++i) n += (n_rows * l.blk[i].deg + 15) / 16 + n_groups;
+  return n * ((cout + 15) / 16);
 }
 
 // Most tiles that n_rows rows in n_groups groups (and some without) can fill.

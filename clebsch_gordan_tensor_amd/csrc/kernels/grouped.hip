@@ -703,8 +703,11 @@ hipError_t launch_few(const MixArgs& a, MixList l, hipStream_t s) {
 
 template <class T>
 hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
-  if (few_rows(a.n_rows, a.n_groups, l)) return launch_few<T>(a, l, s);
-  if (streams(a, l))
+  const bool stream = streams(a, l);
+  if (stream ? few_rows(a.n_rows, a.n_groups, l)
+             : small_tiles(a.n_rows, a.n_groups, l, a.cout) <= (sizeof(T) == 4 ? 6000 : 1200))
+    return launch_few<T>(a, l, s);
+  if (stream)
     return a.w_trans ? launch_stream_k<T, true>(a, l, s) : launch_stream_k<T, false>(a, l, s);
   int64_t wgs = 0;
   for (int i = 0; i < l.n_blocks; ++i) {

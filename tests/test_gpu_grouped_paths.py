@@ -115,6 +115,33 @@ def test_mixing_in_8_bits(gpu, xs, os_, rows, groups, cin, cout, out_dtype):
     R.check(host(y), ref, "y", bf16, adds=1, drops=R.EIGHTS if bf16 else 0.0)
 
 
+# a row alone, among few and among many: the same bits, whichever tiles it is in
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8 f32", "fp8 bf16"])
+@pytest.mark.parametrize("xs,os_,cin,cout", [
+    ("0e+0e+1o", "0e+1o", 208, 272), ("0e", "0e", 1040, 560), ("0e+1o", "0e+1o", 96, 144)])
+def test_a_row_alone(gpu, xs, os_, cin, cout, dtype):
+    into, out = _ir(xs), _ir(os_)
+    group = _skewed(4000, 3, 0.4)
+    x, W, dy = _case(into, out, group, 3, cin, cout, dtype)
+    if dtype.startswith("fp8"):
+        packed = gpu.linear_fp8_pack(into, out, dev(W))
+        of = torch.float32 if dtype == "fp8 f32" else None
+        runs = [(dev(x), lambda i, t: gpu.linear_fp8(into, out, *gpu.quantize_fp8(t), packed,
+                                                     index=i, dtype=of))]
+    else:
+        Wd = dev(W, dtype)
+        # (zeros for dW's operand: only dx is looked at)
+        runs = [(dev(x, dtype), lambda i, t: gpu.linear_grouped(into, out, i, t, Wd)),
+                (dev(dy, dtype), lambda i, t: gpu.linear_grouped_backward(
+                    into, out, i, torch.zeros((t.shape[0], S.dim(into), cin), device="cuda",
+                                              dtype=t.dtype), Wd, t)[0])]
+    for t, run in runs:
+        whole = run(gpu.group_rows(dev(group), 3), t)
+        for n in (1, 20, 150, 600, 1500):
+            assert torch.equal(run(gpu.group_rows(dev(group[:n]), 3), t[:n].contiguous()),
+                               whole[:n]), n
+
+
 def _train(gpu, ir, groups, X, Rd, Wn, B, W, Gd, dY, dH, stream=None):
     """A layer's pass: h = x + r normalised and mixed by element, then back."""
     index = gpu.group_rows(Gd, groups, stream=stream)
