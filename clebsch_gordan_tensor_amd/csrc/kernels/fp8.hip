@@ -72,6 +72,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Whether the weights are packed for this call; without pairs there are none,
+// nor a header.
+__device__ __forceinline__ bool weights_match(const Fp8MixArgs& a) {
+  if (a.pairs == 0) return true;
+  const int* header = static_cast<const int*>(a.packed);
+  return (header[0] == kFp8Magic) & (header[1] == a.cin) & (header[2] == a.cout) &
+         (header[3] == a.pairs) & (header[4] == a.n_groups);
+}
+
 // A block of 128 x 128 weights a workgroup: thread (c, k) takes 4 columns of
 // 16 consecutive k, whose codes it stores side by side.
 __global__ void __launch_bounds__(kThreads)
@@ -187,10 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_mix(const Fp8MixArgs a, con
   __shared__ __attribute__((aligned(128))) uint8_t s_x0[TileLoad::kBytes], s_w0[TileLoad::kBytes];
   __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_w1[TileLoad::kBytes];
   __shared__ float s_scale[kTileRows][kScaleSteps + 1];
-  bool valid = index_matches(a.index, a.n_rows, a.n_groups);
-  const int* header = static_cast<const int*>(a.packed);
-  valid &= (header[0] == kFp8Magic) & (header[1] == a.cin) & (header[2] == a.cout) &
-           (header[3] == a.pairs) & (header[4] == a.n_groups);  // packed for this call
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups) && weights_match(a);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
@@ -362,10 +368,7 @@ constexpr int kStreamRows = 64;  // of a workgroup's wavefronts together
 template <class T, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, const MixList l,
                                                             const Fp8Layout lay, int chunk) {
-  bool valid = index_matches(a.index, a.n_rows, a.n_groups);
-  const int* header = static_cast<const int*>(a.packed);
-  valid &= (header[0] == kFp8Magic) & (header[1] == a.cin) & (header[2] == a.cout) &
-           (header[3] == a.pairs) & (header[4] == a.n_groups);  // packed for this call
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups) && weights_match(a);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];
@@ -523,10 +526,7 @@ template <class T>
 __global__ void __launch_bounds__(64) k_fp8_few(const Fp8MixArgs a, const MixList l,
                                                 const Fp8Layout lay) {
   constexpr int N = std::is_same_v<T, float> ? 4 : 8;
-  bool valid = index_matches(a.index, a.n_rows, a.n_groups);
-  const int* header = static_cast<const int*>(a.packed);
-  valid &= (header[0] == kFp8Magic) & (header[1] == a.cin) & (header[2] == a.cout) &
-           (header[3] == a.pairs) & (header[4] == a.n_groups);  // packed for this call
+  const bool valid = index_matches(a.index, a.n_rows, a.n_groups) && weights_match(a);
   int bi = 0;
   while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
   const MixBlock blk = l.blk[bi];

@@ -115,6 +115,25 @@ def test_mixing_in_8_bits(gpu, xs, os_, rows, groups, cin, cout, out_dtype):
     R.check(host(y), ref, "y", bf16, adds=1, drops=R.EIGHTS if bf16 else 0.0)
 
 
+# no block of the input has a target: nothing of W is there to be read
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C", [(5, 48), (700, 48), (5, 208), (9000, 208)])
+def test_no_pairs(gpu, rows, C, dtype):
+    into, out = _ir("0e+2e"), _ir("1o+0o")
+    group = _skewed(rows, 3, 0.3)
+    x, W, dy = _case(into, out, group, 3, C, C, dtype)
+    assert W.shape[1] == 0
+    index, X, Wd = gpu.group_rows(dev(group), 3), dev(x, dtype), torch.empty(
+        W.shape, device="cuda", dtype=torch.float32 if dtype == "f32" else torch.bfloat16)
+    y = gpu.linear_grouped(into, out, index, X, Wd, out=torch.full_like(dev(dy, dtype), 3.0))
+    dx, dW = gpu.linear_grouped_backward(into, out, index, X, Wd, dev(dy, dtype),
+                                         dx=torch.full_like(X, 3.0))
+    assert not y.any() and not dx.any() and dW.shape == W.shape
+    packed = gpu.linear_fp8_pack(into, out, torch.empty(W.shape, device="cuda"))
+    y = gpu.linear_fp8(into, out, *gpu.quantize_fp8(X), packed, index=index)
+    assert y.shape == dy.shape and not y.any()
+
+
 # a row alone, among few and among many: the same bits, whichever tiles it is in
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8 f32", "fp8 bf16"])
 @pytest.mark.parametrize("xs,os_,cin,cout", [
