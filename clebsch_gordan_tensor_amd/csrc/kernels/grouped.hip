@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
 // on its way; two workgroups on a compute unit.  W lies along k when it is
 // transposed, and along its columns when not: then it is read across.
 // 16,384 rows in 16 groups, 1024 to 2048 channels: 98 us (700 TFLOP/s), its dx
-// 108; 40% of the cycles are products, no LDS read meets another's bank, and the
+// 96-110; 40% of the cycles are products, no LDS read meets another's bank, and the
 // rest are waits for chunks: 1.1 GB pass from the caches to LDS.
 template <bool WT>
 __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, const MixList l) {
@@ -1030,8 +1030,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load writes to LDS after the end
   // dW past the caches, which x and dy need (16,384 rows in 16 groups, 1024 x
-  // 2048, with dx: 199 us, 226 without; in float32, whose products take longer,
-  // it made no difference); parts are read again soon
+  // 2048, with dx: 199 us, 226 without, where they are in the caches from a call
+  // before, 253 and 257 where not; in float32, whose products take longer, it
+  // made no difference); parts are read again soon
   float* out = d.out(a, l, part_rows);
   const bool part = d.tile.rows > part_rows;
   const RowHalves halves;
@@ -1059,8 +1060,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // dW of the groups with several parts, added in their order, 1024 elements of a
 // (group, pair) at a time; most groups may have nothing here, so that the
 // launch is of kSumTarget workgroups rather than of one for every 1024 elements
-// (16 groups of 1024 x 2048 without parts: 18 us and 4).
-constexpr int kSumTarget = 4096;
+// (16 groups of 1024 x 2048 without parts: 18 us and 4.6).
+constexpr int kSumTarget = 1024;
 __global__ void __launch_bounds__(256) k_mix_dw_sum(const MixDwArgs a, const MixDwList l,
                                                     int64_t part_rows) {
   if (!index_matches(a.index, a.n_rows, a.n_groups)) return;

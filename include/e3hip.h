@@ -15,8 +15,10 @@
  * (conservative forces F = -dE/dpos, "Ab Initio Accuracy Beyond the Cutoff:
  * Distributed Message-Passing Equivariant Attention at Tens-of-Millions-of-
  * Atom Scale", cited as Tessera, 2.2 Eq.3).  Next to it: the channel mixing
- * within irreps, the radial edge weights, and for training the normalisation
- * of irreps features, the norm of all gradients and the AdamW step.
+ * within irreps (one set of weights, or one for each group of rows), the radial
+ * edge weights, for training the normalisation of irreps features, the norm of
+ * all gradients and the AdamW step, and for simulation the normalisation and
+ * the mixing in 8 bits.
  *
  * Conventions
  *   - An irreps list is a sequence of (l, parity) blocks; a block of degree l
