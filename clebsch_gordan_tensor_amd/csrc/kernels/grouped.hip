@@ -742,8 +742,9 @@ struct MixDwList {
 // Rows of a workgroup's part of a group's sum.  Parts of a group that has
 // several are written to the workspace and added afterwards; the only part of a
 // group goes straight to dW.  Parts are short enough to fill the chip, in bf16
-// once (two workgroups on a compute unit at a time: 20,000 x 16 rows of 128
-// channels with dx 80 us in 350 parts, 91 in 550), in float32, whose rows take
+// about once (with dx, 384 parts and 512 of all tiles: 20,000 x 16 rows of 128
+// channels 94 us and 104, 100,000 x 9 rows of 64 138 and 125, 16,411 rows of
+// 1024 x 2048 243 both), in float32, whose rows take
 // longest, twice; but not so short that a part's beginning and end outweigh its
 // rows, or that all of them are more than half of what x and dy are (3,051 rows
 // in 9 groups, 744 x 256 channels in float32 with dx: 57 us, 89 with parts of an
@@ -820,19 +821,19 @@ struct DwTile {
   }
 };
 
-// Rows that a lane loads: k, k + STRIDE, k + 2 STRIDE, k + 3 STRIDE of a chunk of
-// BK, in memory (row, component).  A chunk's rows are asked for a chunk ahead of
-// their channels; past the end they are the last row again.
-template <int STRIDE, int BK>
+// NR rows that a lane loads, k, k + STRIDE and so on of a chunk of BK, in memory
+// (row, component).  A chunk's rows are asked for a chunk ahead of their channels;
+// past the end they are the last row again.
+template <int STRIDE, int BK, int NR>
 struct DwRows {
-  int at[4], m[4], row[4], deg, last, step_at, step_m;
+  int at[NR], m[NR], row[NR], deg, last, step_at, step_m;
   const int* order;
   __device__ __forceinline__ DwRows(const DwTile& d, int deg_, int k)
       : deg(deg_), last(d.last), step_at(BK / deg_), step_m(BK % deg_), order(d.order) {
     const int64_t from = d.tile.at / deg;
     const unsigned m0 = unsigned(d.tile.at - from * deg);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NR; ++j) {
       const unsigned u = m0 + unsigned(k + j * STRIDE), e = u / unsigned(deg);
       at[j] = int(from) + int(e);
       m[j] = int(u - e * unsigned(deg));
@@ -840,14 +841,14 @@ struct DwRows {
   }
   __device__ __forceinline__ void find() {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NR; ++j) {
       const int t = min(at[j], last);
       row[j] = order ? order[t] : t;
     }
   }
   __device__ __forceinline__ void next() {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NR; ++j) {
       at[j] += step_at;
       m[j] += step_m;
       if (m[j] >= deg) {
@@ -886,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     (in_x ? d.a0 + c * 4 : 0);
   const float* y0 = static_cast<const float*>(a.dy) + int64_t(p.out_off) * a.cout +
                     (in_y ? d.b0 + c * 4 : 0);
-  DwRows<1, BK> rows(d, p.deg, k);
+  DwRows<1, BK, 4> rows(d, p.deg, k);
   f32x4 xv[4], yv[4];
   const auto fetch = [&]() {
 #pragma unroll
@@ -958,14 +959,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // The same in bf16: rows of x and dy go straight to LDS as they lie in memory
-// and are read across them; one chunk of 64 rows is multiplied while the next is
-// on its way.  Rows past the end are zeros.
+// and are read across them; one chunk of 32 rows is multiplied while the next is
+// on its way, three workgroups on a compute unit (16,411 rows in 16 groups, 1024
+// x 2048 channels with dx: 245 us, 252 with chunks of 64 and two workgroups).
+// Rows past the end are zeros.
 // (Turned in registers on their way to LDS instead: 13,742 rows in 6 groups,
 // 1264 x 312 channels, 92 us, 65 so.)
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     k_mix_dw_across(const MixDwArgs a, const MixDwList l, int64_t part_rows) {
-  __shared__ __attribute__((aligned(128))) uint8_t s_x0[TileLoad::kBytes], s_y0[TileLoad::kBytes];
-  __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_y1[TileLoad::kBytes];
+  constexpr int BK = 32, BYTES = BK * kTile * 2;
+  __shared__ __attribute__((aligned(128))) uint8_t s_x0[BYTES], s_y0[BYTES];
+  __shared__ __attribute__((aligned(128))) uint8_t s_x1[BYTES], s_y1[BYTES];
   DwTile d;
   if (!d.find(a, l, part_rows)) return;
   const MixPair p = l.p[d.pair];
@@ -983,41 +987,38 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint8_t* x0 = static_cast<const uint8_t*>(a.x) + (int64_t(p.in_off) * a.cin + ca) * 2;
   const uint8_t* y0 = static_cast<const uint8_t*>(a.dy) + (int64_t(p.out_off) * a.cout + cb) * 2;
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kTileZeros);
-  DwRows<16, 64> rows(d, p.deg, across.row);
+  DwRows<16, BK, 2> rows(d, p.deg, across.row);
   int64_t left = d.n - across.row;
   const auto fetch = [&](uint8_t* x, uint8_t* y) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const bool in = j * 16 < left;
       const int64_t xo = (int64_t(rows.row[j]) * a.din + rows.m[j]) * a.cin * 2;
       const int64_t yo = (int64_t(rows.row[j]) * a.dout + rows.m[j]) * a.cout * 2;
       load.ask(in && in_x ? x0 + xo : zeros, x, j);
       load.ask(in && in_y ? y0 + yo : zeros, y, j);
     }
-    left -= 64;
+    left -= BK;
     rows.next();
     rows.find();
   };
-  const int64_t steps = (d.n + 63) / 64;
+  const int64_t steps = (d.n + BK - 1) / BK;
   const auto turn = [&](const uint8_t* x, const uint8_t* y, uint8_t* x_free, uint8_t* y_free,
                         int64_t step) {
     tile_wait();
     fetch(x_free, y_free);
     if (step >= steps) return;
     __builtin_amdgcn_sched_barrier(0);
+    bf16x8 yf[4][1];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 yf[4][1];
+    for (int j = 0; j < 4; ++j)
+      yf[j][0] = across.read(y, 0, wn * 8 + j * 2 + ((lane & 3) >> 1), lane & 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        yf[j][0] = across.read(y, kk, wn * 8 + j * 2 + ((lane & 3) >> 1), lane & 1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8 xf[1][1] = {
-            {across.read(x, kk, wm * 8 + i * 2 + ((lane & 3) >> 1), lane & 1)}};
-        // rows of the products: output channels
-        products<1, 4, 1>(yf, xf, reinterpret_cast<f32x4(&)[4][1]>(acc[i]));
-      }
+    for (int i = 0; i < 4; ++i) {
+      const bf16x8 xf[1][1] = {
+          {across.read(x, 0, wm * 8 + i * 2 + ((lane & 3) >> 1), lane & 1)}};
+      // rows of the products: output channels
+      products<1, 4, 1>(yf, xf, reinterpret_cast<f32x4(&)[4][1]>(acc[i]));
     }
   };
   if (steps > 0) {
