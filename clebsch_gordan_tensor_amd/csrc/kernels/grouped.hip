@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
 // on its way; two workgroups on a compute unit.  W lies along k when it is
 // transposed, and along its columns when not: then it is read across.
 // 16,384 rows in 16 groups, 1024 to 2048 channels: 98 us (700 TFLOP/s), its dx
-// 96-110; 40% of the cycles are products, no LDS read meets another's bank, and the
+// 95-110; 40-44% of the cycles are products, no LDS read meets another's bank, and the
 // rest are waits for chunks: 1.1 GB pass from the caches to LDS.
 template <bool WT>
 __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, const MixList l) {
@@ -1031,8 +1031,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load writes to LDS after the end
   // dW past the caches, which x and dy need (16,384 rows in 16 groups, 1024 x
-  // 2048, with dx: 199 us, 226 without, where they are in the caches from a call
-  // before, 253 and 257 where not; in float32, whose products take longer, it
+  // 2048, in chunks of 64 rows, with dx: 199 us, 226 without, where they are in the
+  // caches from a call before, 253 and 257 where not; in float32, whose products take longer, it
   // made no difference); parts are read again soon
   float* out = d.out(a, l, part_rows);
   const bool part = d.tile.rows > part_rows;
