@@ -860,7 +860,8 @@ struct DwRows {
 };
 
 // float32: rows pass through registers, where they are split and turned, to
-// LDS (64,000 x 16 rows of 128 channels: 275 us, 41% of the cycles products).  Channel 4 c + e of a tile lies in LDS row 32 e + c, so that neighbouring
+// LDS (64,000 x 16 rows of 128 channels: 275 us, 41% of the cycles products).
+// Channel 4 c + e of a tile lies in LDS row 32 e + c, so that neighbouring
 // threads write neighbouring rows.
 __global__ void __launch_bounds__(kThreads, 2)
     k_mix_dw(const MixDwArgs a, const MixDwList l, int64_t part_rows) {
@@ -892,8 +893,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const auto fetch = [&]() {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      xv[j] = *reinterpret_cast<const f32x4*>(x0 + (int64_t(rows.row[j]) * a.din + rows.m[j]) * a.cin);
-      yv[j] = *reinterpret_cast<const f32x4*>(y0 + (int64_t(rows.row[j]) * a.dout + rows.m[j]) * a.cout);
+      const int64_t r = rows.row[j];
+      xv[j] = *reinterpret_cast<const f32x4*>(x0 + (r * a.din + rows.m[j]) * a.cin);
+      yv[j] = *reinterpret_cast<const f32x4*>(y0 + (r * a.dout + rows.m[j]) * a.cout);
     }
     rows.next();
   };
@@ -1031,9 +1033,9 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load writes to LDS after the end
   // dW past the caches, which x and dy need (16,384 rows in 16 groups, 1024 x
-  // 2048, in chunks of 64 rows, with dx: 199 us, 226 without, where they are in the
-  // caches from a call before, 253 and 257 where not; in float32, whose products take longer, it
-  // made no difference); parts are read again soon
+  // 2048, in chunks of 64 rows, with dx: 199 us, 226 without, where they are in
+  // the caches from a call before, 253 and 257 where not; in float32, whose
+  // products take longer, it made no difference); parts are read again soon
   float* out = d.out(a, l, part_rows);
   const bool part = d.tile.rows > part_rows;
   const RowHalves halves;

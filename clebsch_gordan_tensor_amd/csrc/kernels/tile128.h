@@ -42,9 +42,9 @@ __device__ __forceinline__ const uint8_t* tile_at(const uint8_t* lds, int r, int
   return lds + r * 128 + ((piece ^ (r & 7)) << 4);
 }
 
-// Tiles of 64 k of 128 bf16 channels that lie along the channels in memory: 16
-// pieces a k, which a transposing read turns to the order of the products.  A
-// lane's pieces are of rows row, row + 16, row + 32 and row + 48; FLIP: the bit
+// Tiles of 32 or 64 k of 128 bf16 channels that lie along the channels in
+// memory: 16 pieces a k, which a transposing read turns to the order of the
+// products.  A lane's pieces are of rows row, row + 16 and so on; FLIP: the bit
 // of the piece at which the rows of 16 lanes part, 4 for reads of 4 channels
 // out of every 8, 2 for 16 channels in a row (then 32 lanes meet no bank twice).
 template <int FLIP>
