@@ -267,23 +267,59 @@ struct Block {
         runs(fp8_runs(a.C)) {}
 };
 
-// The sum with the residual, rounded to the storage type as it is kept: the
+// Where h may be x or the residual, and dx the cotangent of h: whether a team's
+// wavefronts have to wait for each other between the last loads and the first
+// stores.  A row's last vector, where it is moved back, may be the first of its
+// wavefront; it then reads (and repeats) channels that the wavefront before
+// stores.  Lanes of one wavefront all load before any of them stores, and
+// without a mask no vector is moved back.
+template <int MODE, int TEAM, bool MASK>
+constexpr bool kWaitToStore = (MODE & kNormResidual) != 0 && TEAM > 64 && MASK;
+
+// Waits until every wavefront has what these values were loaded for: the barrier
+// alone would let loads pass that are still under way.
+template <int V, int K, int NC, int U>
+__device__ __forceinline__ void wait_to_store(const float (&x)[U][NC][K][V]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) asm volatile("" ::"v"(x[u][c][i][v]) : "memory");
+  __syncthreads();
+}
+
+// The sums with the residual, rounded to the storage type as they are kept: the
 // backward finds the same values.
-template <bool STREAM, bool MASK, class T, int V, int K, int NC>
-__device__ __forceinline__ void add_residual(const Block<T, V, K>& b, int64_t row, bool valid,
-                                             const Lane<V, K>& ln, float (&x)[NC][K][V]) {
-  float r[NC][K][V];
-  load_segment<T, STREAM>(b.add + row * b.ld, b.C, ln, r);
+template <bool WAIT, bool STREAM, bool MASK, class T, int V, int K, int NC, int U>
+__device__ __forceinline__ void add_residual(const Block<T, V, K>& b, const Rows<U>& rows,
+                                             const Lane<V, K>& ln, float (&x)[U][NC][K][V]) {
+  const auto keep = [&](int u) {
+    if (!MASK || rows.valid[u])
+      store_segment<T, STREAM, MASK>(b.h + rows.at[u] * b.ld, b.C, ln, x[u]);
+  };
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int u = 0; u < U; ++u) {
+    float r[NC][K][V];
+    load_segment<T, STREAM>(b.add + rows.at[u] * b.ld, b.C, ln, r);
 #pragma unroll
-    for (int i = 0; i < K; ++i)
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        x[c][i][v] += r[c][i][v];
-        if constexpr (!std::is_same_v<T, float>) x[c][i][v] = float(__bf16(x[c][i][v]));
-      }
-  if (valid) store_segment<T, STREAM, MASK>(b.h + row * b.ld, b.C, ln, x);
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          x[u][c][i][v] += r[c][i][v];
+          if constexpr (!std::is_same_v<T, float>) x[u][c][i][v] = float(__bf16(x[u][c][i][v]));
+        }
+    if constexpr (!WAIT) keep(u);
+  }
+  if constexpr (WAIT) {
+    wait_to_store(x);
+#pragma unroll
+    for (int u = 0; u < U; ++u) keep(u);
+  }
 }
 
 // Results of V channels each in 8 bits, with the scale of every run of 128
@@ -327,9 +363,7 @@ __device__ __forceinline__ void fwd_step(const Block<T, V, K>& b, const Rows<U>&
 #pragma unroll
   for (int u = 0; u < U; ++u) load_segment<T, STREAM>(b.x + r.at[u] * b.ld, b.C, ln, xs[u]);
   if constexpr ((MODE & kNormResidual) != 0)
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      add_residual<STREAM, MASK>(b, r.at[u], !MASK || r.valid[u], ln, xs[u]);
+    add_residual<kWaitToStore<MODE, TEAM, MASK>, STREAM, MASK>(b, r, ln, xs);
   if constexpr (NC == 1)
     if (b.centered) center<TEAM, MASK>(xs, inv, ln, b.group, lds, phase);
 #pragma unroll
@@ -402,6 +436,11 @@ __device__ __forceinline__ void bwd_step(const Block<T, V, K>& b, const Rows<U>&
         }
   }
   team_sum<TEAM>(s, b.group, lds, phase);
+  constexpr bool kWait = kWaitToStore<MODE, TEAM, MASK>;
+  const auto put_dx = [&](int u) {
+    if (!MASK || r.valid[u])
+      store_segment<T, STREAM, MASK>(b.y + r.at[u] * b.ld, b.C, ln, xs[u]);
+  };
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const float* q = s + u * S;
@@ -432,8 +471,12 @@ __device__ __forceinline__ void bwd_step(const Block<T, V, K>& b, const Rows<U>&
 #pragma unroll
           for (int v = 0; v < V; ++v) xs[u][c][i][v] += d[u][c][i][v];
     }
-    if (!MASK || r.valid[u])
-      store_segment<T, STREAM, MASK>(b.y + r.at[u] * b.ld, b.C, ln, xs[u]);
+    if constexpr (!kWait) put_dx(u);
+  }
+  if constexpr (kWait) {
+    wait_to_store(xs);
+#pragma unroll
+    for (int u = 0; u < U; ++u) put_dx(u);
   }
 }
 

@@ -170,6 +170,37 @@ def test_residual_in_place(gpu):
             assert torch.equal(got, ref), (C, k)
 
 
+# widths whose last vector is moved back over the channels of another wavefront's (257 to 259 of
+# every 256 in lists with a degree above 0; of scalars 1025 and up), and their neighbours
+@pytest.mark.parametrize("irreps,C,dtype", [
+    ("0e+1o", 257, "f32"), ("0e+1o+2e", 258, "bf16"), ("1o", 259, "f32"), ("0e+1o", 260, "f32"),
+    ("4e+0e", 257, "f32"), ("0e+1o", 514, "f32"), ("0e+5o", 513, "bf16"), ("1o+0e", 771, "f32"),
+    ("0e+1o", 1025, "f32"), ("1o", 2049, "bf16"), ("0e", 1025, "f32"), ("0e", 1027, "f32"),
+    ("0e", 1281, "f32"), ("0e", 2049, "f32"), ("0e", 1025, "bf16"), ("0e", 1031, "bf16"),
+    ("0o", 1537, "bf16"), ("0e", 1300, "f32")])
+def test_residual_in_place_wide(gpu, irreps, C, dtype):
+    ir, rows = _ir(irreps), 2003
+    x, r, dy, dh, w, b, _ = _norm_case(ir, rows, C, dtype)
+    X, Rd, D, H = (dev(t, dtype) for t in (x, r, dy, dh))
+    W, B = dev(w), dev(b)
+    y, h = gpu.layer_norm_residual(ir, X, Rd, W, B)
+    assert torch.equal(h, (X.float() + Rd.float()).to(X.dtype))
+    assert torch.equal(y, gpu.layer_norm(ir, h, W, B))
+    ref = gpu.layer_norm_residual_backward(ir, h, W, D, H)
+    for _ in range(3):
+        for hx, yx in ((0, 1), (1, 0), (0, None), (1, None), (None, 1), (None, 0)):
+            t = [X.clone(), Rd.clone()]
+            gy, gh = gpu.layer_norm_residual(ir, t[0], t[1], W, B,
+                                             h=None if hx is None else t[hx],
+                                             out=None if yx is None else t[yx])
+            assert torch.equal(gh, h) and torch.equal(gy, y), (hx, yx)
+        for k in range(3):
+            t = [h.clone(), D.clone(), H.clone()]
+            got = gpu.layer_norm_residual_backward(ir, t[0], W, t[1], t[2], dx=t[k])
+            for a, c in zip(got, ref):
+                assert torch.equal(a, c), k
+
+
 def test_residual_without_weights_and_rows(gpu):
     ir = _ir("0e+1o")
     x, r, dy, dh, w, b, h = _norm_case(ir, 40, 64, "f32")
