@@ -68,9 +68,13 @@ struct AcrossLoad {
   }
 };
 
-// Waits for this wavefront's loads, then for the other wavefronts.
+// Waits for this wavefront's loads and for its reads of LDS, then for the other
+// wavefronts: what it asked for is there, and nobody still reads the stage that
+// is asked for next.  (The products of a turn may come after the barrier, and
+// without the wait for LDS so may the last of their operands.)
 __device__ __forceinline__ void tile_wait() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
