@@ -381,15 +381,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_stream(const Fp8MixArgs a, 
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int col0 = int(blockIdx.y) * 128, deg = blk.deg;
   const int n = int(min(int64_t(chunk), tile.rows - tile.at));
-  const int last = int((tile.at + n - 1) / deg);
+  // (places count on past the last one, and that may be 2^31 - 2: unsigned)
+  const unsigned last = unsigned((tile.at + n - 1) / deg), step_at = unsigned(kStreamRows / deg);
   const TileRows rows(tile.at, deg);
-  const int step_at = kStreamRows / deg, step_m = kStreamRows % deg;
-  int m, at = rows.place(wave * 16 + q, m);  // of the next row to look up
+  const int step_m = kStreamRows % deg;
+  int m;
+  unsigned at = unsigned(rows.place(wave * 16 + q, m));  // of the next row to look up
   struct Row {
     int row, m;
   };
   const auto look = [&]() {
-    const Row r{order(min(at, last)), m};
+    const Row r{order(int(min(at, last))), m};
     at += step_at;
     m += step_m;
     if (m >= deg) {

@@ -126,7 +126,7 @@ struct TileRows {
   __device__ __forceinline__ int place(int r, int& m) const {
     const unsigned c = m0 + unsigned(r), d = c / deg;
     m = int(c - d * deg);
-    return from + int(d);
+    return int(unsigned(from) + d);
   }
 };
 

@@ -386,15 +386,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_stream(const MixArgs a, con
 
   // where the rows are: thread r of the first wavefront keeps to row r of the
   // tiles, and has the next one's place in `place`
-  const int last = int((tile.at + n - 1) / deg), step_at = kStreamRows / deg,
-            step_m = kStreamRows % deg;
+  // (places count on past the last one, and that may be 2^31 - 2: unsigned)
+  const unsigned last = unsigned((tile.at + n - 1) / deg), step_at = unsigned(kStreamRows / deg);
+  const int step_m = kStreamRows % deg;
   const int64_t from = tile.at / deg;
   const unsigned u = unsigned(tile.at - from * deg) + unsigned(lane);
-  int at = int(from) + int(u / unsigned(deg)), m = int(u % unsigned(deg));
+  unsigned at = unsigned(from) + u / unsigned(deg);
+  int m = int(u % unsigned(deg));
   const int* source = order ? order : static_cast<const int*>(a.x);  // (read in any case)
   const auto look = [&]() {
-    const int t = min(at, last), row = source[order ? t : 0];
-    return order ? row : t;
+    const unsigned t = min(at, last);
+    const int row = source[order ? t : 0u];
+    return order ? row : int(t);
   };
   const auto put = [&](int buf, int place) {
     if (wave == 0) s_row[buf][lane] = {place, m};
@@ -823,27 +826,30 @@ struct DwTile {
 
 // NR rows that a lane loads, k, k + STRIDE and so on of a chunk of BK, in memory
 // (row, component).  A chunk's rows are asked for a chunk ahead of their channels;
-// past the end they are the last row again.
+// past the end they are the last row again (places count on, and the last one
+// may be 2^31 - 2: unsigned).
 template <int STRIDE, int BK, int NR>
 struct DwRows {
-  int at[NR], m[NR], row[NR], deg, last, step_at, step_m;
+  unsigned at[NR], last, step_at;
+  int m[NR], row[NR], deg, step_m;
   const int* order;
   __device__ __forceinline__ DwRows(const DwTile& d, int deg_, int k)
-      : deg(deg_), last(d.last), step_at(BK / deg_), step_m(BK % deg_), order(d.order) {
+      : last(unsigned(d.last)), step_at(unsigned(BK / deg_)), deg(deg_), step_m(BK % deg_),
+        order(d.order) {
     const int64_t from = d.tile.at / deg;
     const unsigned m0 = unsigned(d.tile.at - from * deg);
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
       const unsigned u = m0 + unsigned(k + j * STRIDE), e = u / unsigned(deg);
-      at[j] = int(from) + int(e);
+      at[j] = unsigned(from) + e;
       m[j] = int(u - e * unsigned(deg));
     }
   }
   __device__ __forceinline__ void find() {
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
-      const int t = min(at[j], last);
-      row[j] = order ? order[t] : t;
+      const unsigned t = min(at[j], last);
+      row[j] = order ? order[t] : int(t);
     }
   }
   __device__ __forceinline__ void next() {

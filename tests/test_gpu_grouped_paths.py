@@ -217,3 +217,59 @@ def test_layers_on_two_streams(gpu):
         for one, two in zip(alone, both):
             for p, q in zip(one, two):
                 assert torch.equal(p, q)
+
+
+def _ends(rows, k, width, dtype, seed):
+    """Zeros but for k random rows at the end, [rows][1][width], and these."""
+    rng = np.random.default_rng(seed)
+    end = S.round_bf16(rng.standard_normal((k, 1, width)).astype(np.float32))
+    t = torch.zeros((rows, 1, width), device="cuda", dtype=dtype)
+    t[rows - k:] = dev(end).to(dtype)
+    return t, end
+
+
+# as many rows as an index may have: places past the last row are past 2^31 as well
+@pytest.mark.parametrize("with_index", [False, True])
+def test_most_rows(gpu, with_index):
+    rows, k, into = 2 ** 31 - 1, 700, _ir("0e")
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 180e9:
+        pytest.skip("needs 180 GB")
+    groups, g = (2, 1) if with_index else (1, 0)
+    index = None
+    if with_index:
+        index = gpu.group_rows(torch.ones(rows, device="cuda", dtype=torch.int32), groups)
+        assert index.offsets.tolist() == [0, 0, rows]
+        assert torch.equal(index.order[-k:].long(), torch.arange(rows - k, rows, device="cuda"))
+    x, xe = _ends(rows, k, 8, torch.bfloat16, 1)
+    dy, de = _ends(rows, k, 8, torch.bfloat16, 2)
+    W = S.round_bf16(np.random.default_rng(3).standard_normal((groups, 1, 8, 8)).astype(np.float32))
+    Wd, of = dev(W, "bf16"), np.full(k, g)
+    y = gpu.linear_grouped(into, into, index, x, Wd)
+    R.check(host(y[-k:]), R.mix(into, into, of, xe, W), "y", True)
+    assert not y[:100_000_000].any() and not y[-100_000_000:-k].any()
+    del y
+    dx, dW = gpu.linear_grouped_backward(into, into, index, x, Wd, dy)
+    rx, rW = R.mix_backward(into, into, of, xe, W, de)
+    R.check(host(dx[-k:]), rx, "dx", True)
+    R.check(host(dW), rW, "dW")
+    del x, dx, dy, index
+    torch.cuda.empty_cache()
+
+
+def test_most_rows_in_8_bits(gpu):
+    rows, k, into = 2 ** 31 - 1, 700, _ir("0e")
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 180e9:
+        pytest.skip("needs 180 GB")
+    q, xe = _ends(rows, k, 16, torch.float8_e4m3fn, 4)
+    scale = torch.ones((rows, 1, 1), device="cuda")
+    W = np.random.default_rng(5).standard_normal((1, 1, 16, 16)).astype(np.float32)
+    y = gpu.linear_fp8(into, into, q, scale, gpu.linear_fp8_pack(into, into, dev(W)))
+    xv = host(q[-k:].float()).astype(np.float64)
+    assert np.array_equal(xv, R.e4m3(xe))
+    ref = R.mix(into, into, np.zeros(k, int), xv, R.weight_values(*R.quantize_weights(W)))
+    R.check(host(y[-k:]), ref, "y", True, adds=1, drops=R.EIGHTS)
+    assert not y[:100_000_000].any() and not y[-100_000_000:-k].any()
+    del q, scale, y
+    torch.cuda.empty_cache()
