@@ -197,13 +197,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_mix(const Fp8MixArgs a, con
   __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_w1[TileLoad::kBytes];
   __shared__ float s_scale[kTileRows][kScaleSteps + 1];
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups) && weights_match(a);
+  const unsigned wg = a.wg0 + blockIdx.x;
   int bi = 0;
-  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(wg)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   int col_tile;
   if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg,
-                     kTileRows, blockIdx.x - unsigned(blk.wg0),
+                     kTileRows, wg - unsigned(blk.wg0),
                      unsigned((a.cout + 127) / 128), tile, col_tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.q);
@@ -622,8 +623,11 @@ hipError_t launch_fp8_mix_t(const Fp8MixArgs& a, MixList l, hipStream_t s) {
     if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
   }
   const Fp8Layout at = fp8_layout(a.n_groups, a.pairs, a.cin, a.cout);
-  hipLaunchKernelGGL((k_fp8_mix<T>), dim3(unsigned(wgs)), dim3(kThreads), 0, s, a, l, at);
-  return hipGetLastError();
+  return launch_tiles(wgs, kThreads, [&](unsigned n, unsigned first) {
+    Fp8MixArgs part = a;
+    part.wg0 = first;
+    hipLaunchKernelGGL((k_fp8_mix<T>), dim3(n), dim3(kThreads), 0, s, part, l, at);
+  });
 }
 
 }  // namespace

@@ -158,4 +158,19 @@ inline int64_t most_tiles(int64_t n_rows, int n_groups, int deg, int64_t size, b
   return (n_rows * deg + size - 1) / size + (grouped ? n_groups : 0);
 }
 
+// Launches `wgs` workgroups of `threads` as go(workgroups, the first one's number).
+// A launch holds fewer than 2^32 threads; more workgroups than that (a single
+// column tile of 2^31 rows and components has as many) go in several, each from
+// a multiple of the XCDs on.
+template <class F>
+hipError_t launch_tiles(int64_t wgs, int threads, F&& go) {
+  const int64_t most = (int64_t(1) << 31) / threads;
+  for (int64_t at = 0; at < wgs; at += most) {
+    go(unsigned(wgs - at < most ? wgs - at : most), unsigned(at));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace e3k

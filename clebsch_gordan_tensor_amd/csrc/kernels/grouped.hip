@@ -90,13 +90,14 @@ __global__ void __launch_bounds__(kThreads) k_mix(const MixArgs a, const MixList
   constexpr int CT = kTile / 4;           // threads of a row of W
   __shared__ __attribute__((aligned(16))) __bf16 s_x[3][kTile * BK], s_w[3][kTile * BK];
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
+  const unsigned wg = a.wg0 + blockIdx.x;
   int bi = 0;
-  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(wg)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   int col_tile;
   if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
-                     blockIdx.x - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
+                     wg - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
                      col_tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.x);
@@ -229,13 +230,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_mix_along(const MixArgs a, cons
   __shared__ __attribute__((aligned(128))) uint8_t s_x0[TileLoad::kBytes], s_w0[TileLoad::kBytes];
   __shared__ __attribute__((aligned(128))) uint8_t s_x1[TileLoad::kBytes], s_w1[TileLoad::kBytes];
   const bool valid = index_matches(a.index, a.n_rows, a.n_groups);
+  const unsigned wg = a.wg0 + blockIdx.x;
   int bi = 0;
-  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(blockIdx.x)) ++bi;
+  while (bi + 1 < l.n_blocks && l.blk[bi + 1].wg0 <= int(wg)) ++bi;
   const MixBlock blk = l.blk[bi];
   GroupTile tile;
   int col_tile;
   if (!find_tile_xcd(a.index ? a.index + a.offsets : nullptr, a.n_groups, a.n_rows, blk.deg, kTile,
-                     blockIdx.x - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
+                     wg - unsigned(blk.wg0), unsigned((a.cout + kTile - 1) / kTile), tile,
                      col_tile) || !valid)
     return;
   const RowOrder order(a.index, a.order, tile, a.x);
@@ -724,15 +726,18 @@ hipError_t launch_mix_t(const MixArgs& a, MixList l, hipStream_t s) {
                                      a.index != nullptr), (a.cout + kTile - 1) / kTile);
     if (wgs > (int64_t(1) << 30)) return hipErrorInvalidValue;
   }
-  const dim3 grid{unsigned(wgs)};
-  if constexpr (sizeof(T) == 2) {
-    if (a.w_trans) hipLaunchKernelGGL((k_mix_along<true>), grid, dim3(kThreads), 0, s, a, l);
-    else hipLaunchKernelGGL((k_mix_along<false>), grid, dim3(kThreads), 0, s, a, l);
-  } else {
-    if (a.w_trans) hipLaunchKernelGGL((k_mix<true>), grid, dim3(kThreads), 0, s, a, l);
-    else hipLaunchKernelGGL((k_mix<false>), grid, dim3(kThreads), 0, s, a, l);
-  }
-  return hipGetLastError();
+  return launch_tiles(wgs, kThreads, [&](unsigned n, unsigned first) {
+    MixArgs part = a;
+    part.wg0 = first;
+    const dim3 grid{n};
+    if constexpr (sizeof(T) == 2) {
+      if (a.w_trans) hipLaunchKernelGGL((k_mix_along<true>), grid, dim3(kThreads), 0, s, part, l);
+      else hipLaunchKernelGGL((k_mix_along<false>), grid, dim3(kThreads), 0, s, part, l);
+    } else {
+      if (a.w_trans) hipLaunchKernelGGL((k_mix<true>), grid, dim3(kThreads), 0, s, part, l);
+      else hipLaunchKernelGGL((k_mix<false>), grid, dim3(kThreads), 0, s, part, l);
+    }
+  });
 }
 
 // ------------------------------------------------------- weight gradients

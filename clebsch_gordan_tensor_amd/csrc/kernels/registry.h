@@ -500,6 +500,7 @@ struct MixArgs {
   const void* x;
   const void* W;     // [groups][pairs][cin][cout], storage type
   void* y;
+  unsigned wg0;      // first workgroup of this launch (launch_tiles)
 };
 hipError_t launch_mix(const MixArgs& a, const MixList& l, int bf16, hipStream_t s);
 
@@ -544,6 +545,7 @@ struct Fp8MixArgs {
   const float* scale;  // [rows][din][runs of 128 channels]
   const void* packed;
   void* y;
+  unsigned wg0;        // first workgroup of this launch (launch_tiles)
 };
 hipError_t launch_fp8_mix(const Fp8MixArgs& a, const MixList& l, int bf16, hipStream_t s);
 

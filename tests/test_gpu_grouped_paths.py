@@ -219,11 +219,11 @@ def test_layers_on_two_streams(gpu):
                 assert torch.equal(p, q)
 
 
-def _ends(rows, k, width, dtype, seed):
-    """Zeros but for k random rows at the end, [rows][1][width], and these."""
+def _ends(rows, k, width, dtype, seed, comps=1):
+    """Zeros but for k random rows at the end, [rows][comps][width], and these."""
     rng = np.random.default_rng(seed)
-    end = S.round_bf16(rng.standard_normal((k, 1, width)).astype(np.float32))
-    t = torch.zeros((rows, 1, width), device="cuda", dtype=dtype)
+    end = S.round_bf16(rng.standard_normal((k, comps, width)).astype(np.float32))
+    t = torch.zeros((rows, comps, width), device="cuda", dtype=dtype)
     t[rows - k:] = dev(end).to(dtype)
     return t, end
 
@@ -272,4 +272,41 @@ def test_most_rows_in_8_bits(gpu):
     R.check(host(y[-k:]), ref, "y", True, adds=1, drops=R.EIGHTS)
     assert not y[:100_000_000].any() and not y[-100_000_000:-k].any()
     del q, scale, y
+    torch.cuda.empty_cache()
+
+
+# more tiles than one launch holds threads for: 2^24 workgroups and more
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_more_tiles_than_a_launch(gpu, dtype):
+    rows, k, ir = 2 ** 30 + 70_000, 700, _ir("0e+0e")
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 180e9:
+        pytest.skip("needs 180 GB")
+    C, of = 16 if dtype == "fp8" else 8, np.zeros(k, int)
+    T = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn}[dtype]
+    x, xe = _ends(rows, k, C, T, 1, 2)
+    W = S.round_bf16(np.random.default_rng(3).standard_normal((1, 4, C, C)).astype(np.float32))
+    y = torch.full((rows, 2, C), 3.0, device="cuda",
+                   dtype=torch.float32 if dtype == "f32" else torch.bfloat16)
+    if dtype == "fp8":
+        scale = torch.ones((rows, 2, 1), device="cuda")
+        gpu.linear_fp8(ir, ir, x, scale, gpu.linear_fp8_pack(ir, ir, dev(W)), out=y)
+        ref = R.mix(ir, ir, of, R.e4m3(xe), R.weight_values(*R.quantize_weights(W)))
+        R.check(host(y[-k:]), ref, "y", True, adds=1, drops=R.EIGHTS)
+        del scale
+    else:
+        Wd, bf16 = dev(W, dtype), dtype == "bf16"
+        gpu.linear_grouped(ir, ir, None, x, Wd, out=y)
+        R.check(host(y[-k:]), R.mix(ir, ir, of, xe, W), "y", bf16)
+    assert not y[:-k].any()
+    if dtype == "bf16":
+        del y
+        dx = torch.full_like(x, 3.0)
+        _, dW = gpu.linear_grouped_backward(ir, ir, None, x, Wd, x, dx=dx)
+        rx, rW = R.mix_backward(ir, ir, of, xe, W, xe)
+        R.check(host(dx[-k:]), rx, "dx", True)
+        R.check(host(dW), rW, "dW")
+        assert not dx[:-k].any()
+        del dx
+    del x
     torch.cuda.empty_cache()
