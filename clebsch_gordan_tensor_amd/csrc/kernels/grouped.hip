@@ -10,9 +10,10 @@
 // All products run on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16, fp32
 // accumulation).  A float32 operand is split into three bf16 parts, a = a1 +
 // a2 + a3 with each part the rest rounded to nearest: 24 bits and the range of
-// float32.  Of the nine products of two split operands the six largest are
-// kept; what is left out is below 2^-26 of a product.  Six bf16 products cost
-// 6/16 of a float32 one's matrix-core time.
+// float32, down to 2^-110 (bf16's least value is 2^-133: of a smaller operand
+// what lies below 2^-134 is lost).  Of the nine products of two split operands
+// the six largest are kept; what is left out is below 2^-26 of a product.  Six
+// bf16 products cost 6/16 of a float32 one's matrix-core time.
 //
 // Layout of the operands (A[i][k]: lane i + 16 (k / 8) holds 8 consecutive k;
 // B[k][j] likewise; D[i][j]: register r of lane j + 16 h is i = 4 h + r): W is

@@ -712,7 +712,8 @@ e3_status e3_group_index(int64_t n_rows, int32_t n_groups, const int32_t* group,
  * get 0.  Cin and Cout multiples of 8 up to 8192, degrees up to 8, at most 32
  * blocks on a side and 256 pairs; x, W, y 16-byte aligned, y overlapping
  * nothing.  float32 products keep 24 bits of both factors (three bf16 parts
- * each on the bf16 matrix cores); a component row of x that holds a value
+ * each on the bf16 matrix cores) of 2^-110 and more in size; of a smaller factor
+ * what lies below 2^-134 is lost.  A component row of x that holds a value
  * that is not finite in bf16 (past 3.39e38) gives NaN throughout its row of
  * y, and such a weight in its column.  Sums are float32, in an order that does not
  * depend on the other rows. */

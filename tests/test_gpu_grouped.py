@@ -149,6 +149,55 @@ def test_values_far_apart(gpu):
     R.check(host(y), R.mix(into, out, group, x, W), "far apart")
 
 
+def _near(got, ref, extra, what):
+    """R.check's bound for every element, and `extra` besides."""
+    y, size, terms = ref
+    tol = (R.ADDS * terms + 16) * R.U * size + R.U * np.abs(y) + extra
+    bad = np.abs(got.astype(np.float64) - y) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outside"
+
+
+# factors down to float32's least: 24 bits to 2^-110, what is below 2^-134 of a smaller one is lost
+# (bf16's least value is 2^-133, and a part is the rest rounded to nearest)
+@pytest.mark.parametrize("rows,cin,cout", [(3, 96, 64), (400, 96, 64), (300, 520, 136),
+                                           (6000, 264, 200)])
+def test_values_near_the_least(gpu, rows, cin, cout):
+    into = out = _ir("0e")
+    rng = np.random.default_rng(rows + cin)
+    group = rng.integers(0, 2, rows).astype(np.int32)
+    index = gpu.group_rows(dev(group), 2)
+
+    def factors(low, high):
+        """Rows and weights, every channel's of inverse sizes."""
+        size = 2.0 ** rng.uniform(low, high, cin)
+        sign = lambda *n: rng.choice([-1.0, 1.0], n) * rng.uniform(1, 2, n)  # noqa: E731
+        return ((sign(rows, 1, cin) * size).astype(np.float32),
+                (sign(2, 1, cin, cout) / size[:, None]).astype(np.float32))
+
+    def both(x, W, least):
+        """least: the error of every x (of every W, of neither)."""
+        y = gpu.linear_grouped(into, out, index, dev(x), dev(W))
+        of_x = R.mix(into, out, group, np.ones_like(x), np.abs(W))[1] * (least == "x")
+        of_w = R.mix(into, out, group, np.abs(x), np.ones_like(W))[1] * (least == "W")
+        _near(host(y), R.mix(into, out, group, x, W), 2.0 ** -134 * (of_x + of_w), "y")
+
+    both(*factors(-110, -100), None)
+    both(*factors(-124, -100), "x")
+    x, W = factors(100, 124)
+    both(x, W, "W")
+    # the gradients: dy in the place of x or W
+    x, W = factors(-124, -100)
+    dy = (rng.standard_normal((rows, 1, cout)) * 2.0 ** rng.uniform(-124, -100, (rows, 1, 1))
+          ).astype(np.float32)
+    W = (rng.standard_normal(W.shape) * 2.0 ** 100).astype(np.float32)
+    x = (rng.standard_normal(x.shape) * 2.0 ** 100).astype(np.float32)
+    dx, dW = gpu.linear_grouped_backward(into, out, index, dev(x), dev(W), dev(dy))
+    rx, rW = R.mix_backward(into, out, group, x, W, dy)
+    one = R.mix_backward(into, out, group, np.abs(x), np.abs(W), np.ones_like(dy))
+    _near(host(dx), rx, 2.0 ** -134 * one[0][1], "dx")
+    _near(host(dW), rW, 2.0 ** -134 * one[1][1], "dW")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_values_that_are_not_finite_stay_in_their_rows(gpu, dtype):
     into = out = _ir("0e+1o")
