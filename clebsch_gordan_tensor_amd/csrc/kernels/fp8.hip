@@ -10,7 +10,8 @@
 //     consecutive products that drops what lies below 2^-13 of the largest one
 //     (measured, and so does v_mfma_f32_16x16x32_fp8_fp8); the eights are added
 //     in float32.  On normal values the sums are off by 1.5e-5 (root mean
-//     square, relative), a hundredth of the rounding to bf16 that follows;
+//     square, relative), a hundredth of the rounding to bf16 that follows; of
+//     a small difference of large terms they are off by as much of the terms;
 //   for float32 y from the codes' values in bf16, which are exact, by four
 //     v_mfma_f32_16x16x32_bf16 (2e-8 off on the same values).
 //

@@ -753,7 +753,9 @@ e3_status e3_linear_grouped_backward(const e3_irreps* in, const e3_irreps* out, 
  *     for a single group).  Weights packed for other sizes change nothing.
  * For float32 y the products are exact and the sums float32; for bf16 y the
  * sums of 8 consecutive products drop what lies below 2^-13 of the largest one
- * (the 8-bit matrix cores), far below the rounding of y.
+ * (the 8-bit matrix cores).  On values of one size that is a hundredth of y's
+ * rounding, but it goes with the terms and not with y: of a small difference of
+ * large terms it is more than the rounding, and float32 y keeps it.
  * Cin and Cout multiples of 16 up to 8192; otherwise e3_linear_grouped's
  * limits.  scale x s_W is formed in float32: features and weights whose scales
  * multiply to less than 2^-126 lose digits. */
