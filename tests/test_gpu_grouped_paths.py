@@ -96,6 +96,46 @@ def test_around_few_rows(gpu, rows, dtype):
         _check(gpu, into, out, group, *_case(into, out, group, groups, 200, 264, dtype), dtype)
 
 
+# every row on both sides of the sizes at which tiles of few rows give way to the others: where
+# every block has one source of at most 128 channels at (16 groups + 112) / components rows,
+# elsewhere by the tiles of 16 x 16 of all blocks (1200 in bf16, 6000 in float32, 1600 and 3000 in
+# 8 bits; a row and a column of them for every group besides).  264 columns are 17 tiles.
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8 f32", "fp8 bf16"])
+@pytest.mark.parametrize("xs,os_,groups,cin,cout", [
+    ("0e", "0e", 1, 144, 264), ("0e", "0e", 5, 264, 144), ("0e+0e+1o", "0e+1o", 2, 48, 80),
+    ("0e+1o", "0e+1o", 3, 64, 48)])
+def test_rows_on_both_sides(gpu, xs, os_, groups, cin, cout, dtype):
+    into, out, most = _ir(xs), _ir(os_), 9001
+    fp8 = dtype.startswith("fp8")
+    if fp8:
+        cin, cout = (-(-c // 16) * 16 for c in (cin, cout))
+    group = _skewed(most, groups, 0.3) if groups > 1 else np.zeros(most, np.int32)
+    x, W, dy = _case(into, out, group, groups, cin, cout, dtype)
+    if fp8:
+        packed = gpu.linear_fp8_pack(into, out, dev(W))
+        of = torch.float32 if dtype == "fp8 f32" else None
+        runs = [(dev(x), lambda i, t: gpu.linear_fp8(into, out, *gpu.quantize_fp8(t), packed,
+                                                     index=i, dtype=of))]
+    else:
+        Wd = dev(W, dtype)
+        # (zeros for dW's operand: only dx is looked at)
+        runs = [(dev(x, dtype), lambda i, t: gpu.linear_grouped(into, out, i, t, Wd)),
+                (dev(dy, dtype), lambda i, t: gpu.linear_grouped_backward(
+                    into, out, i, torch.zeros((t.shape[0], S.dim(into), cin), device="cuda",
+                                              dtype=t.dtype), Wd, t)[0])]
+    limit = {"f32": 6000, "bf16": 1200, "fp8 f32": 3000, "fp8 bf16": 1600}[dtype]
+    for k, (t, run) in enumerate(runs):
+        whole = run(gpu.group_rows(dev(group), groups), t)
+        blocks = [2 * l + 1 for l, _ in (into if k else out)]
+        cols = -(-(cin if k else cout) // 16)
+        last = max(n for n in range(1, most) if sum(
+            (n * d + 15) // 16 + groups for d in blocks) * cols <= limit)
+        few = (16 * groups + 112) // max(blocks)
+        for n in {1, 17, few, few + 1, 400, last, last + 1, 6001}:
+            got = run(gpu.group_rows(dev(group[:n]), groups), t[:n].contiguous())
+            assert torch.equal(got, whole[:n]), n
+
+
 @pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("xs,os_,rows,groups,cin,cout", [
     ("0e", "0e", 200, 1, 4096, 144), ("0e", "0e", 300, 3, 2064, 160), ("0e", "0e", 5, 1, 8192, 48),
