@@ -83,7 +83,8 @@ __device__ __forceinline__ bool weights_match(const Fp8MixArgs& a) {
 }
 
 // A block of 128 x 128 weights a workgroup: thread (c, k) takes 4 columns of
-// 16 consecutive k, whose codes it stores side by side.
+// 16 consecutive k, whose codes it stores side by side.  16 x 2048 x 1024: 27 us
+// (6.2 TB/s, in part from the caches).
 __global__ void __launch_bounds__(kThreads)
     k_fp8_pack(int pairs, int groups, int cin, int cout, Fp8Layout l, const float* __restrict__ W,
                uint8_t* __restrict__ packed) {
@@ -186,7 +187,8 @@ constexpr int kScaleSteps = 16;
 
 // Tiles of 128 rows by 128 columns, one chunk of 128 k multiplied while the
 // next is on its way; two workgroups on a compute unit.  16,411 rows of 16
-// experts, 2048 to 1024 channels: 72 us (960 TFLOP/s); 256 columns a
+// experts, 2048 to 1024 channels: 73 us (940 TFLOP/s), to float32 107 (its bf16
+// products and twice the results); 256 columns a
 // workgroup, alone on its compute unit with two chunks on their way, 85 us,
 // three rounds of workgroups where 2.3 would do.
 template <class T>

@@ -139,9 +139,11 @@ inline bool few_rows(int64_t n_rows, int n_groups, const MixList& l) {
   return n_rows * deg <= 16 * int64_t(n_groups) + 112;
 }
 
-// Tiles of 16 rows and columns of all blocks.  Kernels of such tiles fetch W for
-// each, and yet they answer sooner than large tiles as long as the chip isn't
-// full of them.  us by small tiles and by large, 1024 to 1024 channels: float32,
+// Tiles of 16 rows and columns of all blocks, a row of tiles for every group
+// besides, also where there are fewer rows than groups (one row of 4096 columns
+// counts 1,280 at 4 groups and goes to the large tiles in bf16, where 256 would
+// do).  Kernels of such tiles fetch W for each, and yet they answer sooner than
+// large tiles as long as the chip isn't full of them.  us by small tiles and by large, 1024 to 1024 channels: float32,
 // one group, 512 rows 32 and 78, 1024 52 and 79, 2048 93 and 79; 16 groups,
 // 1024 67 and 81, 2048 113 and 82; bf16, one group, 256 rows 11.5 and 14.8, 512
 // 15.8 and 14.7; 16 groups, 128 15.5 and 15.7, 256 18.6 and 15.6; the same of

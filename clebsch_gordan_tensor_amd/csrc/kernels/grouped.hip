@@ -975,8 +975,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // The same in bf16: rows of x and dy go straight to LDS as they lie in memory
 // and are read across them; one chunk of 32 rows is multiplied while the next is
 // on its way, three workgroups on a compute unit (16,411 rows in 16 groups, 1024
-// x 2048 channels with dx: 245 us, 252 with chunks of 64 and two workgroups).
-// Rows past the end are zeros.
+// x 2048 channels with dx: 245 us, chunks of 64 and two workgroups 252, where
+// runs of either lie between 245 and 270).  Rows past the end are zeros.
 // (Turned in registers on their way to LDS instead: 13,742 rows in 6 groups,
 // 1264 x 312 channels, 92 us, 65 so.)
 __global__ void __launch_bounds__(kThreads, 3)
@@ -1046,8 +1046,9 @@ __global__ void __launch_bounds__(kThreads, 3)
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load writes to LDS after the end
   // dW past the caches, which x and dy need (16,384 rows in 16 groups, 1024 x
   // 2048, in chunks of 64 rows, with dx: 199 us, 226 without, where they are in
-  // the caches from a call before, 253 and 257 where not; in float32, whose
-  // products take longer, it made no difference); parts are read again soon
+  // the caches from a call before; 253 and 257 where not, no more than runs
+  // differ; in float32, whose products take longer, no difference either); parts
+  // are read again soon
   float* out = d.out(a, l, part_rows);
   const bool part = d.tile.rows > part_rows;
   const RowHalves halves;

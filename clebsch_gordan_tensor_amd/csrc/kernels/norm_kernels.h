@@ -272,7 +272,10 @@ struct Block {
 // stores.  A row's last vector, where it is moved back, may be the first of its
 // wavefront; it then reads (and repeats) channels that the wavefront before
 // stores.  Lanes of one wavefront all load before any of them stores, and
-// without a mask no vector is moved back.
+// without a mask no vector is moved back.  It costs nothing (us with and without,
+// out of place: 10,007 rows of 600 bf16 channels of 0e+1o, forward 43.5 and 43.1,
+// backward 57.8 and 65.3; 20,011 rows of 1300 float32 scalars 81.7 and 85.5, 88.4
+// and 91.4).
 template <int MODE, int TEAM, bool MASK>
 constexpr bool kWaitToStore = (MODE & kNormResidual) != 0 && TEAM > 64 && MASK;
 

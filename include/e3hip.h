@@ -708,15 +708,16 @@ e3_status e3_group_index(int64_t n_rows, int32_t n_groups, const int32_t* group,
  * W [n_groups][pairs][Cin][Cout], the pairs in e3_linear's order, in the
  * storage type (for bf16 the copies that e3_adamw writes).  index: of
  * e3_group_index for this n_rows and n_groups (with an index of other sizes
- * the call changes nothing); NULL for a single group.  Rows without a group
- * get 0.  Cin and Cout multiples of 8 up to 8192, degrees up to 8, at most 32
- * blocks on a side and 256 pairs; x, W, y 16-byte aligned, y overlapping
- * nothing.  float32 products keep 24 bits of both factors (three bf16 parts
- * each on the bf16 matrix cores) of 2^-110 and more in size; of a smaller factor
- * what lies below 2^-134 is lost.  A component row of x that holds a value
- * that is not finite in bf16 (past 3.39e38) gives NaN throughout its row of
- * y, and such a weight in its column.  Sums are float32, in an order that does not
- * depend on the other rows. */
+ * the call changes nothing); NULL for a single group, whose rows then get what
+ * e3_linear computes, for more widths than it takes (for bf16 from bf16
+ * weights).  Rows without a group get 0.  Cin and Cout multiples of 8 up to 8192,
+ * degrees up to 8, at most 32 blocks on a side and 256 pairs; x, W, y 16-byte
+ * aligned, y overlapping nothing.  float32 products keep 24 bits of both factors
+ * (three bf16 parts each on the bf16 matrix cores) of 2^-110 and more in size; of
+ * a smaller factor what lies below 2^-134 is lost.  A component row of x that
+ * holds a value that is not finite in bf16 (past 3.39e38) gives NaN throughout
+ * its row of y, and such a weight in its column.  Sums are float32, in an order
+ * that does not depend on the other rows. */
 e3_status e3_linear_grouped(const e3_irreps* in, const e3_irreps* out, int64_t n_rows,
                             int32_t n_groups, const void* index, size_t index_bytes, const void* x,
                             const void* W, void* y, e3_dtype dtype, void* stream);
